@@ -22,6 +22,11 @@ __all__ = [
     "gdn2_chunk_bwd_tc", "gdn2_chunk_bwd_tc_workspace_bytes",
     "gdn2_chunk_fwd_edges_workspace_bytes", "gdn2_recurrence", "gdn2_gemm_phase_probe",
     "PHASE_PROBE_FLOPS_PER_CHUNK", "gdn2_layer_edge_maps", "gdn2_rms_norm",
+    "gdn2_gated_norm_fwd", "gdn2_gated_norm_bwd", "gdn2_gated_norm_bwd_workspace_bytes", "gated_norm_fwd",
+    "gated_norm_bwd", "gdn2_gated_norm", "gdn2_add_norm_fwd", "gdn2_add_norm_bwd",
+    "gdn2_add_norm_bwd_workspace_bytes", "add_norm_fwd", "add_norm_bwd", "gdn2_add_norm", "gdn2_tree_fwd",
+    "tree_fwd", "gdn2_recurrent_fwd", "recurrent_fwd", "gdn2_state_copy", "TREE_MAX_NODES",
+    "STATE_COPY_MAX_PAIRS", "DEV_RANGE", "DEV_SLOT", "DEV_PARENT", "DEV_INDEX", "DEV_CONFLICT",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -32,6 +37,11 @@ GDN2_F32, GDN2_BF16 = 0, 1
 STATUS_HEADER_BYTES = 256
 NOALLOC_SCRATCH_BYTES = 32 << 20   # GDN2_NOALLOC_SCRATCH_BYTES in include/gdn2.h
 PHASE_PROBE_FLOPS_PER_CHUNK = 14680064   # GDN2_PHASE_PROBE_FLOPS_PER_CHUNK in include/gdn2.h
+TREE_MAX_NODES = 64              # GDN2_TREE_MAX_NODES in include/gdn2.h
+STATE_COPY_MAX_PAIRS = 1024      # GDN2_STATE_COPY_MAX_PAIRS
+GATES = {"silu": 0, "sigmoid": 1}   # gdn2_gate
+# bits of a workspace's status word for malformed device-side indices (GDN2_DEV_*)
+DEV_RANGE, DEV_SLOT, DEV_PARENT, DEV_INDEX, DEV_CONFLICT = 0x100, 0x200, 0x400, 0x800, 0x1000
 
 
 class GDN2Error(RuntimeError):
@@ -85,6 +95,25 @@ def load_library():
     lib.gdn2_rms_norm.restype = i
     lib.gdn2_gemm_phase_probe.argtypes = [i, i, i, vp, sz, vp]
     lib.gdn2_gemm_phase_probe.restype = i
+    ll, f = ctypes.c_longlong, ctypes.c_float
+    lib.gdn2_gated_norm_bwd_workspace_bytes.argtypes = [ll, i]
+    lib.gdn2_gated_norm_bwd_workspace_bytes.restype = sz
+    lib.gdn2_gated_norm_fwd.argtypes = [vp] * 4 + [ll, i, i, f, i, vp]
+    lib.gdn2_gated_norm_fwd.restype = i
+    lib.gdn2_gated_norm_bwd.argtypes = [vp] * 7 + [ll, i, i, f, i, vp, sz, vp]
+    lib.gdn2_gated_norm_bwd.restype = i
+    lib.gdn2_add_norm_bwd_workspace_bytes.argtypes = [ll, i]
+    lib.gdn2_add_norm_bwd_workspace_bytes.restype = sz
+    lib.gdn2_add_norm_fwd.argtypes = [vp] * 6 + [ll, i, f, i, vp]
+    lib.gdn2_add_norm_fwd.restype = i
+    lib.gdn2_add_norm_bwd.argtypes = [vp] * 10 + [ll, i, f, i, vp, sz, vp]
+    lib.gdn2_add_norm_bwd.restype = i
+    lib.gdn2_tree_fwd.argtypes = [vp] * 7 + [ll, i] + [vp] * 4 + [i] * 7 + [vp, sz, vp]
+    lib.gdn2_tree_fwd.restype = i
+    lib.gdn2_recurrent_fwd.argtypes = [vp] * 7 + [ll, i] + [vp] * 5 + [i] * 7 + [vp, sz, vp]
+    lib.gdn2_recurrent_fwd.restype = i
+    lib.gdn2_state_copy.argtypes = [vp, ll, i, vp, ll, i, vp, vp, i, ll, vp, sz, vp]
+    lib.gdn2_state_copy.restype = i
     lib.gdn2_status_str.argtypes = [i]
     lib.gdn2_status_str.restype = ctypes.c_char_p
     _lib = lib
@@ -374,6 +403,226 @@ def gdn2_rms_norm(o, weight, stream=None) -> None:
         raise GDN2Error(rc, "gdn2_rms_norm")
 
 
+def gdn2_gated_norm_bwd_workspace_bytes(rows, d_v) -> int:
+    return int(load_library().gdn2_gated_norm_bwd_workspace_bytes(int(rows), int(d_v)))
+
+
+def gdn2_add_norm_bwd_workspace_bytes(rows, width) -> int:
+    return int(load_library().gdn2_add_norm_bwd_workspace_bytes(int(rows), int(width)))
+
+
+def _gate_code(act) -> int:
+    if act not in GATES:
+        raise ValueError(f"act must be one of {sorted(GATES)}, got {act!r}")
+    return GATES[act]
+
+
+def _check_f32(named):
+    import torch
+    for name, t in named:
+        if t is not None and t.dtype != torch.float32:
+            raise TypeError(f"{name} must be float32")
+
+
+def _check_i32(named):
+    import torch
+    for name, t in named:
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 1):
+            raise TypeError(f"{name} must be a one-dimensional int32 tensor")
+
+
+def _rows(t) -> int:
+    """Rows of a tensor whose last axis is the channels."""
+    rows = 1
+    for n in t.shape[:-1]:
+        rows *= n
+    return rows
+
+
+def gdn2_gated_norm_fwd(o, gate, weight, y, act="silu", eps=1e-6, stream=None) -> None:
+    """y = RMSNorm(o) * weight * act(gate) over the last axis (include/gdn2.h, gdn2_gated_norm_fwd):
+    o, gate, y of one shape and the token dtype, weight [d_v] fp32, act "silu" or "sigmoid"."""
+    _check_cuda(o, gate, weight, y)
+    dt, code = _dtype_code(o), _gate_code(act)
+    _check_f32((("weight", weight),))
+    _check_dtypes(o, (("gate", gate), ("y", y)))
+    _check_shapes((("gate", gate, o.shape), ("y", y, o.shape), ("weight", weight, o.shape[-1:])))
+    with _on_device(o):
+        rc = load_library().gdn2_gated_norm_fwd(_ptr(o), _ptr(gate), _ptr(weight), _ptr(y), _rows(o), o.shape[-1], code,
+                                                float(eps), dt, _stream(stream))
+    if rc != 0:
+        raise GDN2Error(rc, "gdn2_gated_norm_fwd")
+
+
+def gdn2_gated_norm_bwd(o, gate, weight, dy, do, dgate, dweight, act="silu", eps=1e-6, workspace=None,
+                        stream=None) -> None:
+    """Gradients of gdn2_gated_norm_fwd (include/gdn2.h): do, dgate in the token dtype, dweight fp32."""
+    _check_cuda(o, gate, weight, dy, do, dgate, dweight, workspace)
+    dt, code = _dtype_code(o), _gate_code(act)
+    _check_f32((("weight", weight), ("dweight", dweight)))
+    _check_dtypes(o, (("gate", gate), ("dy", dy), ("do", do), ("dgate", dgate)))
+    shp, d_v = o.shape, o.shape[-1]
+    _check_shapes((("gate", gate, shp), ("dy", dy, shp), ("do", do, shp), ("dgate", dgate, shp),
+                   ("weight", weight, (d_v,)), ("dweight", dweight, (d_v,))))
+    if workspace is None:
+        workspace = new_workspace(gdn2_gated_norm_bwd_workspace_bytes(_rows(o), d_v), o.device)
+    with _on_device(o):
+        rc = load_library().gdn2_gated_norm_bwd(*(_ptr(t) for t in (o, gate, weight, dy, do, dgate, dweight)), _rows(o),
+                                                d_v, code, float(eps), dt, _ptr(workspace),
+                                                workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != 0:
+        raise GDN2Error(rc, "gdn2_gated_norm_bwd")
+
+
+def gdn2_add_norm_fwd(x, residual, scale, weight, h, y, eps=1e-6, stream=None) -> None:
+    """h = residual + scale * x, y = RMSNorm(h) * weight over the last axis (include/gdn2.h,
+    gdn2_add_norm_fwd).  residual, scale and h may be None (zero, one, not stored)."""
+    _check_cuda(x, residual, scale, weight, h, y)
+    dt, width = _dtype_code(x), x.shape[-1]
+    _check_f32((("scale", scale), ("weight", weight)))
+    _check_dtypes(x, (("residual", residual), ("h", h), ("y", y)))
+    _check_shapes((("residual", residual, x.shape), ("h", h, x.shape), ("y", y, x.shape), ("scale", scale, (width,)),
+                   ("weight", weight, (width,))))
+    with _on_device(x):
+        rc = load_library().gdn2_add_norm_fwd(*(_ptr(t) for t in (x, residual, scale, weight, h, y)), _rows(x), width,
+                                              float(eps), dt, _stream(stream))
+    if rc != 0:
+        raise GDN2Error(rc, "gdn2_add_norm_fwd")
+
+
+def gdn2_add_norm_bwd(h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweight, eps=1e-6, workspace=None,
+                      stream=None) -> None:
+    """Gradients of gdn2_add_norm_fwd at the stored h (include/gdn2.h).  dh may be None (zero); without a
+    scale, x, dx and dscale are not used (dx equals dresidual)."""
+    _check_cuda(h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweight, workspace)
+    dt, shp, width = _dtype_code(h), h.shape, h.shape[-1]
+    _check_f32((("scale", scale), ("weight", weight), ("dscale", dscale), ("dweight", dweight)))
+    _check_dtypes(h, (("x", x), ("dy", dy), ("dh", dh), ("dresidual", dresidual), ("dx", dx)))
+    _check_shapes((("x", x, shp), ("dy", dy, shp), ("dh", dh, shp), ("dresidual", dresidual, shp), ("dx", dx, shp),
+                   ("scale", scale, (width,)), ("weight", weight, (width,)), ("dscale", dscale, (width,)),
+                   ("dweight", dweight, (width,))))
+    if workspace is None:
+        workspace = new_workspace(gdn2_add_norm_bwd_workspace_bytes(_rows(h), width), h.device)
+    with _on_device(h):
+        rc = load_library().gdn2_add_norm_bwd(*(_ptr(t) for t in (h, x, scale, weight, dy, dh, dresidual, dx, dscale,
+                                                                  dweight)), _rows(h), width, float(eps), dt,
+                                              _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                              _stream(stream))
+    if rc != 0:
+        raise GDN2Error(rc, "gdn2_add_norm_bwd")
+
+
+def _check_pool(S, H, K, V, device) -> int:
+    """The slot stride of a state cache [slots, H, d_k, d_v]: each slot contiguous, the slots any
+    distance apart (one layer's part of a larger pool)."""
+    import torch
+    if not S.is_cuda or S.device != device:
+        raise ValueError(f"the state cache must be a CUDA tensor on {device}")
+    if S.dtype != torch.float32:
+        raise TypeError("the state cache must be float32")
+    if S.dim() != 4 or tuple(S.shape[1:]) != (H, K, V):
+        raise ValueError(f"the state cache has shape {tuple(S.shape)}, expected (slots, {H}, {K}, {V})")
+    return _slot_stride(S)
+
+
+def _slot_stride(S) -> int:
+    floats = 1
+    for n in S.shape[1:]:
+        floats *= n
+    if S.shape[0] == 0 or floats == 0:
+        return floats
+    if not S[0].is_contiguous() or (S.shape[0] > 1 and S.stride(0) < floats):
+        raise ValueError("each slot of the state cache must be contiguous and overlap no other")
+    return S.stride(0) if S.shape[0] > 1 else floats
+
+
+def gdn2_tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, o, max_nodes, workspace=None,
+                  stream=None) -> None:
+    """Read-out of every node of every drafted tree over the state cache S [slots, H, d_k, d_v], which is
+    unchanged (include/gdn2.h, gdn2_tree_fwd).  q, k, b, alpha [total, H, d_k]; v, w, o [total, H, d_v];
+    slots [batch], cu_nodes [batch + 1], parents [total] int32 on the device; max_nodes: the most nodes of
+    a tree, at most TREE_MAX_NODES.  Malformed indices are reported in the workspace's status."""
+    _check_cuda(q, k, v, alpha, b, w, slots, cu_nodes, parents, o, workspace)
+    total, H, K = q.shape
+    V = v.shape[-1]
+    dt = _dtype_code(q)
+    _check_f32((("alpha", alpha),))
+    _check_dtypes(q, (("k", k), ("b", b), ("v", v), ("w", w), ("o", o)))
+    tk, tv = (total, H, K), (total, H, V)
+    _check_shapes((("k", k, tk), ("b", b, tk), ("alpha", alpha, tk), ("v", v, tv), ("w", w, tv), ("o", o, tv)))
+    _check_i32((("slots", slots), ("cu_nodes", cu_nodes), ("parents", parents)))
+    batch = slots.shape[0]
+    _check_shapes((("cu_nodes", cu_nodes, (batch + 1,)), ("parents", parents, (total,))))
+    stride = _check_pool(S, H, K, V, q.device)
+    if workspace is None:
+        workspace = new_workspace(0, q.device)
+    with _on_device(q):
+        rc = load_library().gdn2_tree_fwd(*(_ptr(t) for t in (q, k, v, alpha, b, w, S)), stride, S.shape[0],
+                                          *(_ptr(t) for t in (slots, cu_nodes, parents, o)), batch, H, total,
+                                          int(max_nodes), K, V, dt, _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != 0:
+        raise GDN2Error(rc, "gdn2_tree_fwd")
+
+
+def gdn2_recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index, o, workspace=None,
+                       stream=None) -> None:
+    """The recurrence over ragged runs of tokens, from slot to slot of the state cache S
+    [slots, H, d_k, d_v] (include/gdn2.h, gdn2_recurrent_fwd).  q, k, b, alpha [rows, H, d_k]; v, w
+    [rows, H, d_v]; slots_in, slots_out [batch] and cu_tokens [batch + 1] int32 on the device; index [total]
+    int32 or None (entry t is row t); o [total, H, d_v] or None (not wanted).  Malformed indices are reported
+    in the workspace's status."""
+    _check_cuda(q, k, v, alpha, b, w, slots_in, slots_out, cu_tokens, index, o, workspace)
+    rows, H, K = q.shape
+    V = v.shape[-1]
+    dt = _dtype_code(q)
+    _check_f32((("alpha", alpha),))
+    _check_dtypes(q, (("k", k), ("b", b), ("v", v), ("w", w), ("o", o)))
+    tk, tv = (rows, H, K), (rows, H, V)
+    _check_i32((("slots_in", slots_in), ("slots_out", slots_out), ("cu_tokens", cu_tokens), ("index", index)))
+    batch, total = slots_in.shape[0], rows if index is None else index.shape[0]
+    _check_shapes((("k", k, tk), ("b", b, tk), ("alpha", alpha, tk), ("v", v, tv), ("w", w, tv),
+                   ("o", o, (total, H, V)), ("slots_out", slots_out, (batch,)), ("cu_tokens", cu_tokens, (batch + 1,))))
+    stride = _check_pool(S, H, K, V, q.device)
+    if workspace is None:
+        workspace = new_workspace(0, q.device)
+    with _on_device(q):
+        rc = load_library().gdn2_recurrent_fwd(*(_ptr(t) for t in (q, k, v, alpha, b, w, S)), stride, S.shape[0],
+                                               *(_ptr(t) for t in (slots_in, slots_out, cu_tokens, index, o)), batch,
+                                               H, total, rows, K, V, dt, _ptr(workspace),
+                                               workspace.numel() * workspace.element_size(), _stream(stream))
+    if rc != 0:
+        raise GDN2Error(rc, "gdn2_recurrent_fwd")
+
+
+def gdn2_state_copy(dst, src, dst_index, src_index, workspace=None, stream=None) -> None:
+    """dst[dst_index[i]] = src[src_index[i]] (-1: zeros) for every pair, as if all sources were read first
+    (include/gdn2.h, gdn2_state_copy): fork, compact, reorder and clear slots of a state cache.  dst, src:
+    fp32 caches [slots, ...] with equal slot shapes, one cache or two that do not overlap; the indices int32
+    on the device, at most STATE_COPY_MAX_PAIRS."""
+    _check_cuda(dst_index, src_index, workspace)
+    _check_i32((("dst_index", dst_index), ("src_index", src_index)))
+    _check_shapes((("src_index", src_index, dst_index.shape),))
+    _check_f32((("dst", dst), ("src", src)))
+    for t in (dst, src):
+        if not t.is_cuda or t.device != dst_index.device:
+            raise ValueError(f"the state caches must be CUDA tensors on {dst_index.device}")
+    if dst.dim() < 2 or tuple(dst.shape[1:]) != tuple(src.shape[1:]):
+        raise ValueError(f"slots of shape {tuple(dst.shape[1:])} and {tuple(src.shape[1:])}: expected equal ones")
+    floats = 1
+    for n in dst.shape[1:]:
+        floats *= n
+    if workspace is None:
+        workspace = new_workspace(0, dst.device)
+    with _on_device(dst):
+        rc = load_library().gdn2_state_copy(_ptr(dst), _slot_stride(dst), dst.shape[0], _ptr(src), _slot_stride(src),
+                                            src.shape[0], _ptr(dst_index), _ptr(src_index), dst_index.shape[0], floats,
+                                            _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                            _stream(stream))
+    if rc != 0:
+        raise GDN2Error(rc, "gdn2_state_copy")
+
+
 def gdn2_gemm_phase_probe(mode, reps, nctas, workspace, stream=None) -> None:
     """Measurement aid (include/gdn2.h): one chunk's tensor-core products, `reps` chunks per CTA on
     `nctas` CTAs; mode 0 back to back, mode 1 each group waiting for the one before."""
@@ -412,6 +661,60 @@ def decode_step(q, k, v, alpha, b, w, S, stream=None):
     B, H, K = q.shape
     o = torch.empty((B, H, v.shape[-1]), dtype=q.dtype, device=q.device)
     gdn2_decode_step(q, k, v, alpha, b, w, S, o, stream=stream)
+    return o
+
+
+def gated_norm_fwd(o, gate, weight, act="silu", eps=1e-6, stream=None):
+    """Allocating convenience wrapper: returns y."""
+    import torch
+    y = torch.empty_like(o)
+    gdn2_gated_norm_fwd(o, gate, weight, y, act=act, eps=eps, stream=stream)
+    return y
+
+
+def gated_norm_bwd(o, gate, weight, dy, act="silu", eps=1e-6, workspace=None, stream=None):
+    """Allocating convenience wrapper: returns (do, dgate, dweight)."""
+    import torch
+    do, dgate, dweight = torch.empty_like(o), torch.empty_like(gate), torch.empty_like(weight)
+    gdn2_gated_norm_bwd(o, gate, weight, dy, do, dgate, dweight, act=act, eps=eps, workspace=workspace, stream=stream)
+    return do, dgate, dweight
+
+
+def add_norm_fwd(x, residual, scale, weight, eps=1e-6, stream=None):
+    """Allocating convenience wrapper: returns (y, h)."""
+    import torch
+    y, h = torch.empty_like(x), torch.empty_like(x)
+    gdn2_add_norm_fwd(x, residual, scale, weight, h, y, eps=eps, stream=stream)
+    return y, h
+
+
+def add_norm_bwd(h, x, scale, weight, dy, dh=None, eps=1e-6, workspace=None, stream=None):
+    """Allocating convenience wrapper: returns (dresidual, dx, dscale, dweight); without a scale dx is
+    dresidual and dscale None."""
+    import torch
+    dresidual, dweight = torch.empty_like(h), torch.empty_like(weight)
+    dx, dscale = (None, None) if scale is None else (torch.empty_like(h), torch.empty_like(scale))
+    gdn2_add_norm_bwd(h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweight, eps=eps, workspace=workspace,
+                      stream=stream)
+    return dresidual, dresidual if dx is None else dx, dscale, dweight
+
+
+def tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, max_nodes, workspace=None, stream=None):
+    """Allocating convenience wrapper of gdn2_tree_fwd: returns o (rows of no tree hold no values)."""
+    import torch
+    o = torch.empty_like(v)
+    gdn2_tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, o, max_nodes, workspace=workspace, stream=stream)
+    return o
+
+
+def recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index=None, workspace=None, stream=None):
+    """Allocating convenience wrapper of gdn2_recurrent_fwd: updates S, returns o by entry (entries of no
+    sequence hold no values)."""
+    import torch
+    total = q.shape[0] if index is None else index.shape[0]
+    o = torch.empty((total, *v.shape[1:]), dtype=v.dtype, device=v.device)
+    gdn2_recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index, o, workspace=workspace,
+                       stream=stream)
     return o
 
 
@@ -457,3 +760,68 @@ def gdn2_recurrence(q, k, v, alpha, b, w, S0=None):
     if _GDN2_FN is None:
         _GDN2_FN = _recurrence_function()
     return _GDN2_FN.apply(q, k, v, alpha, b, w, S0)
+
+
+def _norm_functions():
+    """torch.autograd.Functions of the two norms over the C ABI."""
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class GatedNorm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, o, gate, weight, act, eps):
+            ctx.save_for_backward(o, gate, weight)
+            ctx.act, ctx.eps = act, eps
+            return gated_norm_fwd(o, gate, weight, act=act, eps=eps)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dy):
+            o, gate, weight = ctx.saved_tensors
+            return (*gated_norm_bwd(o, gate, weight, dy.contiguous(), act=ctx.act, eps=ctx.eps), None, None)
+
+    class AddNorm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, residual, scale, weight, eps):
+            ctx.set_materialize_grads(False)
+            y, h = add_norm_fwd(x, residual, scale, weight, eps=eps)
+            ctx.save_for_backward(h, x if scale is not None else None, scale, weight)
+            ctx.eps = eps
+            return y, h
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dy, dh):
+            h, x, scale, weight = ctx.saved_tensors
+            dy = torch.zeros_like(h) if dy is None else dy.contiguous()
+            dres, dx, dscale, dweight = add_norm_bwd(h, x, scale, weight, dy, None if dh is None else dh.contiguous(),
+                                                     eps=ctx.eps)
+            need = ctx.needs_input_grad
+            # without a scale the two gradients are equal: each input gets memory of its own
+            if scale is None and need[0] and need[1]:
+                dx = dres.clone()
+            return dx, dres if need[1] else None, dscale, dweight, None
+
+    return GatedNorm, AddNorm
+
+
+_NORM_FNS = None
+
+
+def _norm_fn(which):
+    global _NORM_FNS
+    if _NORM_FNS is None:
+        _NORM_FNS = _norm_functions()
+    return _NORM_FNS[which]
+
+
+def gdn2_gated_norm(o, gate, weight, act="silu", eps=1e-6):
+    """Differentiable gated norm: y = RMSNorm(o) * weight * act(gate) over the last axis, with gradients of
+    o, gate and weight through gdn2_gated_norm_bwd.  CUDA tensors as gdn2_gated_norm_fwd's."""
+    return _norm_fn(0).apply(o, gate, weight, act, eps)
+
+
+def gdn2_add_norm(x, residual, weight, scale=None, eps=1e-6):
+    """Differentiable residual norm: returns (y, h) with h = residual + scale * x and y = RMSNorm(h) * weight,
+    gradients of x, residual, scale and weight through gdn2_add_norm_bwd.  residual and scale may be None."""
+    return _norm_fn(1).apply(x, residual, scale, weight, eps)

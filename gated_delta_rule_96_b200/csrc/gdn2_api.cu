@@ -2,6 +2,8 @@
 // Declarations and the meaning of every argument: include/gdn2.h.
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "gdn2.h"
 #include "gdn2_internal.h"
 
@@ -9,6 +11,38 @@ namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool dim_ok(int d) { return d == 64 || d == 128; }
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// width of the residual norm: whole 16-byte vectors in either token type, a row within one block's registers
+bool width_ok(int width) { return width > 0 && width % 8 == 0 && width <= 8192; }
+
+int check_ptrs(std::initializer_list<const void *> ptrs) {
+    for (const void *p : ptrs) {
+        if (!p) return GDN2_ERR_NULL;
+        if (!aligned16(p)) return GDN2_ERR_ALIGN;
+    }
+    return GDN2_OK;
+}
+
+int check_workspace(const void *workspace, size_t bytes, size_t need) {
+    if (!workspace) return GDN2_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return GDN2_ERR_ALIGN;
+    return bytes < need ? GDN2_ERR_WORKSPACE : GDN2_OK;
+}
+
+// arguments that the norms share; the comparison also refuses a NaN
+int check_norm(long long rows, float eps, int dtype) {
+    if (rows < 0) return GDN2_ERR_SHAPE;
+    if (dtype != GDN2_F32 && dtype != GDN2_BF16) return GDN2_ERR_DTYPE;
+    return eps >= 0.f && eps <= 1.f ? GDN2_OK : GDN2_ERR_VALUE;
+}
+
+// a cache of states: `num_slots` slots of [H, d_k, d_v] floats, `slot_stride` floats apart
+int check_pool(const void *S, long long slot_stride, int num_slots, int H, int K, int V) {
+    if (slot_stride < (long long)H * K * V) return GDN2_ERR_SHAPE;
+    if (num_slots > 0 && !S) return GDN2_ERR_NULL;
+    return aligned16(S) && slot_stride % 4 == 0 ? GDN2_OK : GDN2_ERR_ALIGN;
+}
 
 int check_common(const void *q, const void *k, const void *v, const float *alpha, const void *b, const void *w,
                  const void *o, int B, int H, int K, int V, int dtype) {
@@ -229,6 +263,142 @@ int gdn2_rms_norm(void *o, const float *weight, long long rows, int d_v, void *s
     return gdn2::launch_rms_norm(o, weight, rows, d_v, reinterpret_cast<cudaStream_t>(stream));
 }
 
+size_t gdn2_gated_norm_bwd_workspace_bytes(long long rows, int d_v) {
+    if (rows < 0 || !dim_ok(d_v)) return 0;
+    return gdn2::gated_norm_bwd_workspace_bytes(rows, d_v);
+}
+
+int gdn2_gated_norm_fwd(const void *o, const void *gate, const float *weight, void *y, long long rows, int d_v, int act,
+                        float eps, int dtype, void *stream) {
+    int rc = check_norm(rows, eps, dtype);
+    if (rc != GDN2_OK) return rc;
+    if (act != GDN2_GATE_SILU && act != GDN2_GATE_SIGMOID) return GDN2_ERR_VALUE;
+    if (!dim_ok(d_v)) return GDN2_ERR_UNSUPPORTED;
+    if (rows == 0) return GDN2_OK;
+    if ((rc = check_ptrs({o, gate, weight, y})) != GDN2_OK) return rc;
+    return gdn2::launch_gated_norm_fwd(o, gate, weight, y, rows, d_v, act, eps, dtype == GDN2_BF16 ? 1 : 0,
+                                       reinterpret_cast<cudaStream_t>(stream));
+}
+
+int gdn2_gated_norm_bwd(const void *o, const void *gate, const float *weight, const void *dy, void *d_o, void *dgate,
+                        float *dweight, long long rows, int d_v, int act, float eps, int dtype, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    int rc = check_norm(rows, eps, dtype);
+    if (rc != GDN2_OK) return rc;
+    if (act != GDN2_GATE_SILU && act != GDN2_GATE_SIGMOID) return GDN2_ERR_VALUE;
+    if (!dim_ok(d_v)) return GDN2_ERR_UNSUPPORTED;
+    if (rows > 0 && (rc = check_ptrs({o, gate, dy, d_o, dgate})) != GDN2_OK) return rc;
+    if ((rc = check_ptrs({weight, dweight})) != GDN2_OK) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, gdn2::gated_norm_bwd_workspace_bytes(rows, d_v))) != GDN2_OK)
+        return rc;
+    return gdn2::launch_gated_norm_bwd(o, gate, weight, dy, d_o, dgate, dweight, rows, d_v, act, eps,
+                                       dtype == GDN2_BF16 ? 1 : 0, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t gdn2_add_norm_bwd_workspace_bytes(long long rows, int width) {
+    if (rows < 0 || !width_ok(width)) return 0;
+    return gdn2::add_norm_bwd_workspace_bytes(rows, width);
+}
+
+int gdn2_add_norm_fwd(const void *x, const void *residual, const float *scale, const float *weight, void *h, void *y,
+                      long long rows, int width, float eps, int dtype, void *stream) {
+    int rc = check_norm(rows, eps, dtype);
+    if (rc != GDN2_OK) return rc;
+    if (!width_ok(width)) return GDN2_ERR_UNSUPPORTED;
+    if (rows == 0) return GDN2_OK;
+    if ((rc = check_ptrs({x, weight, y})) != GDN2_OK) return rc;
+    if (!aligned16(residual) || !aligned16(scale) || !aligned16(h)) return GDN2_ERR_ALIGN;   // NULL is aligned
+    return gdn2::launch_add_norm_fwd(x, residual, scale, weight, h, y, rows, width, eps, dtype == GDN2_BF16 ? 1 : 0,
+                                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+int gdn2_add_norm_bwd(const void *h, const void *x, const float *scale, const float *weight, const void *dy,
+                      const void *dh, void *dresidual, void *dx, float *dscale, float *dweight, long long rows,
+                      int width, float eps, int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = check_norm(rows, eps, dtype);
+    if (rc != GDN2_OK) return rc;
+    if (!width_ok(width)) return GDN2_ERR_UNSUPPORTED;
+    if (rows > 0 && (rc = check_ptrs({h, dy, dresidual})) != GDN2_OK) return rc;
+    if (rows > 0 && scale && (rc = check_ptrs({x, dx})) != GDN2_OK) return rc;
+    if ((rc = check_ptrs({weight, dweight})) != GDN2_OK) return rc;
+    if (scale && (rc = check_ptrs({scale, dscale})) != GDN2_OK) return rc;
+    if (!aligned16(dh)) return GDN2_ERR_ALIGN;
+    if ((rc = check_workspace(workspace, workspace_bytes, gdn2::add_norm_bwd_workspace_bytes(rows, width))) != GDN2_OK)
+        return rc;
+    return gdn2::launch_add_norm_bwd(h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweight, rows, width, eps,
+                                     dtype == GDN2_BF16 ? 1 : 0, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int gdn2_tree_fwd(const void *q, const void *k, const void *v, const float *alpha, const void *b, const void *w,
+                  const float *S, long long slot_stride, int num_slots, const int *slots, const int *cu_nodes,
+                  const int *parents, void *o, int batch, int H, int total, int max_nodes, int d_k, int d_v, int dtype,
+                  void *workspace, size_t workspace_bytes, void *stream) {
+    if (batch < 0 || total < 0 || max_nodes < 0 || num_slots < 0) return GDN2_ERR_SHAPE;
+    if (total == 0) {   // empty token tensors may be NULL
+        if (H < 0) return GDN2_ERR_SHAPE;
+        if (dtype != GDN2_F32 && dtype != GDN2_BF16) return GDN2_ERR_DTYPE;
+        if (!dim_ok(d_k) || !dim_ok(d_v)) return GDN2_ERR_UNSUPPORTED;
+    } else {
+        const int rc = check_common(q, k, v, alpha, b, w, o, batch, H, d_k, d_v, dtype);
+        if (rc != GDN2_OK) return rc;
+    }
+    if (max_nodes > GDN2_TREE_MAX_NODES || batch > 65535) return GDN2_ERR_UNSUPPORTED;
+    int rc = check_pool(S, slot_stride, num_slots, H, d_k, d_v);
+    if (rc != GDN2_OK) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, gdn2::kStatusBytes)) != GDN2_OK) return rc;
+    if (batch == 0 || H == 0 || total == 0 || max_nodes == 0) return GDN2_OK;
+    if (!slots || !cu_nodes || !parents) return GDN2_ERR_NULL;
+    if (!aligned4(slots) || !aligned4(cu_nodes) || !aligned4(parents)) return GDN2_ERR_ALIGN;
+    return gdn2::launch_tree(q, k, v, alpha, b, w, S, slot_stride, num_slots, slots, cu_nodes, parents, o, batch, H,
+                             total, max_nodes, d_k, d_v, dtype == GDN2_BF16 ? 1 : 0,
+                             reinterpret_cast<unsigned *>(workspace), reinterpret_cast<cudaStream_t>(stream));
+}
+
+int gdn2_recurrent_fwd(const void *q, const void *k, const void *v, const float *alpha, const void *b, const void *w,
+                       float *S, long long slot_stride, int num_slots, const int *slots_in, const int *slots_out,
+                       const int *cu_tokens, const int *index, void *o, int batch, int H, int total, int rows, int d_k,
+                       int d_v, int dtype, void *workspace, size_t workspace_bytes, void *stream) {
+    if (batch < 0 || total < 0 || rows < 0 || num_slots < 0) return GDN2_ERR_SHAPE;
+    if (!index && total > rows) return GDN2_ERR_SHAPE;
+    if (total == 0) {   // no tokens: states are copied or cleared, token tensors may be NULL
+        if (H < 0) return GDN2_ERR_SHAPE;
+        if (dtype != GDN2_F32 && dtype != GDN2_BF16) return GDN2_ERR_DTYPE;
+        if (!dim_ok(d_k) || !dim_ok(d_v)) return GDN2_ERR_UNSUPPORTED;
+    } else {
+        // o is optional: without it only the states are advanced
+        const int rc = check_common(q, k, v, alpha, b, w, o ? o : q, batch, H, d_k, d_v, dtype);
+        if (rc != GDN2_OK) return rc;
+    }
+    if (batch > 65535 || H > 65535) return GDN2_ERR_UNSUPPORTED;
+    int rc = check_pool(S, slot_stride, num_slots, H, d_k, d_v);
+    if (rc != GDN2_OK) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, gdn2::kStatusBytes)) != GDN2_OK) return rc;
+    if (batch == 0 || H == 0) return GDN2_OK;
+    if (!slots_in || !slots_out || !cu_tokens) return GDN2_ERR_NULL;
+    if (!aligned4(slots_in) || !aligned4(slots_out) || !aligned4(cu_tokens) || !aligned4(index)) return GDN2_ERR_ALIGN;
+    return gdn2::launch_recurrent(q, k, v, alpha, b, w, S, slot_stride, num_slots, slots_in, slots_out, cu_tokens,
+                                  index, o, batch, H, total, rows, d_k, d_v, dtype == GDN2_BF16 ? 1 : 0,
+                                  reinterpret_cast<unsigned *>(workspace), reinterpret_cast<cudaStream_t>(stream));
+}
+
+int gdn2_state_copy(float *dst, long long dst_stride, int dst_slots, const float *src, long long src_stride,
+                    int src_slots, const int *dst_index, const int *src_index, int pairs, long long slot_floats,
+                    void *workspace, size_t workspace_bytes, void *stream) {
+    if (dst_slots < 0 || src_slots < 0 || pairs < 0 || slot_floats < 0) return GDN2_ERR_SHAPE;
+    if (dst_stride < slot_floats || src_stride < slot_floats) return GDN2_ERR_SHAPE;
+    if (slot_floats % 4 || dst_stride % 4 || src_stride % 4) return GDN2_ERR_ALIGN;
+    if (pairs > GDN2_STATE_COPY_MAX_PAIRS || slot_floats > (1ll << 31)) return GDN2_ERR_UNSUPPORTED;
+    if (dst == src && dst_stride != src_stride) return GDN2_ERR_SHAPE;
+    int rc = check_workspace(workspace, workspace_bytes, gdn2::kStatusBytes);
+    if (rc != GDN2_OK) return rc;
+    if (pairs == 0 || slot_floats == 0) return GDN2_OK;
+    if ((dst_slots && !dst) || (src_slots && !src) || !dst_index || !src_index) return GDN2_ERR_NULL;
+    if (!aligned16(dst) || !aligned16(src) || !aligned4(dst_index) || !aligned4(src_index)) return GDN2_ERR_ALIGN;
+    return gdn2::launch_state_copy(dst, dst_stride, dst_slots, src, src_stride, src_slots, dst_index, src_index, pairs,
+                                   slot_floats, reinterpret_cast<unsigned *>(workspace),
+                                   reinterpret_cast<cudaStream_t>(stream));
+}
+
 int gdn2_gemm_phase_probe(int mode, int reps, int nctas, void *workspace, size_t workspace_bytes, void *stream) {
     if ((mode != 0 && mode != 1) || reps < 1 || nctas < 1) return GDN2_ERR_SHAPE;
     if (!workspace) return GDN2_ERR_WORKSPACE;
@@ -266,6 +436,7 @@ const char *gdn2_status_str(int status) {
         case GDN2_ERR_DEVICE: return "a kernel reported an internal error";
         case GDN2_ERR_NOALLOC_LIMIT:
             return "problem needs more scratch than the no-allocation entry point's fixed array";
+        case GDN2_ERR_VALUE: return "an argument's value is out of its range";
         default: return "unknown status";
     }
 }

@@ -69,4 +69,33 @@ int launch_chunk_bwd_tc(const void *q, const void *k, const void *v, const float
                         float *dalpha, float *db, float *dw, float *dS0, int B, int H, int T, void *ws,
                         cudaStream_t st);
 
+// The layer's norms with their gradients (d_v in {64, 128}; width a multiple of 8, at most 8192).
+size_t gated_norm_bwd_workspace_bytes(long long rows, int D);
+size_t add_norm_bwd_workspace_bytes(long long rows, int width);
+int launch_gated_norm_fwd(const void *o, const void *gate, const float *weight, void *y, long long rows, int D, int act,
+                          float eps, int bf16, cudaStream_t st);
+int launch_gated_norm_bwd(const void *o, const void *gate, const float *weight, const void *dy, void *d_o, void *dgate,
+                          float *dweight, long long rows, int D, int act, float eps, int bf16, void *ws,
+                          cudaStream_t st);
+int launch_add_norm_fwd(const void *x, const void *residual, const float *scale, const float *weight, void *h, void *y,
+                        long long rows, int width, float eps, int bf16, cudaStream_t st);
+int launch_add_norm_bwd(const void *h, const void *x, const float *scale, const float *weight, const void *dy,
+                        const void *dh, void *dres, void *dx, float *dscale, float *dweight, long long rows, int width,
+                        float eps, int bf16, void *ws, cudaStream_t st);
+
+// Over slots of a state cache: drafted trees, ragged runs, copies (d_k, d_v in {64, 128}).
+constexpr int kTreeMaxNodes = 64;
+constexpr int kStateCopyMaxPairs = 1024;
+int launch_tree(const void *q, const void *k, const void *v, const float *alpha, const void *b, const void *w,
+                const float *S, long long slot_stride, int num_slots, const int *slots, const int *cu,
+                const int *parents, void *o, int batch, int H, int total, int max_nodes, int K, int V, int bf16,
+                unsigned *status, cudaStream_t st);
+int launch_recurrent(const void *q, const void *k, const void *v, const float *alpha, const void *b, const void *w,
+                     float *S, long long slot_stride, int num_slots, const int *slots_in, const int *slots_out,
+                     const int *cu, const int *index, void *o, int batch, int H, int total, int rows, int K, int V,
+                     int bf16, unsigned *status, cudaStream_t st);
+int launch_state_copy(float *dst, long long dst_stride, int dst_slots, const float *src, long long src_stride,
+                      int src_slots, const int *dst_idx, const int *src_idx, int n, long long slot_floats,
+                      unsigned *status, cudaStream_t st);
+
 }  // namespace gdn2

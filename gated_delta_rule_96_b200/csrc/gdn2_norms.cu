@@ -1,0 +1,508 @@
+// The layer's norms (sm_100a): the gated RMSNorm behind the mixer and the residual RMSNorm before the
+// next block, each with its gradients.
+//
+// Gated norm, per row of d_v channels:   x^ = o r,  r = (mean(o^2) + eps)^(-1/2),  y = x^ weight act(g)
+//   backward, dn = dy act(g):  dg = dy x^ weight act'(g),  dx^ = dn weight,
+//                              do = r (dx^ - x^ mean(dx^ x^)),  dweight = sum_rows dn x^
+// Residual norm, per row of `width` channels:   h = residual + scale x,  y = h r(h) weight
+//   backward, at the stored h:  dresidual = dh + r (dy weight - h^ mean(dy weight h^)),
+//                               dx = scale dresidual,  dscale = sum_rows dresidual x,  dweight = sum_rows dy h^
+// Both are one pass over their tensors: a row lives in the registers of the threads that own it, the
+// row sums are fp32 shuffles (and one exchange through shared memory where a row spans warps), and every
+// output is rounded once.  The column sums are fp32 per thread over the rows that it walks, then added in
+// a fixed order (per block, then over the blocks by a second kernel), so results do not change from run
+// to run.
+#include "gdn2_common.cuh"
+#include "gdn2_internal.h"
+
+namespace gdn2 {
+namespace norms {
+
+// 16 bytes of tokens as fp32
+template <typename Tok>
+struct V16;
+template <>
+struct V16<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void unpack(const uint4 &u, float (&x)[8]) {
+        const uint32_t p[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // bf16 is the upper half of an fp32
+            x[2 * i] = __uint_as_float(p[i] << 16);
+            x[2 * i + 1] = __uint_as_float(p[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+        uint32_t p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            p[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        return make_uint4(p[0], p[1], p[2], p[3]);
+    }
+};
+template <>
+struct V16<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void unpack(const uint4 &u, float (&x)[4]) {
+        x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
+        x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+};
+
+// N consecutive fp32 weights (N = 4 or 8, 16-byte aligned)
+template <int N>
+__device__ __forceinline__ void load_f32(const float *p, float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(p + i);
+        x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+    }
+}
+
+// sum over groups of LANES consecutive lanes
+template <int LANES>
+__device__ __forceinline__ float lane_sum(float x) {
+#pragma unroll
+    for (int m = LANES / 2; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    return x;
+}
+
+__device__ __forceinline__ float sigmoid_(float x) { return 1.f / (1.f + __expf(-x)); }
+
+constexpr int ACT_SILU = 0;
+
+// ---------------------------------------------------------------- gated norm
+
+// A row of D channels is held by LPR lanes, 16 bytes each; a thread has U rows in flight.
+template <typename Tok, int D, int ACT, int U>
+__global__ void __launch_bounds__(256) gated_norm_fwd_kernel(const Tok *o, const Tok *gate,
+                                                             const float *__restrict__ weight, Tok *y,
+                                                             long long rows, float eps) {
+    using V = V16<Tok>;
+    constexpr int N = V::N, LPR = D / N, RPW = 32 / LPR;
+    const int lane = threadIdx.x & 31, sub = lane % LPR;
+    const long long first = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * (RPW * U) + lane / LPR;
+    float wt[N];
+    load_f32<N>(weight + sub * N, wt);
+    uint4 xo[U], xg[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const long long r = first + u * RPW;
+        xo[u] = xg[u] = make_uint4(0, 0, 0, 0);
+        if (r < rows) {
+            xo[u] = __ldcs(reinterpret_cast<const uint4 *>(o + r * D) + sub);
+            xg[u] = __ldcs(reinterpret_cast<const uint4 *>(gate + r * D) + sub);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const long long r = first + u * RPW;
+        float x[N], g[N], ss = 0.f;
+        V::unpack(xo[u], x);
+        V::unpack(xg[u], g);
+#pragma unroll
+        for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
+        const float inv = rsqrtf(lane_sum<LPR>(ss) * (1.f / D) + eps);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float s = sigmoid_(g[i]);
+            x[i] = x[i] * inv * wt[i] * (ACT == ACT_SILU ? g[i] * s : s);
+        }
+        if (r < rows) __stcs(reinterpret_cast<uint4 *>(y + r * D) + sub, V::pack(x));
+    }
+}
+
+template <typename Tok, int D, int ACT>
+__global__ void __launch_bounds__(256) gated_norm_bwd_kernel(const Tok *__restrict__ o, const Tok *__restrict__ gate,
+                                                             const float *__restrict__ weight,
+                                                             const Tok *__restrict__ dy, Tok *__restrict__ d_o,
+                                                             Tok *__restrict__ dgate, float *__restrict__ partial,
+                                                             long long rows, float eps) {
+    using V = V16<Tok>;
+    constexpr int N = V::N, LPR = D / N, RPW = 32 / LPR;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR;
+    float wt[N], dw[N];
+    load_f32<N>(weight + sub * N, wt);
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw[i] = 0.f;
+    const long long step = (long long)gridDim.x * 8 * RPW;
+    // rows are walked by whole warps: the shuffles below need every lane
+    for (long long r0 = ((long long)blockIdx.x * 8 + warp) * RPW; r0 < rows; r0 += step) {
+        const long long r = r0 + lane / LPR;
+        uint4 xo = make_uint4(0, 0, 0, 0), xg = xo, xy = xo;
+        if (r < rows) {
+            xo = __ldcs(reinterpret_cast<const uint4 *>(o + r * D) + sub);
+            xg = __ldcs(reinterpret_cast<const uint4 *>(gate + r * D) + sub);
+            xy = __ldcs(reinterpret_cast<const uint4 *>(dy + r * D) + sub);
+        }
+        float x[N], g[N], d[N], ss = 0.f, sd = 0.f;
+        V::unpack(xo, x);
+        V::unpack(xg, g);
+        V::unpack(xy, d);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float s = sigmoid_(g[i]);
+            const float act = ACT == ACT_SILU ? g[i] * s : s;
+            const float slope = ACT == ACT_SILU ? s * (1.f + g[i] * (1.f - s)) : s * (1.f - s);
+            ss = fmaf(x[i], x[i], ss);
+            const float dn = d[i] * act;                  // d(x^ weight)
+            sd = fmaf(dn * wt[i], x[i], sd);
+            g[i] = d[i] * x[i] * wt[i] * slope;           // dgate / r
+            d[i] = dn;
+        }
+        ss = lane_sum<LPR>(ss);
+        sd = lane_sum<LPR>(sd);
+        const float inv = rsqrtf(ss * (1.f / D) + eps);
+        const float mean = sd * inv * inv * (1.f / D);    // mean(dx^ x^) r, to be multiplied by o
+        float out[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            dw[i] = fmaf(d[i], x[i] * inv, dw[i]);
+            out[i] = inv * (d[i] * wt[i] - x[i] * mean);
+            g[i] *= inv;
+        }
+        if (r < rows) {
+            __stcs(reinterpret_cast<uint4 *>(d_o + r * D) + sub, V::pack(out));
+            __stcs(reinterpret_cast<uint4 *>(dgate + r * D) + sub, V::pack(g));
+        }
+    }
+    __shared__ float s_dw[8][D];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float t = dw[i];
+#pragma unroll
+        for (int m = LPR; m < 32; m <<= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+        if (lane < LPR) s_dw[warp][sub * N + i] = t;
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < D; c += 256) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) t += s_dw[w][c];
+        partial[(size_t)blockIdx.x * D + c] = t;
+    }
+}
+
+// out[c] = sum over g of partial[g][c], in a fixed order: 32 columns a block, 32 row groups
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float *__restrict__ partial, int groups, int columns,
+                                                          float *__restrict__ out0, float *__restrict__ out1,
+                                                          int split) {
+    __shared__ float s[32][33];
+    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float t = 0.f;
+    if (c < columns)
+        for (int g = part; g < groups; g += 32) t += partial[(size_t)g * columns + c];
+    s[part][lane] = t;
+    __syncthreads();
+    t = lane_sum<32>(s[lane][part]);
+    if (lane == 0) {
+        const int col = blockIdx.x * 32 + part;
+        if (col < split) out0[col] = t;
+        else if (col < columns) out1[col - split] = t;
+    }
+}
+
+// ---------------------------------------------------------------- residual norm
+
+// Sum over the block of up to two values at once; `s` is one of two buffers taken in turn, so that one
+// barrier a row is enough.
+template <int C>
+__device__ __forceinline__ void block_sum(float (&x)[C], float (*s)[C]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int c = 0; c < C; ++c) x[c] = lane_sum<32>(x[c]);
+    if (warps == 1) return;
+    if (lane == 0)
+#pragma unroll
+        for (int c = 0; c < C; ++c) s[warp][c] = x[c];
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        x[c] = 0.f;
+        for (int w = 0; w < warps; ++w) x[c] += s[w][c];
+    }
+}
+
+constexpr int MAX_WARPS = 16;   // of a block: rows of up to 512 threads
+
+template <typename Tok, int NV>
+__global__ void __launch_bounds__(512) add_norm_fwd_kernel(const Tok *x, const Tok *residual,
+                                                           const float *__restrict__ scale,
+                                                           const float *__restrict__ weight, Tok *h, Tok *y,
+                                                           long long rows, int vecs, float eps) {
+    using V = V16<Tok>;
+    constexpr int N = V::N;
+    __shared__ float s_sum[2][MAX_WARPS][1];
+    const float inv_width = 1.f / (float)(vecs * N);
+    int flip = 0;
+    for (long long r = blockIdx.x; r < rows; r += gridDim.x, flip ^= 1) {
+        const size_t base = (size_t)r * vecs;
+        uint4 xr[NV], rr[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            xr[j] = rr[j] = make_uint4(0, 0, 0, 0);
+            if (v < vecs) {
+                xr[j] = __ldcs(reinterpret_cast<const uint4 *>(x) + base + v);
+                if (residual) rr[j] = __ldcs(reinterpret_cast<const uint4 *>(residual) + base + v);
+            }
+        }
+        float a[NV][N], sum[1] = {0.f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            float xf[N], sc[N];
+            V::unpack(xr[j], xf);
+            V::unpack(rr[j], a[j]);
+            if (scale && v < vecs) load_f32<N>(scale + (size_t)v * N, sc);
+            else
+#pragma unroll
+                for (int i = 0; i < N; ++i) sc[i] = 1.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                a[j][i] = fmaf(sc[i], xf[i], a[j][i]);
+                sum[0] = fmaf(a[j][i], a[j][i], sum[0]);
+            }
+            if (h && v < vecs) __stcs(reinterpret_cast<uint4 *>(h) + base + v, V::pack(a[j]));
+        }
+        block_sum<1>(sum, s_sum[flip]);
+        const float inv = rsqrtf(sum[0] * inv_width + eps);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            if (v < vecs) {
+                float wt[N];
+                load_f32<N>(weight + (size_t)v * N, wt);
+#pragma unroll
+                for (int i = 0; i < N; ++i) a[j][i] *= inv * wt[i];
+                __stcs(reinterpret_cast<uint4 *>(y) + base + v, V::pack(a[j]));
+            }
+        }
+    }
+}
+
+template <typename Tok, int NV, bool SCALED>
+__global__ void __launch_bounds__(512) add_norm_bwd_kernel(const Tok *__restrict__ h, const Tok *__restrict__ x,
+                                                           const float *__restrict__ scale,
+                                                           const float *__restrict__ weight,
+                                                           const Tok *__restrict__ dy, const Tok *__restrict__ dh,
+                                                           Tok *__restrict__ dres, Tok *__restrict__ dx,
+                                                           float *__restrict__ partial, long long rows, int vecs,
+                                                           float eps) {
+    using V = V16<Tok>;
+    constexpr int N = V::N;
+    __shared__ float s_sum[2][MAX_WARPS][2];
+    const int width = vecs * N;
+    const float inv_width = 1.f / (float)width;
+    float wt[NV][N], sc[NV][N], dw[NV][N], ds[NV][N];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+#pragma unroll
+        for (int i = 0; i < N; ++i) wt[j][i] = sc[j][i] = dw[j][i] = ds[j][i] = 0.f;
+        if (v < vecs) {
+            load_f32<N>(weight + (size_t)v * N, wt[j]);
+            if (SCALED) load_f32<N>(scale + (size_t)v * N, sc[j]);
+        }
+    }
+    int flip = 0;
+    for (long long r = blockIdx.x; r < rows; r += gridDim.x, flip ^= 1) {
+        const size_t base = (size_t)r * vecs;
+        uint4 hr[NV], xr[NV], yr[NV], gr[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            hr[j] = xr[j] = yr[j] = gr[j] = make_uint4(0, 0, 0, 0);
+            if (v < vecs) {
+                hr[j] = __ldcs(reinterpret_cast<const uint4 *>(h) + base + v);
+                yr[j] = __ldcs(reinterpret_cast<const uint4 *>(dy) + base + v);
+                if (SCALED) xr[j] = __ldcs(reinterpret_cast<const uint4 *>(x) + base + v);
+                if (dh) gr[j] = __ldcs(reinterpret_cast<const uint4 *>(dh) + base + v);
+            }
+        }
+        float sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float hf[N], df[N];
+            V::unpack(hr[j], hf);
+            V::unpack(yr[j], df);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                sum[0] = fmaf(hf[i], hf[i], sum[0]);
+                sum[1] = fmaf(df[i] * wt[j][i], hf[i], sum[1]);
+            }
+        }
+        block_sum<2>(sum, s_sum[flip]);
+        const float inv = rsqrtf(sum[0] * inv_width + eps);
+        const float mean = sum[1] * inv * inv * inv_width;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            float hf[N], df[N], gf[N];
+            V::unpack(hr[j], hf);
+            V::unpack(yr[j], df);
+            V::unpack(gr[j], gf);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                dw[j][i] = fmaf(df[i], hf[i] * inv, dw[j][i]);
+                gf[i] += inv * (df[i] * wt[j][i] - hf[i] * mean);
+            }
+            if (v < vecs) __stcs(reinterpret_cast<uint4 *>(dres) + base + v, V::pack(gf));
+            if (SCALED) {
+                float xf[N];
+                V::unpack(xr[j], xf);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    ds[j][i] = fmaf(gf[i], xf[i], ds[j][i]);
+                    gf[i] *= sc[j][i];
+                }
+                if (v < vecs) __stcs(reinterpret_cast<uint4 *>(dx) + base + v, V::pack(gf));
+            }
+        }
+    }
+    float *mine = partial + (size_t)blockIdx.x * width * (SCALED ? 2 : 1);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        if (v < vecs)
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                *reinterpret_cast<float4 *>(mine + (size_t)v * N + i) =
+                    make_float4(dw[j][i], dw[j][i + 1], dw[j][i + 2], dw[j][i + 3]);
+                if (SCALED)
+                    *reinterpret_cast<float4 *>(mine + width + (size_t)v * N + i) =
+                        make_float4(ds[j][i], ds[j][i + 1], ds[j][i + 2], ds[j][i + 3]);
+            }
+    }
+}
+
+// blocks of the backward kernels, each with one row of partial column sums
+int gated_bwd_blocks(long long rows) {
+    const long long want = (rows + 7) / 8;
+    return (int)(want < 148 * 4 ? (want > 0 ? want : 1) : 148 * 4);
+}
+int add_bwd_blocks(long long rows) { return (int)(rows < 148 * 4 ? (rows > 0 ? rows : 1) : 148 * 4); }
+
+// threads of a block that holds a row of `vecs` 16-byte vectors, NV a thread
+int row_threads(int vecs, int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; }
+
+template <typename Tok, int D, int ACT>
+int gated_fwd_t(const void *o, const void *gate, const float *weight, void *y, long long rows, float eps,
+                cudaStream_t st) {
+    constexpr int PER_WARP = 32 / (D / V16<Tok>::N), U = 4;
+    const long long per_block = 8 * PER_WARP * U;
+    gated_norm_fwd_kernel<Tok, D, ACT, U><<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, st>>>(
+        (const Tok *)o, (const Tok *)gate, weight, (Tok *)y, rows, eps);
+    return launch_status();
+}
+template <typename Tok, int D, int ACT>
+int gated_bwd_t(const void *o, const void *gate, const float *weight, const void *dy, void *d_o, void *dgate,
+                float *dweight, long long rows, float eps, float *partial, cudaStream_t st) {
+    const int blocks = gated_bwd_blocks(rows);
+    gated_norm_bwd_kernel<Tok, D, ACT><<<blocks, 256, 0, st>>>((const Tok *)o, (const Tok *)gate, weight,
+                                                               (const Tok *)dy, (Tok *)d_o, (Tok *)dgate, partial,
+                                                               rows, eps);
+    column_sum_kernel<<<D / 32, 1024, 0, st>>>(partial, blocks, D, dweight, nullptr, D);
+    return launch_status();
+}
+
+template <typename Tok>
+int add_fwd_t(const void *x, const void *residual, const float *scale, const float *weight, void *h, void *y,
+              long long rows, int width, float eps, cudaStream_t st) {
+    const int vecs = width / V16<Tok>::N, nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4, nt = row_threads(vecs, nv);
+    const unsigned blocks = (unsigned)(rows < (1 << 30) ? rows : (1 << 30));
+    auto go = [&](auto kern) {
+        kern<<<blocks, nt, 0, st>>>((const Tok *)x, (const Tok *)residual, scale, weight, (Tok *)h, (Tok *)y, rows,
+                                    vecs, eps);
+    };
+    if (nv == 1) go(add_norm_fwd_kernel<Tok, 1>);
+    else if (nv == 2) go(add_norm_fwd_kernel<Tok, 2>);
+    else if constexpr (sizeof(Tok) == 4) go(add_norm_fwd_kernel<Tok, 4>);   // bf16 rows end at 1024 vectors
+    return launch_status();
+}
+template <typename Tok, bool SCALED>
+int add_bwd_t(const void *h, const void *x, const float *scale, const float *weight, const void *dy, const void *dh,
+              void *dres, void *dx, float *dscale, float *dweight, long long rows, int width, float eps,
+              float *partial, cudaStream_t st) {
+    const int vecs = width / V16<Tok>::N, nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4, nt = row_threads(vecs, nv);
+    const int blocks = add_bwd_blocks(rows), columns = width * (SCALED ? 2 : 1);
+    auto go = [&](auto kern) {
+        kern<<<blocks, nt, 0, st>>>((const Tok *)h, (const Tok *)x, scale, weight, (const Tok *)dy, (const Tok *)dh,
+                                    (Tok *)dres, (Tok *)dx, partial, rows, vecs, eps);
+    };
+    if (nv == 1) go(add_norm_bwd_kernel<Tok, 1, SCALED>);
+    else if (nv == 2) go(add_norm_bwd_kernel<Tok, 2, SCALED>);
+    else if constexpr (sizeof(Tok) == 4) go(add_norm_bwd_kernel<Tok, 4, SCALED>);   // bf16 rows end at 1024 vectors
+    column_sum_kernel<<<(columns + 31) / 32, 1024, 0, st>>>(partial, blocks, columns, dweight, dscale, width);
+    return launch_status();
+}
+
+}  // namespace norms
+
+size_t gated_norm_bwd_workspace_bytes(long long rows, int D) {
+    return kStatusBytes + sizeof(float) * (size_t)norms::gated_bwd_blocks(rows) * D;
+}
+size_t add_norm_bwd_workspace_bytes(long long rows, int width) {
+    return kStatusBytes + sizeof(float) * (size_t)norms::add_bwd_blocks(rows) * width * 2;
+}
+
+int launch_gated_norm_fwd(const void *o, const void *gate, const float *weight, void *y, long long rows, int D, int act,
+                          float eps, int bf16, cudaStream_t st) {
+    using namespace norms;
+    using bf = __nv_bfloat16;
+#define GDN2_GATED(T, DD, A) return gated_fwd_t<T, DD, A>(o, gate, weight, y, rows, eps, st)
+#define GDN2_GATED_ACT(T, DD) do { if (act == 0) GDN2_GATED(T, DD, 0); GDN2_GATED(T, DD, 1); } while (0)
+    if (bf16) {
+        if (D == 128) GDN2_GATED_ACT(bf, 128);
+        GDN2_GATED_ACT(bf, 64);
+    }
+    if (D == 128) GDN2_GATED_ACT(float, 128);
+    GDN2_GATED_ACT(float, 64);
+#undef GDN2_GATED
+}
+
+int launch_gated_norm_bwd(const void *o, const void *gate, const float *weight, const void *dy, void *d_o, void *dgate,
+                          float *dweight, long long rows, int D, int act, float eps, int bf16, void *ws,
+                          cudaStream_t st) {
+    using namespace norms;
+    using bf = __nv_bfloat16;
+    float *partial = reinterpret_cast<float *>(static_cast<char *>(ws) + kStatusBytes);
+#define GDN2_GATED(T, DD, A) return gated_bwd_t<T, DD, A>(o, gate, weight, dy, d_o, dgate, dweight, rows, eps, partial, st)
+    if (bf16) {
+        if (D == 128) GDN2_GATED_ACT(bf, 128);
+        GDN2_GATED_ACT(bf, 64);
+    }
+    if (D == 128) GDN2_GATED_ACT(float, 128);
+    GDN2_GATED_ACT(float, 64);
+#undef GDN2_GATED
+#undef GDN2_GATED_ACT
+}
+
+int launch_add_norm_fwd(const void *x, const void *residual, const float *scale, const float *weight, void *h, void *y,
+                        long long rows, int width, float eps, int bf16, cudaStream_t st) {
+    if (bf16) return norms::add_fwd_t<__nv_bfloat16>(x, residual, scale, weight, h, y, rows, width, eps, st);
+    return norms::add_fwd_t<float>(x, residual, scale, weight, h, y, rows, width, eps, st);
+}
+
+int launch_add_norm_bwd(const void *h, const void *x, const float *scale, const float *weight, const void *dy,
+                        const void *dh, void *dres, void *dx, float *dscale, float *dweight, long long rows, int width,
+                        float eps, int bf16, void *ws, cudaStream_t st) {
+    using namespace norms;
+    using bf = __nv_bfloat16;
+    float *partial = reinterpret_cast<float *>(static_cast<char *>(ws) + kStatusBytes);
+#define GDN2_ADD(T, S) return add_bwd_t<T, S>(h, x, scale, weight, dy, dh, dres, dx, dscale, dweight, rows, width, eps, partial, st)
+    if (bf16) {
+        if (scale) GDN2_ADD(bf, true);
+        GDN2_ADD(bf, false);
+    }
+    if (scale) GDN2_ADD(float, true);
+    GDN2_ADD(float, false);
+#undef GDN2_ADD
+}
+
+}  // namespace gdn2

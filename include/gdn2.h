@@ -54,11 +54,24 @@ typedef enum {
     GDN2_ERR_ALIGN = -7,        /* a pointer is not 16-byte aligned                  */
     GDN2_ERR_DEVICE = -8,       /* a kernel reported an internal error (bounded wait
                                    expired); read by gdn2_workspace_status           */
-    GDN2_ERR_NOALLOC_LIMIT = -9 /* gdn2_chunk_fwd_noalloc: the problem needs more
+    GDN2_ERR_NOALLOC_LIMIT = -9, /* gdn2_chunk_fwd_noalloc: the problem needs more
                                    scratch than GDN2_NOALLOC_SCRATCH_BYTES           */
+    GDN2_ERR_VALUE = -10        /* a value (an eps, a gate's code) is out of its range */
 } gdn2_status;
 
 typedef enum { GDN2_F32 = 0, GDN2_BF16 = 1 } gdn2_dtype;
+
+typedef enum { GDN2_GATE_SILU = 0, GDN2_GATE_SIGMOID = 1 } gdn2_gate;
+
+/* Bits of a workspace's status word (gdn2_workspace_status) for device-side indices that the host
+ * cannot check: gdn2_tree_fwd, gdn2_recurrent_fwd and gdn2_state_copy leave the sequence or pair
+ * that has one out as a whole, write nothing of it, and set the bit. */
+#define GDN2_DEV_RANGE 0x100    /* cumulative lengths that decrease, pass the total, or hold more
+                                   than max_nodes nodes                                          */
+#define GDN2_DEV_SLOT 0x200     /* a slot outside [-1, num_slots)                                */
+#define GDN2_DEV_PARENT 0x400   /* a parent that is not -1 or an earlier node of the same tree   */
+#define GDN2_DEV_INDEX 0x800    /* a token index outside [0, rows)                               */
+#define GDN2_DEV_CONFLICT 0x1000 /* a destination slot that another sequence reads or writes     */
 
 /* Bytes of device workspace gdn2_chunk_fwd needs for these sizes (0 on bad sizes is
  * never returned: at least the 256-byte status header is always required).
@@ -131,6 +144,136 @@ GDN2_API int gdn2_layer_edge_maps(const void *q_raw, const void *k_raw, const fl
 /* RMSNorm of the layer output in place: o <- o / sqrt(mean_v(o^2) + 1e-6) * weight, per row of d_v.
  * o [rows, d_v] bf16, weight [d_v] fp32; d_v in {64, 128}. */
 GDN2_API int gdn2_rms_norm(void *o, const float *weight, long long rows, int d_v, void *stream);
+
+/*
+ * RMSNorm of the mixer's output with the layer's output gate, out of place (the gate of the layer's
+ * output, beside gdn2_rms_norm).  Per row:
+ *   y = o / sqrt(mean_v(o^2) + eps) * weight * act(gate),   act(g) = g sigmoid(g) (GDN2_GATE_SILU)
+ *                                                           or sigmoid(g) (GDN2_GATE_SIGMOID)
+ *   o, gate, y   [rows, d_v]  token dtype; y may be o or gate
+ *   weight       [d_v]        fp32
+ * d_v in {64, 128}; eps in [0, 1].  fp32 arithmetic, y rounded once.
+ */
+GDN2_API int gdn2_gated_norm_fwd(const void *o, const void *gate, const float *weight, void *y, long long rows, int d_v,
+                                 int act, float eps, int dtype, void *stream);
+
+/* Bytes of device workspace gdn2_gated_norm_bwd needs (0 on bad sizes): the status header and one
+ * fp32 row of d_v partial sums for each of at most 592 blocks.  Depends only on its arguments. */
+GDN2_API size_t gdn2_gated_norm_bwd_workspace_bytes(long long rows, int d_v);
+
+/* Gradients of gdn2_gated_norm_fwd at its inputs, given dy = dL/dy [rows, d_v] (token dtype):
+ *   d_o, dgate (out)  [rows, d_v]  token dtype, rounded once from fp32
+ *   dweight    (out)  [d_v]        fp32, summed over the rows in a fixed order (deterministic)
+ *   workspace         at least gdn2_gated_norm_bwd_workspace_bytes(...) bytes, no initialisation
+ *                     needed; it serves one call at a time
+ * The outputs must not alias the inputs or each other.  rows = 0 writes dweight = 0. */
+GDN2_API int gdn2_gated_norm_bwd(const void *o, const void *gate, const float *weight, const void *dy, void *d_o,
+                                 void *dgate, float *dweight, long long rows, int d_v, int act, float eps, int dtype,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Residual sum and RMSNorm before a block, with the residual scale of the block before.  Per row:
+ *   h = residual + scale * x,   y = h / sqrt(mean(h^2) + eps) * weight
+ *   x, residual, h, y  [rows, width]  token dtype; residual may be NULL (zero: the first block); h may
+ *                      be NULL (not stored), x or residual; y may be x or residual
+ *   scale, weight      [width]        fp32; scale may be NULL (one)
+ * width a multiple of 8, at most 8192; eps in [0, 1].  h and y are each rounded once from fp32 (y is
+ * the norm of the sum before its rounding).
+ */
+GDN2_API int gdn2_add_norm_fwd(const void *x, const void *residual, const float *scale, const float *weight, void *h,
+                               void *y, long long rows, int width, float eps, int dtype, void *stream);
+
+/* Bytes of device workspace gdn2_add_norm_bwd needs (0 on bad sizes): the status header and two fp32
+ * rows of width partial sums for each of at most 592 blocks.  Depends only on its arguments. */
+GDN2_API size_t gdn2_add_norm_bwd_workspace_bytes(long long rows, int width);
+
+/* Gradients of gdn2_add_norm_fwd, given dy = dL/dy and dh = dL/dh (the residual stream's own
+ * gradient; NULL for zero), at the stored h:
+ *   dresidual (out)  [rows, width]  token dtype, dL/dresidual
+ *   dx        (out)  [rows, width]  token dtype, scale * dresidual (rounded from fp32); not written
+ *                                   and may be NULL when scale is NULL, where it equals dresidual
+ *   dscale    (out)  [width]        fp32, sum_rows dresidual x; not written when scale is NULL
+ *   dweight   (out)  [width]        fp32
+ * x is read only when scale is given.  The sums over the rows are taken in a fixed order
+ * (deterministic).  Workspace and aliasing as gdn2_gated_norm_bwd.  rows = 0 writes zero sums. */
+GDN2_API int gdn2_add_norm_bwd(const void *h, const void *x, const float *scale, const float *weight, const void *dy,
+                               const void *dh, void *dresidual, void *dx, float *dscale, float *dweight,
+                               long long rows, int width, float eps, int dtype, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/*
+ * A state cache: num_slots slots of [H, d_k, d_v] fp32 states, slot_stride floats apart (at least
+ * H*d_k*d_v, a multiple of 4: the slots may be one layer's part of a larger pool).  The three calls
+ * below address it by slot, with index arrays (int32) in DEVICE memory.  Their workspace holds only
+ * the 256-byte status header (zeroed once); malformed indices are reported there (GDN2_DEV_*).
+ *
+ * Drafted tokens in trees: the read-out of every node of every sequence's tree, the cache unchanged.
+ * A node's state is its parent's after one step of the recurrence; o is the step's read-out.
+ *
+ *   q, k, b    [total, H, d_k]  token dtype: the nodes of all trees, one tree after the other
+ *   v, w       [total, H, d_v]  token dtype
+ *   alpha      [total, H, d_k]  fp32
+ *   slots      [batch]          the slot of the state that a tree hangs on; -1: a zero state
+ *   cu_nodes   [batch + 1]      tree i owns the nodes cu_nodes[i] .. cu_nodes[i+1]-1 (none: an
+ *                               empty tree)
+ *   parents    [total]          a node's parent, counted within its tree: an earlier node, or -1
+ *                               for one that hangs on the state itself (several may)
+ *   o  (out)   [total, H, d_v]  token dtype; rows of no tree are left as they were
+ *   max_nodes  the most nodes of a tree, at most GDN2_TREE_MAX_NODES
+ *
+ * A node reads only itself and its ancestors: values of other branches, NaN included, do not reach
+ * it.  Any decay is exact, zero included.  batch at most 65,535.  An accepted path is taken into the
+ * cache by gdn2_recurrent_fwd with the path's nodes as `index`.
+ */
+#define GDN2_TREE_MAX_NODES 64
+GDN2_API int gdn2_tree_fwd(const void *q, const void *k, const void *v, const float *alpha, const void *b,
+                           const void *w, const float *S, long long slot_stride, int num_slots, const int *slots,
+                           const int *cu_nodes, const int *parents, void *o, int batch, int H, int total,
+                           int max_nodes, int d_k, int d_v, int dtype, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
+ * The recurrence over ragged runs of tokens, from slot to slot of the cache: a served batch's decode
+ * step (runs of one), short prompt tails, and the accepted paths of drafted trees.
+ *
+ *   q, k, b     [rows, H, d_k]   token dtype
+ *   v, w        [rows, H, d_v]   token dtype
+ *   alpha       [rows, H, d_k]   fp32
+ *   slots_in    [batch]          the slot a sequence's state is read from; -1: a zero state
+ *   slots_out   [batch]          the slot its last state is written to (the same one: in place);
+ *                                -1: not written
+ *   cu_tokens   [batch + 1]      sequence i owns the entries cu_tokens[i] .. cu_tokens[i+1]-1; an
+ *                                empty run moves (or clears) the state
+ *   index       [total]          the row of each entry's token; NULL: entry t is row t
+ *   o  (out)    [total, H, d_v]  token dtype, by entry; NULL: not wanted.  Rows of no sequence are
+ *                                left as they were
+ *
+ * A slot that one sequence writes may be neither read nor written by another one of the call: such a
+ * writer is left out (GDN2_DEV_CONFLICT).  The token rows are walked one at a time in fp32, with the
+ * state in registers: exact for any decay, and meant for runs up to some hundred tokens (long
+ * prompts: gdn2_chunk_fwd).  batch and H at most 65,535.
+ */
+GDN2_API int gdn2_recurrent_fwd(const void *q, const void *k, const void *v, const float *alpha, const void *b,
+                                const void *w, float *S, long long slot_stride, int num_slots, const int *slots_in,
+                                const int *slots_out, const int *cu_tokens, const int *index, void *o, int batch,
+                                int H, int total, int rows, int d_k, int d_v, int dtype, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
+ * Copies between slots: for each pair, dst slot dst_index[i] = src slot src_index[i] (-1: zeros), as
+ * if every source were read before any destination is written -- copy, fork (one source, several
+ * destinations), compact, reorder in place (any permutation) and clear.  A destination of -1 is
+ * skipped; of several pairs with one destination the last counts.
+ *
+ *   dst, src   caches of dst_slots / src_slots slots, slot_floats floats each, dst_stride /
+ *              src_stride floats apart (multiples of 4); one cache (same pointer and stride) or two
+ *              that do not overlap
+ *   pairs      at most GDN2_STATE_COPY_MAX_PAIRS in one call
+ */
+#define GDN2_STATE_COPY_MAX_PAIRS 1024
+GDN2_API int gdn2_state_copy(float *dst, long long dst_stride, int dst_slots, const float *src, long long src_stride,
+                             int src_slots, const int *dst_index, const int *src_index, int pairs,
+                             long long slot_floats, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * One decode token per sequence, state updated in place (constant memory per token,

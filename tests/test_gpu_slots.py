@@ -1,0 +1,385 @@
+"""GPU parity of the operators over a state cache (drafted trees, ragged runs, copies) against the fp64
+definitions, their reports of malformed indices, and a run of them together.
+
+Tolerances.  A step of the recurrence in fp32 adds at most some 22 roundings of 2^-24 to an element, relative
+to the largest term (16 in-thread and 3 shuffled additions of a dot product, the decay, the update), the map
+of a step does not grow what came before by more than the terms' own size, and the longest runs here have 64
+steps: 22 * 64 * 2^-24 = 8.4e-5 of the largest value, under the fp32 bar of 1e-4 that the other parity tests
+use.  bf16 outputs add one rounding, 2^-8 of the value.  Copies are exact."""
+import numpy as np
+import pytest
+
+from oracle import operators as op
+from tests.gpu_util import cuda_or_skip, f64
+
+pytestmark = pytest.mark.gpu
+BAR = 1e-4
+HALF = {"bf16": 2.0 ** -8, "f32": 0.0}
+
+
+def tokens(torch, seed, n, H, K, V, dtype, low=None):
+    gen = torch.Generator().manual_seed(seed)
+    td = torch.bfloat16 if dtype == "bf16" else torch.float32
+    r = lambda d: torch.randn(n, H, d, generator=gen)  # noqa: E731
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True)  # noqa: E731
+    alpha = torch.exp(-torch.nn.functional.softplus(r(K) + 1))
+    if low is not None:
+        alpha[torch.rand(alpha.shape, generator=gen) < 0.1] = low
+    x = [unit(r(K)).to(td), unit(r(K)).to(td), r(V).to(td), alpha, torch.sigmoid(r(K)).to(td), torch.sigmoid(r(V)).to(td)]
+    return [a.cuda() for a in x]
+
+
+def make_pool(torch, seed, slots, H, K, V):
+    return (0.2 * torch.randn(slots, H, K, V, generator=torch.Generator().manual_seed(seed))).cuda()
+
+
+def i32(torch, v):
+    return torch.tensor(list(v), dtype=torch.int32, device="cuda")
+
+
+def close(got, ref, dtype):
+    got = f64(got)
+    assert np.isfinite(got).all()
+    bar = BAR * np.abs(ref).max() + HALF[dtype] * np.abs(ref)
+    assert (np.abs(got - ref) <= bar).all(), f"worst {np.max(np.abs(got - ref) / bar):.2f} of the bar"
+
+
+def random_tree(rng, n, back):
+    return [-1] + [int(rng.integers(max(-1, i - back), i)) for i in range(1, n)] if n else []
+
+
+def run_tree(torch, g, x, pool, slots, sizes, parents, extra=0, most=None):
+    total, H, V = x[0].shape[0], x[0].shape[1], x[2].shape[2]
+    cu = np.concatenate([[0], np.cumsum(sizes)])
+    assert cu[-1] + extra == total
+    o = torch.full((total, H, V), float("nan"), dtype=x[0].dtype, device="cuda")
+    ws = g.new_workspace(0)
+    par = list(parents) + [-7] * extra
+    before = pool.clone()
+    g.gdn2_tree_fwd(*x, pool, i32(torch, slots), i32(torch, cu), i32(torch, par), o, most or max(list(sizes) + [0]),
+                    workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(pool, before)
+    ref = op.tree(*(f64(a) for a in x), f64(pool), slots, cu, par) if total - extra else None
+    return o, ref, int(cu[-1]), g.gdn2_workspace_status(ws)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 64), (64, 128), (128, 64)])
+@pytest.mark.parametrize("sizes", [[1], [2, 0, 5], [8, 3, 1, 0, 7], [17, 31, 32], [33, 64], [64, 63, 2, 48]])
+def test_tree(dtype, K, V, sizes):
+    torch, g = cuda_or_skip()
+    rng, H = np.random.default_rng(sum(sizes)), 3
+    x = tokens(torch, sum(sizes), sum(sizes) + 2, H, K, V, dtype)
+    parents = sum((random_tree(rng, n, 9) for n in sizes), [])
+    o, ref, rows, status = run_tree(torch, g, x, make_pool(torch, 1, 7, H, K, V), rng.permutation(7)[:len(sizes)].tolist(),
+                                    sizes, parents, extra=2)
+    assert status == 0
+    close(o[:rows], ref[:rows], dtype)
+    assert torch.isnan(o[rows:]).all()           # rows of no tree stay as they were
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", ["chain", "star", "roots", "twos"])
+@pytest.mark.parametrize("n", [6, 64])
+def test_tree_shapes_on_a_zero_state_and_with_hard_decays(dtype, shape, n):
+    torch, g = cuda_or_skip()
+    parents = {"chain": [i - 1 for i in range(n)], "star": [-1] + [0] * (n - 1), "roots": [-1] * n,
+               "twos": [-1] + [(i - 1) // 2 for i in range(1, n)]}[shape]
+    for low in (None, 0.0, 1e-30):               # decays that end the past, or nearly
+        x = tokens(torch, n, 2 * n, 2, 128, 128, dtype, low)
+        if low is None:                          # and decays that keep it
+            x[3].copy_(1 - 0.01 * x[3])
+        o, ref, rows, status = run_tree(torch, g, x, make_pool(torch, 2, 3, 2, 128, 128), [-1, 2], [n, n], parents * 2)
+        assert status == 0
+        close(o, ref, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [7, 40])
+def test_tree_branches_do_not_touch_one_another(dtype, n):
+    """NaN and infinities on one branch, and in another sequence's state, stay there."""
+    torch, g = cuda_or_skip()
+    parents = [-1, 0, 0] + [1 + (i % 2) for i in range(n - 3)]    # two branches below node 0
+    x = tokens(torch, 3, 2 * n, 2, 128, 128, dtype)
+    pool = make_pool(torch, 4, 3, 2, 128, 128)
+    clean, ref, _, _ = run_tree(torch, g, x, pool, [0, 1], [n, n], parents * 2)
+    sick = [i for i in range(n) if i == 1 or parents[i] == 1]
+    y = [a.clone() for a in x]
+    for a, bad in zip(y, (float("nan"), float("inf"), float("nan"), float("nan"), float("inf"), float("nan"))):
+        a[sick] = bad
+        a[n:] = bad                               # the whole second tree
+    pool[1:] = float("nan")
+    o = torch.empty_like(clean)
+    g.gdn2_tree_fwd(*y, pool, i32(torch, [0, 1]), i32(torch, [0, n, 2 * n]), i32(torch, parents * 2), o, n)
+    well = [i for i in range(n) if i not in sick]
+    assert torch.equal(o[well], clean[well])
+    assert not torch.isfinite(o[sick].float()).any()
+
+
+def test_tree_reports_malformed_indices_and_serves_the_rest():
+    torch, g = cuda_or_skip()
+    H, n = 2, 5
+    x = tokens(torch, 5, 6 * n, H, 128, 128, "f32")
+    pool = make_pool(torch, 6, 4, H, 128, 128)
+    good = [-1, 0, 1, 1, 0]
+    base = dict(slots=[0, 1, 2, 3, 0, 1], cu=[n * i for i in range(7)], parents=good * 6)
+    want = op.tree(*(f64(a) for a in x), f64(pool), base["slots"], base["cu"], base["parents"])
+
+    def go(most=n, **change):
+        c = {k: list(v) for k, v in base.items()}
+        for key, (at, value) in change.items():
+            c[key][at] = value
+        o = torch.full((6 * n, H, 128), float("nan"), device="cuda")
+        ws = g.new_workspace(0)
+        g.gdn2_tree_fwd(*x, pool, i32(torch, c["slots"]), i32(torch, c["cu"]), i32(torch, c["parents"]), o, most, workspace=ws)
+        return f64(o).reshape(6, n, H, 128), g.gdn2_workspace_status(ws)
+
+    ref = want.reshape(6, n, H, 128)
+    for change, bit, out in (({"slots": (2, 4)}, g.DEV_SLOT, [2]), ({"slots": (0, -2)}, g.DEV_SLOT, [0]),
+                             ({"parents": (n + 2, 2)}, g.DEV_PARENT, [1]), ({"parents": (3 * n, -2)}, g.DEV_PARENT, [3]),
+                             ({"parents": (4 * n + 1, 1 << 30)}, g.DEV_PARENT, [4]),
+                             ({"cu": (6, 6 * n + 1)}, g.DEV_RANGE, [5]), ({"cu": (0, -1)}, g.DEV_RANGE, [0]),
+                             ({"cu": (3, 2 * n - 1)}, g.DEV_RANGE, [2, 3])):
+        o, status = go(**change)
+        assert status == bit, (change, hex(status))
+        for i in range(6):
+            if i in out:
+                assert np.isnan(o[i]).all(), (change, i)
+            else:
+                assert np.abs(o[i] - ref[i]).max() <= BAR * np.abs(ref).max()
+    o, status = go(most=n - 1)
+    assert status == g.DEV_RANGE and np.isnan(o).all()
+
+
+def run_recurrent(torch, g, x, pool, src, dst, sizes, index=None, want_o=True, extra=0):
+    H, V = x[0].shape[1], x[2].shape[2]
+    cu = np.concatenate([[0], np.cumsum(sizes)])
+    total = x[0].shape[0] if index is None else len(index)
+    assert cu[-1] + extra == total
+    o = torch.full((total, H, V), float("nan"), dtype=x[0].dtype, device="cuda") if want_o else None
+    ws = g.new_workspace(0)
+    ref = op.recurrent(*(f64(a) for a in x), f64(pool), src, dst, cu, index)
+    g.gdn2_recurrent_fwd(*x, pool, i32(torch, src), i32(torch, dst), i32(torch, cu),
+                         None if index is None else i32(torch, index), o, workspace=ws)
+    torch.cuda.synchronize()
+    assert g.gdn2_workspace_status(ws) == 0
+    return o, ref[0], ref[1], int(cu[-1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 64), (64, 128), (128, 64)])
+@pytest.mark.parametrize("H,sizes", [(1, [1]), (3, [1, 1, 1, 1]), (2, [2, 0, 9, 1]), (5, [8, 7, 17, 0, 3]), (16, [64]),
+                                     (16, [1] * 20 + [5])])
+def test_recurrent(dtype, K, V, H, sizes):
+    torch, g = cuda_or_skip()
+    rng, n = np.random.default_rng(len(sizes)), len(sizes)
+    x = tokens(torch, sum(sizes) + H, sum(sizes) + 3, H, K, V, dtype)
+    pool = make_pool(torch, 7, 2 * n + 1, H, K, V)
+    slots = rng.permutation(2 * n + 1).tolist()
+    for src, dst in ((slots[:n], slots[:n]), (slots[:n], slots[n:2 * n])):      # in place, and to other slots
+        p = pool.clone()
+        o, ref, after, rows = run_recurrent(torch, g, x, p, src, dst, sizes, extra=3)
+        close(o[:rows], ref[:rows], dtype)
+        close(p, after, "f32")
+        assert torch.isnan(o[rows:]).all()
+        idle = [s for s in range(2 * n + 1) if s not in dst]
+        assert torch.equal(p[idle], pool[idle])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_recurrent_gathers_clears_moves_and_only_reads(dtype):
+    torch, g = cuda_or_skip()
+    H, K, V = 4, 128, 128
+    x = tokens(torch, 9, 12, H, K, V, dtype, low=0.0)
+    pool = make_pool(torch, 8, 8, H, K, V)
+    #        from zero, moved, cleared, not written, in place, neither read nor written
+    src, dst = [-1, 3, -1, 0, 2, -1], [5, 6, 7, -1, 2, -1]
+    sizes, index = [3, 0, 0, 4, 2, 1], [11, 0, 3, 3, 5, 5, 1, 2, 10, 4]
+    p = pool.clone()
+    o, ref, after, rows = run_recurrent(torch, g, x, p, src, dst, sizes, index)
+    close(o, ref, dtype)
+    close(p, after, "f32")
+    assert torch.equal(p[6], pool[3]) and (p[7] == 0).all() and torch.equal(p[0], pool[0])
+    q = pool.clone()
+    run_recurrent(torch, g, x, q, src, dst, sizes, index, want_o=False)
+    assert torch.equal(p, q)
+
+
+def test_recurrent_is_the_decode_step_and_the_prefill():
+    """Against the framework's own calls: runs of one against gdn2_decode_step, one run against gdn2_chunk_fwd
+    on its fp32 path; the bars are those of the two calls' parity tests, once for each side."""
+    torch, g = cuda_or_skip()
+    B, H = 6, 3
+    x = tokens(torch, 20, B, H, 128, 128, "bf16")
+    pool = make_pool(torch, 21, B, H, 128, 128)
+    S = pool.clone()
+    o = g.recurrent_fwd(*x, pool, i32(torch, range(B)), i32(torch, range(B)), i32(torch, range(B + 1)))
+    ref = g.decode_step(*x, S)
+    close(o, f64(ref), "bf16")
+    close(pool, f64(S), "f32")
+    T = 64
+    x = tokens(torch, 22, T, H, 64, 64, "f32")
+    pool = make_pool(torch, 23, 1, H, 64, 64)
+    ref_o, ref_S = g.chunk_fwd(*(a[None] for a in x), pool.clone())
+    o = g.recurrent_fwd(*x, pool, i32(torch, [0]), i32(torch, [0]), i32(torch, [0, T]))
+    assert np.abs(f64(o) - f64(ref_o)[0]).max() <= 2 * BAR * np.abs(f64(ref_o)).max()
+    assert np.abs(f64(pool) - f64(ref_S)).max() <= 2 * BAR * np.abs(f64(ref_S)).max()
+
+
+def test_recurrent_reports_malformed_indices_and_conflicts():
+    torch, g = cuda_or_skip()
+    H, n = 2, 3
+    x = tokens(torch, 10, 12, H, 64, 128, "f32")
+    pool = make_pool(torch, 11, 8, H, 64, 128)
+    base = dict(src=[0, 1, 2, -1], dst=[0, 4, 5, 6], cu=[0, 3, 6, 9, 12], index=list(range(12)))
+    ref, after = op.recurrent(*(f64(a) for a in x), f64(pool), *(base[k] for k in ("src", "dst", "cu", "index")))
+    cases = (({"src": (1, 8)}, g.DEV_SLOT, [1]), ({"dst": (2, -2)}, g.DEV_SLOT, [2]), ({"dst": (3, 99)}, g.DEV_SLOT, [3]),
+             ({"index": (4, 12)}, g.DEV_INDEX, [1]), ({"index": (9, -1)}, g.DEV_INDEX, [3]),
+             ({"cu": (4, 13)}, g.DEV_RANGE, [3]), ({"cu": (0, -3)}, g.DEV_RANGE, [0]),
+             ({"dst": (1, 5)}, g.DEV_CONFLICT, [1, 2]),          # two writers of one slot: neither writes
+             ({"dst": (3, 2)}, g.DEV_CONFLICT, [3]),             # a writer of a slot that another one reads
+             ({"src": (2, 0)}, g.DEV_CONFLICT, [0]))             # the same, seen from an update in place
+    for change, bit, out in cases:
+        c = {k: list(v) for k, v in base.items()}
+        for key, (at, value) in change.items():
+            c[key][at] = value
+        p, ws = pool.clone(), g.new_workspace(0)
+        o = torch.full((12, H, 128), float("nan"), device="cuda")
+        g.gdn2_recurrent_fwd(*x, p, i32(torch, c["src"]), i32(torch, c["dst"]), i32(torch, c["cu"]), i32(torch, c["index"]), o,
+                             workspace=ws)
+        assert g.gdn2_workspace_status(ws) == bit, change
+        for i in range(4):
+            rows = o[3 * i:3 * i + 3]
+            if i in out:
+                assert torch.isnan(rows).all(), (change, i)
+            elif not ("src" in change and change["src"][0] == i):
+                assert np.abs(f64(rows) - ref[3 * i:3 * i + 3]).max() <= BAR * np.abs(ref).max(), (change, i)
+        written = {c["dst"][i] for i in range(4) if i not in out}
+        idle = [s for s in range(8) if s not in written]
+        assert torch.equal(p[idle], pool[idle]), change
+
+
+@pytest.mark.parametrize("slots,shape,n", [(5, (1, 64, 64), 1), (9, (3, 64, 128), 4), (40, (2, 128, 128), 33),
+                                           (300, (1, 64, 64), 250), (1100, (1, 4), 1024), (2000, (3, 64, 64), 1024)])
+def test_state_copy(slots, shape, n):
+    torch, g = cuda_or_skip()
+    rng = np.random.default_rng(n)
+    pool = torch.randn(slots, *shape, generator=torch.Generator().manual_seed(n)).cuda()
+    perm = rng.permutation(slots)
+    cyc = perm[:n]
+    cases = [("reorder in place", cyc, np.roll(cyc, 1)), ("fork", perm[:n], np.full(n, perm[-1])),
+             ("random, with repeats", rng.integers(-1, slots, n), rng.integers(-1, slots, n)),
+             ("clear", perm[:n], np.full(n, -1)), ("one destination", np.full(n, 2), rng.integers(0, slots, n))]
+    for name, dst, src in cases:
+        p, ws = pool.clone(), g.new_workspace(0)
+        g.gdn2_state_copy(p, p, i32(torch, dst), i32(torch, src), workspace=ws)
+        assert np.array_equal(p.cpu().numpy(), op.state_copy(pool.cpu().numpy(), pool.cpu().numpy(), dst, src)), name
+        assert g.gdn2_workspace_status(ws) == 0
+    other = torch.randn(slots + 3, *shape, device="cuda")
+    keep, dst, src = other.clone(), rng.permutation(slots + 3)[:n], rng.integers(0, slots, n)
+    g.gdn2_state_copy(other, pool, i32(torch, dst), i32(torch, src))
+    assert np.array_equal(other.cpu().numpy(), op.state_copy(keep.cpu().numpy(), pool.cpu().numpy(), dst, src))
+
+
+def test_state_copy_reports_bad_slots_and_serves_the_rest():
+    torch, g = cuda_or_skip()
+    pool = make_pool(torch, 12, 6, 1, 64, 64)
+    p, ws = pool.clone(), g.new_workspace(0)
+    g.gdn2_state_copy(p, p, i32(torch, [0, 6, 1, 2, -2]), i32(torch, [3, 0, 6, 4, 5]), workspace=ws)
+    assert g.gdn2_workspace_status(ws, clear=True) == g.DEV_SLOT and g.gdn2_workspace_status(ws) == 0
+    want = pool.clone()
+    want[0], want[2] = pool[3], pool[4]
+    assert torch.equal(p, want)
+
+
+def test_one_layer_of_a_larger_pool():
+    """Every call on one layer's part of a pool of all layers: the other layers stay as they were."""
+    torch, g = cuda_or_skip()
+    whole = make_pool(torch, 13, 6 * 3, 2, 128, 64).view(6, 3, 2, 128, 64)
+    keep, layer = whole.clone(), whole[:, 1]
+    x = tokens(torch, 14, 5, 2, 128, 64, "f32")
+    par, cu, slots = [-1, 0, 0, 2, 1], [0, 5], [4]
+    o = g.tree_fwd(*x, layer, i32(torch, slots), i32(torch, cu), i32(torch, par), 5)
+    close(o, op.tree(*(f64(a) for a in x), f64(layer), slots, cu, par), "f32")
+    ref, after = op.recurrent(*(f64(a) for a in x), f64(layer), slots, [2], cu)
+    o = g.recurrent_fwd(*x, layer, i32(torch, slots), i32(torch, [2]), i32(torch, cu))
+    close(o, ref, "f32")
+    close(layer, after, "f32")
+    now = layer.clone()
+    g.gdn2_state_copy(layer, layer, i32(torch, [0, 5]), i32(torch, [5, 0]))
+    assert torch.equal(layer[0], now[5]) and torch.equal(layer[5], now[0])
+    assert torch.equal(whole[:, [0, 2]], keep[:, [0, 2]])
+
+
+def test_offsets_past_32_bits():
+    """The last slots of a cache of more than 2^32 floats."""
+    torch, g = cuda_or_skip()
+    H, slots = 16, 16500                      # 262,144 floats a slot: 4.3e9 in all, 17 GB
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of free device memory")
+    pool = torch.zeros(slots, H, 128, 128, device="cuda")
+    last, first = slots - 1, slots - 2
+    pool[last] = make_pool(torch, 15, 1, H, 128, 128)[0]
+    x = tokens(torch, 16, 3, H, 128, 128, "bf16")
+    small = pool[last:].clone()
+    o = g.tree_fwd(*x, pool, i32(torch, [last]), i32(torch, [0, 3]), i32(torch, [-1, 0, 0]), 3)
+    close(o, op.tree(*(f64(a) for a in x), f64(small), [0], [0, 3], [-1, 0, 0]), "bf16")
+    o = g.recurrent_fwd(*x, pool, i32(torch, [last]), i32(torch, [first]), i32(torch, [0, 3]))
+    ref, after = op.recurrent(*(f64(a) for a in x), f64(small), [0], [0], [0, 3])
+    close(o, ref, "bf16")
+    close(pool[first], after[0], "f32")
+    g.gdn2_state_copy(pool, pool, i32(torch, [first - 1]), i32(torch, [first]))
+    assert torch.equal(pool[first - 1], pool[first]) and not pool[:first - 1].any()
+
+
+def test_serving_round_together():
+    """As a server uses them: fork a sequence, draft a tree for each continuation, read the tree out, norm and
+    gate it, take the accepted paths into the cache, and move the survivors together; everything captured in
+    one graph and replayed on new inputs, against the fp64 definitions."""
+    torch, g = cuda_or_skip()
+    H, K, V, n = 4, 128, 128, 12
+    rng = np.random.default_rng(3)
+    pool = make_pool(torch, 30, 8, H, K, V)
+    x = tokens(torch, 31, 2 * n, H, K, V, "bf16")
+    gate = torch.randn(2 * n, H, V, generator=torch.Generator().manual_seed(32)).bfloat16().cuda()
+    weight = torch.ones(V, device="cuda")
+    parents = i32(torch, random_tree(rng, n, 4) + random_tree(rng, n, 4))
+    cu, slots = i32(torch, [0, n, 2 * n]), i32(torch, [6, 7])
+    fork = i32(torch, [6, 7]), i32(torch, [2, 2])
+    path_cu, path = i32(torch, [0, 2, 4]), i32(torch, [0, 0, n, n])
+    pack = i32(torch, [0, 1, 6, 7]), i32(torch, [6, 7, -1, -1])
+    o, y, ws = torch.empty_like(x[2]), torch.empty_like(x[2]), g.new_workspace(0)
+
+    def round_():
+        g.gdn2_state_copy(pool, pool, *fork, workspace=ws)
+        g.gdn2_tree_fwd(*x, pool, slots, cu, parents, o, n, workspace=ws)
+        g.gdn2_gated_norm_fwd(o, gate, weight, y)
+        g.gdn2_recurrent_fwd(*x, pool, slots, slots, path_cu, path, None, workspace=ws)
+        g.gdn2_state_copy(pool, pool, *pack, workspace=ws)
+
+    keep = pool.clone()
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        round_()
+    for seed in (40, 41):
+        pool.copy_(keep)
+        for a, b in zip(x, tokens(torch, seed, 2 * n, H, K, V, "bf16")):
+            a.copy_(b)
+        par = random_tree(rng, n, 3), random_tree(rng, n, 6)
+        parents.copy_(i32(torch, par[0] + par[1]))
+        ends = [int(rng.integers(1, n)), int(rng.integers(1, n))]
+        rows = [[max(0, p[e]), e] for p, e in zip(par, ends)]
+        path.copy_(i32(torch, rows[0] + [n + r for r in rows[1]]))
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = f64(keep)
+        ref[[6, 7]] = ref[2]
+        xs = [f64(a) for a in x]
+        ro = op.tree(*xs, ref, [6, 7], [0, n, 2 * n], par[0] + par[1])
+        close(o, ro, "bf16")
+        ry = op.gated_norm(f64(o), f64(gate), f64(weight))
+        assert (np.abs(f64(y) - ry) <= (2.0 ** -8 + 2.0 ** -17) * np.abs(ry) + 1e-30).all()
+        _, ref = op.recurrent(*xs, ref, [6, 7], [6, 7], [0, 2, 4], path.tolist())
+        close(pool, op.state_copy(ref, ref, [0, 1, 6, 7], [6, 7, -1, -1]), "f32")
+        assert g.gdn2_workspace_status(ws) == 0
