@@ -72,7 +72,15 @@ __device__ __forceinline__ float lane_sum(float x) {
     return x;
 }
 
-__device__ __forceinline__ float sigmoid_(float x) { return 1.f / (1.f + __expf(-x)); }
+// 1 / (1 + 2^(-x log2 e)) on the special-function unit: two instructions there and two beside them, where
+// expf and the divide take some twenty, which bounded the kernels at two thirds of the copy rate.  Each of
+// the two is good to about one unit of fp32 (the argument's rounding adds |x| / 2 more); the ends are exact.
+__device__ __forceinline__ float sigmoid_(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
 
 constexpr int ACT_SILU = 0;
 
@@ -131,19 +139,25 @@ __global__ void __launch_bounds__(256) gated_norm_bwd_kernel(const Tok *__restri
 #pragma unroll
     for (int i = 0; i < N; ++i) dw[i] = 0.f;
     const long long step = (long long)gridDim.x * 8 * RPW;
-    // rows are walked by whole warps: the shuffles below need every lane
-    for (long long r0 = ((long long)blockIdx.x * 8 + warp) * RPW; r0 < rows; r0 += step) {
-        const long long r = r0 + lane / LPR;
-        uint4 xo = make_uint4(0, 0, 0, 0), xg = xo, xy = xo;
+    uint4 xo, xg, xy;   // the next rows are on their way while these are worked on
+    auto fetch = [&](long long r) {
+        xo = xg = xy = make_uint4(0, 0, 0, 0);
         if (r < rows) {
             xo = __ldcs(reinterpret_cast<const uint4 *>(o + r * D) + sub);
             xg = __ldcs(reinterpret_cast<const uint4 *>(gate + r * D) + sub);
             xy = __ldcs(reinterpret_cast<const uint4 *>(dy + r * D) + sub);
         }
+    };
+    // rows are walked by whole warps: the shuffles below need every lane
+    long long r0 = ((long long)blockIdx.x * 8 + warp) * RPW;
+    fetch(r0 + lane / LPR);
+    for (; r0 < rows; r0 += step) {
+        const long long r = r0 + lane / LPR;
         float x[N], g[N], d[N], ss = 0.f, sd = 0.f;
         V::unpack(xo, x);
         V::unpack(xg, g);
         V::unpack(xy, d);
+        fetch(r + step);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const float s = sigmoid_(g[i]);
@@ -287,7 +301,7 @@ __global__ void __launch_bounds__(512) add_norm_fwd_kernel(const Tok *x, const T
 }
 
 template <typename Tok, int NV, bool SCALED>
-__global__ void __launch_bounds__(512) add_norm_bwd_kernel(const Tok *__restrict__ h, const Tok *__restrict__ x,
+__global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) add_norm_bwd_kernel(const Tok *__restrict__ h, const Tok *__restrict__ x,
                                                            const float *__restrict__ scale,
                                                            const float *__restrict__ weight,
                                                            const Tok *__restrict__ dy, const Tok *__restrict__ dh,
@@ -299,17 +313,17 @@ __global__ void __launch_bounds__(512) add_norm_bwd_kernel(const Tok *__restrict
     __shared__ float s_sum[2][MAX_WARPS][2];
     const int width = vecs * N;
     const float inv_width = 1.f / (float)width;
-    float wt[NV][N], sc[NV][N], dw[NV][N], ds[NV][N];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int v = threadIdx.x + j * blockDim.x;
-#pragma unroll
-        for (int i = 0; i < N; ++i) wt[j][i] = sc[j][i] = dw[j][i] = ds[j][i] = 0.f;
-        if (v < vecs) {
-            load_f32<N>(weight + (size_t)v * N, wt[j]);
-            if (SCALED) load_f32<N>(scale + (size_t)v * N, sc[j]);
-        }
+    extern __shared__ __align__(16) float s_weights[];   // weight, then scale: registers go to rows in flight
+    float dw[NV][N], ds[NV][N];
+    for (int c = 4 * threadIdx.x; c < width; c += 4 * blockDim.x) {
+        *reinterpret_cast<float4 *>(s_weights + c) = *reinterpret_cast<const float4 *>(weight + c);
+        if (SCALED) *reinterpret_cast<float4 *>(s_weights + width + c) = *reinterpret_cast<const float4 *>(scale + c);
     }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i) dw[j][i] = ds[j][i] = 0.f;
+    __syncthreads();
     int flip = 0;
     for (long long r = blockIdx.x; r < rows; r += gridDim.x, flip ^= 1) {
         const size_t base = (size_t)r * vecs;
@@ -328,13 +342,15 @@ __global__ void __launch_bounds__(512) add_norm_bwd_kernel(const Tok *__restrict
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            float hf[N], df[N];
+            const int v = threadIdx.x + j * blockDim.x;
+            float hf[N], df[N], wt[N];
             V::unpack(hr[j], hf);
             V::unpack(yr[j], df);
+            load_f32<N>(s_weights + (v < vecs ? v : 0) * N, wt);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 sum[0] = fmaf(hf[i], hf[i], sum[0]);
-                sum[1] = fmaf(df[i] * wt[j][i], hf[i], sum[1]);
+                sum[1] = fmaf(df[i] * wt[i], hf[i], sum[1]);
             }
         }
         block_sum<2>(sum, s_sum[flip]);
@@ -343,23 +359,25 @@ __global__ void __launch_bounds__(512) add_norm_bwd_kernel(const Tok *__restrict
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int v = threadIdx.x + j * blockDim.x;
-            float hf[N], df[N], gf[N];
+            float hf[N], df[N], gf[N], wt[N];
             V::unpack(hr[j], hf);
             V::unpack(yr[j], df);
             V::unpack(gr[j], gf);
+            load_f32<N>(s_weights + (v < vecs ? v : 0) * N, wt);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 dw[j][i] = fmaf(df[i], hf[i] * inv, dw[j][i]);
-                gf[i] += inv * (df[i] * wt[j][i] - hf[i] * mean);
+                gf[i] += inv * (df[i] * wt[i] - hf[i] * mean);
             }
             if (v < vecs) __stcs(reinterpret_cast<uint4 *>(dres) + base + v, V::pack(gf));
             if (SCALED) {
-                float xf[N];
+                float xf[N], sc[N];
                 V::unpack(xr[j], xf);
+                load_f32<N>(s_weights + width + (v < vecs ? v : 0) * N, sc);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     ds[j][i] = fmaf(gf[i], xf[i], ds[j][i]);
-                    gf[i] *= sc[j][i];
+                    gf[i] *= sc[i];
                 }
                 if (v < vecs) __stcs(reinterpret_cast<uint4 *>(dx) + base + v, V::pack(gf));
             }
@@ -381,12 +399,19 @@ __global__ void __launch_bounds__(512) add_norm_bwd_kernel(const Tok *__restrict
     }
 }
 
-// blocks of the backward kernels, each with one row of partial column sums
-int gated_bwd_blocks(long long rows) {
-    const long long want = (rows + 7) / 8;
-    return (int)(want < 148 * 4 ? (want > 0 ? want : 1) : 148 * 4);
+// The backward kernels' blocks walk the rows, each with one row of partial column sums at its end: as many
+// as are resident at once (a second, partial wave of such blocks costs as much as the first), at most
+// MAX_BLOCKS.
+constexpr int SMS = 148, MAX_BLOCKS = 4 * SMS;
+int cap_blocks(long long want, int per_sm) {
+    const long long most = per_sm < 4 ? (per_sm < 1 ? 1 : per_sm) * SMS : MAX_BLOCKS;
+    return (int)(want < most ? (want > 0 ? want : 1) : most);
 }
-int add_bwd_blocks(long long rows) { return (int)(rows < 148 * 4 ? (rows > 0 ? rows : 1) : 148 * 4); }
+template <typename Kernel>
+int resident(Kernel kern, int threads, size_t smem) {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) == cudaSuccess ? n : 1;
+}
 
 // threads of a block that holds a row of `vecs` 16-byte vectors, NV a thread
 int row_threads(int vecs, int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; }
@@ -394,16 +419,22 @@ int row_threads(int vecs, int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32
 template <typename Tok, int D, int ACT>
 int gated_fwd_t(const void *o, const void *gate, const float *weight, void *y, long long rows, float eps,
                 cudaStream_t st) {
-    constexpr int PER_WARP = 32 / (D / V16<Tok>::N), U = 4;
-    const long long per_block = 8 * PER_WARP * U;
-    gated_norm_fwd_kernel<Tok, D, ACT, U><<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, st>>>(
-        (const Tok *)o, (const Tok *)gate, weight, (Tok *)y, rows, eps);
+    constexpr int PER_BLOCK = 8 * 32 / (D / V16<Tok>::N);
+    // four rows a thread in flight hide the latency of a long stream; a few rows are spread over more blocks
+    auto go = [&](auto kern, int u) {
+        const long long per_block = (long long)PER_BLOCK * u;
+        kern<<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, st>>>((const Tok *)o, (const Tok *)gate, weight,
+                                                                           (Tok *)y, rows, eps);
+    };
+    if (rows >= (long long)PER_BLOCK * 4 * SMS * 2) go(gated_norm_fwd_kernel<Tok, D, ACT, 4>, 4);
+    else go(gated_norm_fwd_kernel<Tok, D, ACT, 1>, 1);
     return launch_status();
 }
 template <typename Tok, int D, int ACT>
 int gated_bwd_t(const void *o, const void *gate, const float *weight, const void *dy, void *d_o, void *dgate,
                 float *dweight, long long rows, float eps, float *partial, cudaStream_t st) {
-    const int blocks = gated_bwd_blocks(rows);
+    static const int per_sm = resident(gated_norm_bwd_kernel<Tok, D, ACT>, 256, 0);
+    const int blocks = cap_blocks((rows + 7) / 8, per_sm);
     gated_norm_bwd_kernel<Tok, D, ACT><<<blocks, 256, 0, st>>>((const Tok *)o, (const Tok *)gate, weight,
                                                                (const Tok *)dy, (Tok *)d_o, (Tok *)dgate, partial,
                                                                rows, eps);
@@ -430,14 +461,21 @@ int add_bwd_t(const void *h, const void *x, const float *scale, const float *wei
               void *dres, void *dx, float *dscale, float *dweight, long long rows, int width, float eps,
               float *partial, cudaStream_t st) {
     const int vecs = width / V16<Tok>::N, nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4, nt = row_threads(vecs, nv);
-    const int blocks = add_bwd_blocks(rows), columns = width * (SCALED ? 2 : 1);
+    const int columns = width * (SCALED ? 2 : 1);
+    int blocks = 0;
+    bool ok = false;
     auto go = [&](auto kern) {
-        kern<<<blocks, nt, 0, st>>>((const Tok *)h, (const Tok *)x, scale, weight, (const Tok *)dy, (const Tok *)dh,
+        const size_t smem = sizeof(float) * (size_t)columns;   // up to 64 KB
+        ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+        if (!ok) return;
+        blocks = cap_blocks(rows, resident(kern, nt, smem));
+        kern<<<blocks, nt, smem, st>>>((const Tok *)h, (const Tok *)x, scale, weight, (const Tok *)dy, (const Tok *)dh,
                                     (Tok *)dres, (Tok *)dx, partial, rows, vecs, eps);
     };
     if (nv == 1) go(add_norm_bwd_kernel<Tok, 1, SCALED>);
     else if (nv == 2) go(add_norm_bwd_kernel<Tok, 2, SCALED>);
     else if constexpr (sizeof(Tok) == 4) go(add_norm_bwd_kernel<Tok, 4, SCALED>);   // bf16 rows end at 1024 vectors
+    if (!ok) return -6;
     column_sum_kernel<<<(columns + 31) / 32, 1024, 0, st>>>(partial, blocks, columns, dweight, dscale, width);
     return launch_status();
 }
@@ -445,10 +483,10 @@ int add_bwd_t(const void *h, const void *x, const float *scale, const float *wei
 }  // namespace norms
 
 size_t gated_norm_bwd_workspace_bytes(long long rows, int D) {
-    return kStatusBytes + sizeof(float) * (size_t)norms::gated_bwd_blocks(rows) * D;
+    return kStatusBytes + sizeof(float) * (size_t)norms::cap_blocks((rows + 7) / 8, 4) * D;
 }
 size_t add_norm_bwd_workspace_bytes(long long rows, int width) {
-    return kStatusBytes + sizeof(float) * (size_t)norms::add_bwd_blocks(rows) * width * 2;
+    return kStatusBytes + sizeof(float) * (size_t)norms::cap_blocks(rows, 4) * width * 2;
 }
 
 int launch_gated_norm_fwd(const void *o, const void *gate, const float *weight, void *y, long long rows, int D, int act,

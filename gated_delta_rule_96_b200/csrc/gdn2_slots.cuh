@@ -8,7 +8,8 @@ namespace gdn2 {
 // Bits of a workspace's status word for malformed device-side indices (include/gdn2.h, GDN2_DEV_*): what
 // is wrong is skipped as a whole and reported, nothing is read or written out of range.
 constexpr unsigned DEV_RANGE = 0x100u, DEV_SLOT = 0x200u, DEV_PARENT = 0x400u, DEV_INDEX = 0x800u,
-                   DEV_CONFLICT = 0x1000u;
+                   DEV_CONFLICT = 0x1000u,
+                   DEV_WAIT = 0x2000u;   // a bounded wait ran out
 
 __device__ __forceinline__ float warp_sum32(float x) {
 #pragma unroll

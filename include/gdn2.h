@@ -72,6 +72,7 @@ typedef enum { GDN2_GATE_SILU = 0, GDN2_GATE_SIGMOID = 1 } gdn2_gate;
 #define GDN2_DEV_PARENT 0x400   /* a parent that is not -1 or an earlier node of the same tree   */
 #define GDN2_DEV_INDEX 0x800    /* a token index outside [0, rows)                               */
 #define GDN2_DEV_CONFLICT 0x1000 /* a destination slot that another sequence reads or writes     */
+#define GDN2_DEV_WAIT 0x2000    /* a kernel's bounded wait ran out (an internal error)           */
 
 /* Bytes of device workspace gdn2_chunk_fwd needs for these sizes (0 on bad sizes is
  * never returned: at least the 256-byte status header is always required).
