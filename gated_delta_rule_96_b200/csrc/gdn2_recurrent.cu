@@ -2,162 +2,465 @@
 // Gated DeltaNet-2 ...", section "Техническая схема", the state-update equation).
 //
 // Sequence i owns the tokens cu[i] .. cu[i+1]-1 (through `index`, if given); its state is read from slot
-// slots_in[i] and written to slot slots_out[i].  Per token, S' = Diag(alpha) S:
-//   delta = w v - S'^T (b k),   S <- S' + k delta^T,   o = S^T q = S'^T q + (k.q) delta
+// slots_in[i] and written to slot slots_out[i].  Four tokens at a time in the chunk form, with G_t the product
+// of the block's decays up to t (its own included), e = b k, u = w v:
+//   delta_t = u_t - S^T (e_t G_t) - sum_{i<t} A[t,i] delta_i,   A[t,i] = sum_c e_t (G_t / G_i) k_i
+//   o_t     = S^T (q_t G_t) + sum_{i<=t} P[t,i] delta_i,        P[t,i] = sum_c q_t (G_t / G_i) k_i
+//   S      <- Diag(G_3) S + sum_t (k_t G_3 / G_t) delta_t^T
+// which takes 13 FMA for each element of S where the recurrence takes 16, and one chain of reductions in
+// place of four.  The ratios of G are running products of decays, never quotients, so any decay is exact.
+// Everything is fp32: the states are returned in it and go on to the next call.
 //
-// The columns of S are independent of one another, so a warp owns 16 columns from the first token to the
-// last: lane = (row group rg = lane & 7, column group cg = lane >> 3), rows 4 (rg + 8 j) + i, four columns,
-// which keeps the slice in K/2 registers a lane.  The two d_k-reductions are in-thread over the lane's rows
-// and then over the 8 row groups by halving shuffles; no barrier stands between the tokens.  The tokens are
-// staged through shared memory in fp32, STAGE at a time, in a layout in which a warp's four-row reads touch
-// 128 contiguous bytes.
+// The columns of S are independent of one another: a consumer warp owns 16 of them from the first token to
+// the last, lane = (row group rg = lane >> 2, column group lane & 3), rows 4 (rg + 8 j) + i, four columns, which
+// keeps its slice of the state in K/2 registers a lane.  One CTA an SM walks the (sequence, head, column
+// range) items, and every latency but the arithmetic is another warp's:
+//   scout      reads an item's lengths and slots, checks them, and has a bulk copy bring its state into one of
+//              DEPTH buffers, an item ahead;
+//   producers  turn the tokens into the block's vectors and coefficients, up to RING blocks ahead;
+//   consumers  state to registers, the blocks, state back to the buffer;
+//   storer     has a bulk copy take the buffer to the slot, and frees it once it has been read.
+// A decode step (one token, 128 KB moved for 0.1 MFMA a head) is then bound by HBM: B256 H16 d128 took 166 us
+// with the state loaded to registers by two CTAs an SM that each waited for every latency in turn, and
+// TIME_DECODE here.
 #include "gdn2_internal.h"
 #include "gdn2_slots.cuh"
+#include "tc_ptx.cuh"
 
 namespace gdn2 {
 namespace rec {
 
-constexpr int STAGE = 8;   // tokens staged at a time
+using namespace gdn2::tc;
+
+constexpr int M = 4;           // tokens of a block
+// producer warps: each takes about 2,000 cycles for a block, most of it latency; where the consumers of a
+// whole head take as long for two, two are enough and leave them 168 registers a thread
+template <int K, int V>
+constexpr int PRODUCERS = K == 128 && V == 128 ? 2 : 4;
+constexpr int DEPTH = 2;       // state buffers
+constexpr int RING = 6;        // token blocks ahead
+constexpr uint32_t WAIT_LIMIT = 1u << 26;
 
 template <int K, int V>
-struct Smem {
-    float a[STAGE][K], e[STAGE][K], q[STAGE][K], k[STAGE][K];   // alpha, b k, q, k
-    float u[STAGE][V];                                          // w v
-    float kq[STAGE];
+struct Block {
+    float e[M][K], q[M][K], k[M][K], g[K];   // e G, q G, k G_3 / G, G_3
+    float u[M][V];                           // w v (the columns of this CTA)
+    float coef[16];                          // A10 A20 A21 A30 A31 A32, P00 P10 P11 P20 .. P33
 };
 
-// Grid: (splits, H, batch); a block owns V / splits columns of one (sequence, head), 32 threads for 16 columns.
+// N consecutive token elements, as they are stored and as fp32
+template <typename Tok, int N>
+struct Raw {
+    static constexpr int W = N * (int)sizeof(Tok) / 4;
+    uint32_t r[W];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) r[i] = 0u;
+    }
+    __device__ __forceinline__ void load(const Tok *p) {
+        if constexpr (W == 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
+        } else if constexpr (W == 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            r[0] = v.x; r[1] = v.y;
+        } else {
+            r[0] = *reinterpret_cast<const uint32_t *>(p);
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[N]) const {
+        if constexpr (sizeof(Tok) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) {   // bf16 is the upper half of an fp32
+                x[2 * i] = __uint_as_float(r[i] << 16);
+                x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+            }
+        }
+    }
+};
+template <int CPL>
+__device__ __forceinline__ void store_f32(float *p, const float (&x)[CPL]) {
+    if constexpr (CPL == 4) *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    else *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+}
+
+// A producer warp's work on one block: up to M tokens (the missing ones are neutral: decay 1, the rest 0).
 template <typename Tok, int K, int V>
-__global__ void __launch_bounds__(V * 2) recurrent_kernel(
-    const Tok *__restrict__ q, const Tok *__restrict__ k, const Tok *__restrict__ v, const float *__restrict__ alpha,
-    const Tok *__restrict__ b, const Tok *__restrict__ w, float *S, long long slot_stride, int num_slots,
-    const int *__restrict__ slots_in, const int *__restrict__ slots_out, const int *__restrict__ cu,
-    const int *__restrict__ index, Tok *__restrict__ o, int batch, int H, int total, int rows, unsigned *status) {
-    constexpr int RJ = K / 32;   // groups of four rows a lane
-    __shared__ __align__(16) Smem<K, V> sm;
-    const int nthreads = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int seq = blockIdx.z, head = blockIdx.y;
-    const int col0 = (blockIdx.x * (nthreads >> 5) + warp) * 16, rg = lane & 7, cg = lane >> 3;
-    const int c0 = col0 + cg * 4;
-
-    // what the sequence asks for, checked by every block of it alike: a sequence that is malformed, or whose
-    // destination another sequence names too, is left out
-    const int lo = cu[seq], hi = cu[seq + 1], from = slots_in[seq], to = slots_out[seq];
-    unsigned bad = 0;
-    if (lo < 0 || hi < lo || hi > total) bad = DEV_RANGE;
-    else if (from < -1 || from >= num_slots || to < -1 || to >= num_slots) bad = DEV_SLOT;
-    else {
-        if (to >= 0)
-            for (int i = tid; i < batch; i += nthreads)
-                if (i != seq && (slots_out[i] == to || slots_in[i] == to)) bad |= DEV_CONFLICT;
-        if (index)
-            for (int t = lo + tid; t < hi; t += nthreads)
-                if (index[t] < 0 || index[t] >= rows) bad |= DEV_INDEX;
+__device__ __forceinline__ void produce(Block<K, V> &out, const Tok *q, const Tok *k, const Tok *v, const float *alpha,
+                                        const Tok *b, const Tok *w, const int *index, int t0, int n, int H, int head,
+                                        int col0, int cols, int lane) {
+    constexpr int CPL = K / 32;
+    float a[M][CPL];
+    Raw<Tok, CPL> rk[M], rb[M], rq[M];   // kept as stored until a token's turn: registers
+#pragma unroll
+    for (int t = 0; t < M; ++t) {
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) a[t][c] = 1.f;
+        rk[t].clear();
+        rb[t].clear();
+        rq[t].clear();
+        if (t < n) {
+            const size_t row = (size_t)(index ? index[t0 + t] : t0 + t) * H + head;
+            Raw<float, CPL> ra;
+            ra.load(alpha + row * K + lane * CPL);
+            ra.get(a[t]);
+            rk[t].load(k + row * K + lane * CPL);
+            rb[t].load(b + row * K + lane * CPL);
+            rq[t].load(q + row * K + lane * CPL);
+            if (lane * 4 < cols) {
+                Raw<Tok, 4> rv, rw;
+                float vv[4], ww[4];
+                rv.load(v + row * V + col0 + lane * 4);
+                rw.load(w + row * V + col0 + lane * 4);
+                rv.get(vv);
+                rw.get(ww);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) vv[c] *= ww[c];
+                store_f32<4>(&out.u[t][lane * 4], vv);
+            }
+        } else if (lane * 4 < cols) {
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+            store_f32<4>(&out.u[t][lane * 4], zero);
+        }
     }
-    if (__syncthreads_or(bad != 0)) {
-        if (bad) atomicOr(status, bad);
-        return;
+    float x[16];
+#pragma unroll
+    for (int t = 0; t < M; ++t) {   // from t back to the block's first token with a running product of decays
+        const int A0 = t * (t - 1) / 2, P0 = 6 + t * (t + 1) / 2;
+        float e[CPL], qq[CPL], kk[CPL];
+        rk[t].get(kk);
+        rb[t].get(e);
+        rq[t].get(qq);
+        x[P0 + t] = 0.f;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            x[P0 + t] = fmaf(qq[c], kk[c], x[P0 + t]);
+            e[c] *= kk[c] * a[t][c];
+            qq[c] *= a[t][c];
+        }
+#pragma unroll
+        for (int i = t - 1; i >= 0; --i) {
+            rk[i].get(kk);
+            x[A0 + i] = x[P0 + i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                x[A0 + i] = fmaf(e[c], kk[c], x[A0 + i]);
+                x[P0 + i] = fmaf(qq[c], kk[c], x[P0 + i]);
+                e[c] *= a[i][c];
+                qq[c] *= a[i][c];
+            }
+        }
+        store_f32<CPL>(&out.e[t][lane * CPL], e);
+        store_f32<CPL>(&out.q[t][lane * CPL], qq);
     }
+    float g[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) g[c] = 1.f;
+#pragma unroll
+    for (int t = M - 1; t >= 0; --t) {
+        float kk[CPL];
+        rk[t].get(kk);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) kk[c] *= g[c], g[c] *= a[t][c];
+        store_f32<CPL>(&out.k[t][lane * CPL], kk);
+    }
+    store_f32<CPL>(&out.g[lane * CPL], g);
+    // sums of the sixteen values over the lanes: each step halves the values a lane carries
+#pragma unroll
+    for (int h = 8, m = 16; h > 0; h /= 2, m /= 2) {
+        const bool up = lane & m;
+#pragma unroll
+        for (int i = 0; i < h; ++i)
+            x[i] = (up ? x[i + h] : x[i]) + __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + h], m);
+    }
+    x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
+    if (!(lane & 1)) out.coef[lane >> 1] = x[0];
+}
 
-    const size_t state = (size_t)head * K * V;
-    float s[RJ][4][4];
+// Sums over the 8 row groups of N tokens x 4 columns (x[4 t + c]): on return x[t] is the total of token t at
+// the lane's column lane >> 3 of its four.
+template <int N>
+__device__ __forceinline__ void column_sums(float (&x)[4 * N], int lane) {
+    const bool hi = lane & 16, lo = lane & 8;
 #pragma unroll
-    for (int j = 0; j < RJ; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (from >= 0)
-                x = ld_stream(reinterpret_cast<const float4 *>(S + (size_t)from * slot_stride + state +
-                                                               (size_t)(4 * (rg + 8 * j) + i) * V + c0));
-            s[j][i][0] = x.x; s[j][i][1] = x.y; s[j][i][2] = x.z; s[j][i][3] = x.w;
-        }
+    for (int t = 0; t < N; ++t) {
+        const float a = (hi ? x[4 * t + 2] : x[4 * t]) + __shfl_xor_sync(0xffffffffu, hi ? x[4 * t] : x[4 * t + 2], 16);
+        const float b = (hi ? x[4 * t + 3] : x[4 * t + 1]) + __shfl_xor_sync(0xffffffffu, hi ? x[4 * t + 1] : x[4 * t + 3], 16);
+        const float s = (lo ? b : a) + __shfl_xor_sync(0xffffffffu, lo ? a : b, 8);
+        x[t] = s + __shfl_xor_sync(0xffffffffu, s, 4);
+    }
+}
 
-    for (int t0 = lo; t0 < hi; t0 += STAGE) {
-        const int n = min(STAGE, hi - t0);
-        __syncthreads();
-        for (int i = tid; i < n * K; i += nthreads) {
-            const int t = i / K, c = i % K;
-            const size_t at = ((size_t)(index ? index[t0 + t] : t0 + t) * H + head) * K + c;
-            const float kk = ld_tok(k + at);
-            sm.a[t][c] = alpha[at];
-            sm.e[t][c] = ld_tok(b + at) * kk;
-            sm.q[t][c] = ld_tok(q + at);
-            sm.k[t][c] = kk;
-        }
-        for (int i = tid; i < n * V; i += nthreads) {
-            const int t = i / V, c = i % V;
-            const size_t at = ((size_t)(index ? index[t0 + t] : t0 + t) * H + head) * V + c;
-            sm.u[t][c] = ld_tok(w + at) * ld_tok(v + at);
-        }
-        __syncthreads();
-        for (int t = warp; t < n; t += nthreads >> 5) {
-            float d = 0.f;
+// A consumer warp's step over the first n of a block's tokens, as N >= n tokens (the others are neutral).
+template <typename Tok, int K, int V, int N>
+__device__ __forceinline__ void consume(const Block<K, V> &in, float (&s)[K / 32][4][4], Tok *o, int t0, int n, int H,
+                                        int head, int col0, int local, int lane) {
+    constexpr int RJ = K / 32, HALF = N > 1 ? 2 : 1;   // two tokens at a time: registers
+    const int rg = lane >> 2, mine = local + (lane & 3) * 4 + (lane >> 3);   // the lane's column, within the CTA's
+    auto dots = [&](const float (&vec)[M][K], float (&out)[N]) {   // S^T vec_t at the lane's column
 #pragma unroll
-            for (int c = lane; c < K; c += 32) d = fmaf(sm.k[t][c], sm.q[t][c], d);
-            d = warp_sum32(d);
-            if (lane == 0) sm.kq[t] = d;
+        for (int h = 0; h < N; h += HALF) {
+            float p[4 * HALF];
+#pragma unroll
+            for (int i = 0; i < 4 * HALF; ++i) p[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < RJ; ++j)
+#pragma unroll
+                for (int t = 0; t < HALF; ++t) {
+                    const float4 x4 = *reinterpret_cast<const float4 *>(&vec[h + t][4 * (rg + 8 * j)]);
+                    const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) p[4 * t + c] = fmaf(x[i], s[j][i][c], p[4 * t + c]);
+                }
+            column_sums<HALF>(p, lane);
+#pragma unroll
+            for (int t = 0; t < HALF; ++t) out[h + t] = p[t];
         }
-        __syncthreads();
-        for (int t = 0; t < n; ++t) {
-            float p[8];   // sums over the lane's rows: S'^T e of its four columns, S'^T q of them
+    };
+    float p[N], d[N];
+    dots(in.e, p);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) p[c] = 0.f;
+    for (int t = 0; t < N; ++t) {
+        d[t] = in.u[t][mine] - p[t];
 #pragma unroll
-            for (int j = 0; j < RJ; ++j) {
-                const float4 a4 = *reinterpret_cast<const float4 *>(&sm.a[t][4 * (rg + 8 * j)]);
-                const float4 e4 = *reinterpret_cast<const float4 *>(&sm.e[t][4 * (rg + 8 * j)]);
-                const float4 q4 = *reinterpret_cast<const float4 *>(&sm.q[t][4 * (rg + 8 * j)]);
-                const float aa[4] = {a4.x, a4.y, a4.z, a4.w}, ee[4] = {e4.x, e4.y, e4.z, e4.w},
-                            qq[4] = {q4.x, q4.y, q4.z, q4.w};
+        for (int i = 0; i < t; ++i) d[t] = fmaf(-in.coef[t * (t - 1) / 2 + i], d[i], d[t]);
+    }
+    if (o) {
+        dots(in.q, p);
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+#pragma unroll
+            for (int i = 0; i <= t; ++i) p[t] = fmaf(in.coef[6 + t * (t + 1) / 2 + i], d[i], p[t]);
+            if (t < n && (t & 1) == (rg & 1)) store_tok(o + ((size_t)(t0 + t) * H + head) * V + col0 + mine, p[t]);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < N; h += HALF) {
+        float dd[HALF][4];
+#pragma unroll
+        for (int t = 0; t < HALF; ++t)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) dd[t][c] = __shfl_sync(0xffffffffu, d[h + t], (lane & 3) | (8 * c));
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) {
+            if (h == 0) {
+                const float4 g4 = *reinterpret_cast<const float4 *>(&in.g[4 * (rg + 8 * j)]);
+                const float g[4] = {g4.x, g4.y, g4.z, g4.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        s[j][i][c] *= aa[i];
-                        p[c] = fmaf(ee[i], s[j][i][c], p[c]);
-                        p[4 + c] = fmaf(qq[i], s[j][i][c], p[4 + c]);
-                    }
-            }
-            const float sum = scatter_sum8(p, lane);
-            // lanes rg = 0..3 hold r of column c0 + rg: delta of that column, to the whole column group
-            const float mine = sm.u[t][c0 + (rg & 3)] - sum;
-            float d[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) d[c] = __shfl_sync(0xffffffffu, mine, (lane & 24) | c);
-            if (o && rg >= 4) {
-                const float dc = rg == 4 ? d[0] : rg == 5 ? d[1] : rg == 6 ? d[2] : d[3];
-                store_tok(o + ((size_t)(t0 + t) * H + head) * V + c0 + rg - 4, fmaf(sm.kq[t], dc, sum));
+                    for (int c = 0; c < 4; ++c) s[j][i][c] *= g[i];
             }
 #pragma unroll
-            for (int j = 0; j < RJ; ++j) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(&sm.k[t][4 * (rg + 8 * j)]);
+            for (int t = 0; t < HALF; ++t) {
+                const float4 k4 = *reinterpret_cast<const float4 *>(&in.k[h + t][4 * (rg + 8 * j)]);
                 const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[j][i][c] = fmaf(kk[i], d[c], s[j][i][c]);
+                    for (int c = 0; c < 4; ++c) s[j][i][c] = fmaf(kk[i], dd[t][c], s[j][i][c]);
             }
         }
     }
-    if (to < 0 || (to == from && lo == hi)) return;
+}
+
+// An item as the scout found it; a malformed one, and one with nothing to do, has n = 0, from = to = -1.
+struct Item {
+    int lo, n, from, to;
+};
+
+template <int K, int V>
+struct Shared {
+    Block<K, V> ring[RING];
+    Item item[DEPTH];
+    // item: known; state: landed; done: consumers finished; free: storer and producers finished with it
+    unsigned long long known[DEPTH], landed[DEPTH], done[DEPTH], free[DEPTH], full[RING], empty[RING];
+};
+
+template <int K, int V>
+constexpr size_t smem_bytes(int cols) { return sizeof(Shared<K, V>) + sizeof(float) * (size_t)DEPTH * K * cols; }
+
+// warps: consumers (16 columns each), PRODUCERS, scout, storer
+template <int K, int V>
+constexpr int EXTRA_WARPS = PRODUCERS<K, V> + 2;
+
+template <typename Tok, int K, int V>
+__global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kernel(
+    const Tok *__restrict__ q, const Tok *__restrict__ k, const Tok *__restrict__ v, const float *__restrict__ alpha,
+    const Tok *__restrict__ b, const Tok *__restrict__ w, float *S, long long slot_stride, int num_slots,
+    const int *__restrict__ slots_in, const int *__restrict__ slots_out, const int *__restrict__ cu,
+    const int *__restrict__ index, Tok *__restrict__ o, int batch, int H, int splits, int total, int rows,
+    unsigned *status) {
+    constexpr int RJ = K / 32, NP = PRODUCERS<K, V>;
+    extern __shared__ __align__(128) unsigned char raw[];
+    Shared<K, V> &sh = *reinterpret_cast<Shared<K, V> *>(raw);
+    float *buffers = reinterpret_cast<float *>(raw + sizeof(Shared<K, V>));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cols = V / splits, consumers = cols / 16;
+    const long long items = (long long)batch * H * splits;
+    auto bar = [&](unsigned long long &x) { return smem_u32(&x); };
+
+    if (tid == 0) {
+        for (int d = 0; d < DEPTH; ++d) {
+            mbar_init(bar(sh.known[d]), 1);
+            mbar_init(bar(sh.landed[d]), 1);
+            mbar_init(bar(sh.done[d]), consumers);
+            mbar_init(bar(sh.free[d]), 1 + NP);
+        }
+        for (int r = 0; r < RING; ++r) {
+            mbar_init(bar(sh.full[r]), 1);
+            mbar_init(bar(sh.empty[r]), consumers);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+
+    bool ok = true;   // every wait is bounded; a warp whose wait ran out reports it and leaves
+    auto wait = [&](unsigned long long &x, int phase) { return ok = ok && mbar_wait(bar(x), phase & 1, WAIT_LIMIT); };
+    int g = 0;        // token blocks so far
+    int it = 0;
+    for (long long at = blockIdx.x; at < items && ok; at += gridDim.x, ++it) {
+        const int d = it % DEPTH, turn = it / DEPTH;
+        const int split = (int)(at % splits), head = (int)(at / splits % H), seq = (int)(at / splits / H);
+        const int col0 = split * cols;
+        const size_t state = (size_t)head * K * V + col0;
+        float *buffer = buffers + (size_t)d * K * cols;
+
+        if (warp == consumers + NP) {   // scout
+            Item x = {cu[seq], 0, slots_in[seq], slots_out[seq]};
+            const int hi = cu[seq + 1];
+            unsigned bad = 0;
+            if (x.lo < 0 || hi < x.lo || hi > total) bad = DEV_RANGE;
+            else if (x.from < -1 || x.from >= num_slots || x.to < -1 || x.to >= num_slots) bad = DEV_SLOT;
+            else {
+                if (x.to >= 0)
+#pragma unroll 4
+                    for (int i = lane; i < batch; i += 32)
+                        if (i != seq && (slots_out[i] == x.to || slots_in[i] == x.to)) bad |= DEV_CONFLICT;
+                if (index)
+#pragma unroll 4
+                    for (int t = x.lo + lane; t < hi; t += 32)
+                        if (index[t] < 0 || index[t] >= rows) bad |= DEV_INDEX;
+            }
+            bad = __reduce_or_sync(0xffffffffu, bad);
+            x.n = hi - x.lo;
+            if (bad && lane == 0) atomicOr(status, bad);
+            if (bad || (x.n == 0 && x.from == x.to)) x = {0, 0, -1, -1};
+            if (!wait(sh.free[d], turn + 1)) break;
+            if (lane == 0) {
+                sh.item[d] = x;
+                mbar_arrive(bar(sh.known[d]));
+                mbar_arrive_expect_tx(bar(sh.landed[d]), x.from >= 0 ? (uint32_t)(4 * K * cols) : 0u);
+            }
+            __syncwarp();
+            if (x.from >= 0) {
+                const float *src = S + (size_t)x.from * slot_stride + state;
+                if (cols == V) {
+                    if (lane == 0) bulk_g2s(smem_u32(buffer), src, 4 * K * V, bar(sh.landed[d]));
+                } else {
+                    for (int r = lane; r < K; r += 32)
+                        bulk_g2s(smem_u32(buffer + r * cols), src + (size_t)r * V, 4 * cols, bar(sh.landed[d]));
+                }
+            }
+            continue;
+        }
+        if (!wait(sh.known[d], turn)) break;
+        const Item x = sh.item[d];
+        const int blocks = (x.n + M - 1) / M;
+        if (warp == consumers + NP + 1) {   // storer
+            if (!wait(sh.done[d], turn)) break;
+            if (x.to >= 0) {
+                float *dst = S + (size_t)x.to * slot_stride + state;
+                if (cols == V) {
+                    if (lane == 0) bulk_s2g(dst, smem_u32(buffer), 4 * K * V);
+                } else {
+                    for (int r = lane; r < K; r += 32)
+                        bulk_s2g(dst + (size_t)r * V, smem_u32(buffer + r * cols), 4 * cols);
+                }
+                bulk_commit();
+                bulk_wait_read_all();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sh.free[d]));
+        } else if (warp >= consumers) {            // producers
+            for (int i = 0; i < blocks; ++i, ++g) {
+                if (g % NP != warp - consumers) continue;
+                if (!wait(sh.empty[g % RING], g / RING + 1)) break;
+                produce<Tok, K, V>(sh.ring[g % RING], q, k, v, alpha, b, w, index, x.lo + i * M, min(M, x.n - i * M), H,
+                                   head, col0, cols, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sh.full[g % RING]));
+            }
+            if (lane == 0) mbar_arrive(bar(sh.free[d]));
+        } else {                                   // consumers
+            float s[RJ][4][4];
+            float *mine = buffer + warp * 16 + (lane & 3) * 4;
+            const int rg = lane >> 2;
+            if (!wait(sh.landed[d], turn)) break;
 #pragma unroll
-    for (int j = 0; j < RJ; ++j)
+            for (int j = 0; j < RJ; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            st_stream(reinterpret_cast<float4 *>(S + (size_t)to * slot_stride + state +
-                                                 (size_t)(4 * (rg + 8 * j) + i) * V + c0),
-                      make_float4(s[j][i][0], s[j][i][1], s[j][i][2], s[j][i][3]));
+                for (int i = 0; i < 4; ++i) {
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (x.from >= 0) y = *reinterpret_cast<const float4 *>(mine + (4 * (rg + 8 * j) + i) * cols);
+                    s[j][i][0] = y.x; s[j][i][1] = y.y; s[j][i][2] = y.z; s[j][i][3] = y.w;
+                }
+#pragma unroll 1
+            for (int i = 0; i < blocks; ++i, ++g) {
+                if (!wait(sh.full[g % RING], g / RING)) break;
+                const int t0 = x.lo + i * M, n = x.n - i * M;
+                const Block<K, V> &in = sh.ring[g % RING];
+                if (n >= 3) consume<Tok, K, V, M>(in, s, o, t0, n, H, head, col0, warp * 16, lane);
+                else if (n == 2) consume<Tok, K, V, 2>(in, s, o, t0, n, H, head, col0, warp * 16, lane);
+                else consume<Tok, K, V, 1>(in, s, o, t0, n, H, head, col0, warp * 16, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sh.empty[g % RING]));
+            }
+            if (x.to >= 0) {
+#pragma unroll
+                for (int j = 0; j < RJ; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<float4 *>(mine + (4 * (rg + 8 * j) + i) * cols) =
+                            make_float4(s[j][i][0], s[j][i][1], s[j][i][2], s[j][i][3]);
+                fence_async_smem();   // the storer's bulk copy reads it
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(sh.done[d]));
+        }
+    }
+    if (!ok && lane == 0) atomicOr(status, DEV_WAIT);
+    if (!ok && warp == consumers + NP)   // no copy may still be on its way into this CTA's memory
+        for (int d = 0; d < DEPTH; ++d) mbar_wait(bar(sh.landed[d]), (it / DEPTH) & 1, WAIT_LIMIT);
 }
 
 template <typename Tok, int K, int V>
 int launch_t(const void *q, const void *k, const void *v, const float *alpha, const void *b, const void *w, float *S,
              long long slot_stride, int num_slots, const int *slots_in, const int *slots_out, const int *cu,
              const int *index, void *o, int batch, int H, int total, int rows, unsigned *status, cudaStream_t st) {
+    constexpr size_t most = smem_bytes<K, V>(V);
+    static const int per_sm = [] {
+        int n = 0;
+        if (cudaFuncSetAttribute(recurrent_kernel<Tok, K, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) !=
+                cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, recurrent_kernel<Tok, K, V>, 2 * V + 32 * EXTRA_WARPS<K, V>,
+                                                          most) != cudaSuccess)
+            return 0;
+        return n;
+    }();
+    if (per_sm < 1) return -6;
+    // few chains: their columns over more SMs
     int splits = 1;
-    while (splits < V / 16 && (long long)batch * H * splits * 2 <= 148 * 2) splits *= 2;
-    recurrent_kernel<Tok, K, V><<<dim3(splits, H, batch), V * 2 / splits, 0, st>>>(
+    while (splits < V / 16 && (long long)batch * H * splits * 2 <= 148) splits *= 2;
+    const long long items = (long long)batch * H * splits, grid = items < 148 * per_sm ? items : 148 * per_sm;
+    recurrent_kernel<Tok, K, V><<<(unsigned)grid, V * 2 / splits + 32 * EXTRA_WARPS<K, V>, smem_bytes<K, V>(V / splits), st>>>(
         (const Tok *)q, (const Tok *)k, (const Tok *)v, alpha, (const Tok *)b, (const Tok *)w, S, slot_stride,
-        num_slots, slots_in, slots_out, cu, index, (Tok *)o, batch, H, total, rows, status);
+        num_slots, slots_in, slots_out, cu, index, (Tok *)o, batch, H, splits, total, rows, status);
     return launch_status();
 }
 
