@@ -20,6 +20,7 @@
 //   producers  turn the tokens into the block's vectors and coefficients, up to RING blocks ahead;
 //   consumers  state to registers, the blocks, state back to the buffer;
 //   storer     has a bulk copy take the buffer to the slot, and frees it once it has been read.
+// Where a head's columns are split over CTAs (few chains), the consumers move their own part of the state.
 // A decode step (one token, 128 KB moved for 0.1 MFMA a head) is then bound by HBM: B256 H16 d128 took 166 us
 // with the state loaded to registers by two CTAs an SM that each waited for every latency in turn, and
 // TIME_DECODE here.
@@ -33,11 +34,11 @@ namespace rec {
 using namespace gdn2::tc;
 
 constexpr int M = 4;           // tokens of a block
-// producer warps: each takes about 2,000 cycles for a block, most of it latency; where the consumers of a
-// whole head take as long for two, two are enough and leave them 168 registers a thread
+// producer warps: each takes about 4,000 cycles for a block, most of it latency; where the consumers of a
+// whole head take longer for two, two are enough and leave them 168 registers a thread
 template <int K, int V>
 constexpr int PRODUCERS = K == 128 && V == 128 ? 2 : 4;
-constexpr int DEPTH = 2;       // state buffers
+constexpr int DEPTH = 2;       // state buffers: one worked on, one on its way in or out
 constexpr int RING = 6;        // token blocks ahead
 constexpr uint32_t WAIT_LIMIT = 1u << 26;
 
@@ -93,38 +94,44 @@ __device__ __forceinline__ void produce(Block<K, V> &out, const Tok *q, const To
                                         const Tok *b, const Tok *w, const int *index, int t0, int n, int H, int head,
                                         int col0, int cols, int lane) {
     constexpr int CPL = K / 32;
-    float a[M][CPL];
+    // every load before the first store: one latency for the block
+    Raw<float, CPL> ra[M];
     Raw<Tok, CPL> rk[M], rb[M], rq[M];   // kept as stored until a token's turn: registers
+    Raw<Tok, 4> rv[M], rw[M];
+    int token[M];
+#pragma unroll
+    for (int t = 0; t < M; ++t) token[t] = t < n ? (index ? index[t0 + t] : t0 + t) : -1;
 #pragma unroll
     for (int t = 0; t < M; ++t) {
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) a[t][c] = 1.f;
         rk[t].clear();
         rb[t].clear();
         rq[t].clear();
+        rv[t].clear();
+        rw[t].clear();
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) ra[t].r[c] = __float_as_uint(1.f);
         if (t < n) {
-            const size_t row = (size_t)(index ? index[t0 + t] : t0 + t) * H + head;
-            Raw<float, CPL> ra;
-            ra.load(alpha + row * K + lane * CPL);
-            ra.get(a[t]);
+            const size_t row = (size_t)token[t] * H + head;
+            ra[t].load(alpha + row * K + lane * CPL);
             rk[t].load(k + row * K + lane * CPL);
             rb[t].load(b + row * K + lane * CPL);
             rq[t].load(q + row * K + lane * CPL);
             if (lane * 4 < cols) {
-                Raw<Tok, 4> rv, rw;
-                float vv[4], ww[4];
-                rv.load(v + row * V + col0 + lane * 4);
-                rw.load(w + row * V + col0 + lane * 4);
-                rv.get(vv);
-                rw.get(ww);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) vv[c] *= ww[c];
-                store_f32<4>(&out.u[t][lane * 4], vv);
+                rv[t].load(v + row * V + col0 + lane * 4);
+                rw[t].load(w + row * V + col0 + lane * 4);
             }
-        } else if (lane * 4 < cols) {
-            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-            store_f32<4>(&out.u[t][lane * 4], zero);
         }
+    }
+    float a[M][CPL];
+#pragma unroll
+    for (int t = 0; t < M; ++t) {
+        ra[t].get(a[t]);
+        float vv[4], ww[4];
+        rv[t].get(vv);
+        rw[t].get(ww);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) vv[c] *= ww[c];
+        if (lane * 4 < cols) store_f32<4>(&out.u[t][lane * 4], vv);
     }
     float x[16];
 #pragma unroll
@@ -195,21 +202,24 @@ __device__ __forceinline__ void column_sums(float (&x)[4 * N], int lane) {
 }
 
 // A consumer warp's step over the first n of a block's tokens, as N >= n tokens (the others are neutral).
-template <typename Tok, int K, int V, int N>
+// Straight-line code (whether o is wanted is known to the compiler): the products with q fill the latency of
+// the sums over the lanes and of the substitution.
+template <typename Tok, int K, int V, int N, bool OUT>
 __device__ __forceinline__ void consume(const Block<K, V> &in, float (&s)[K / 32][4][4], Tok *o, int t0, int n, int H,
                                         int head, int col0, int local, int lane) {
-    constexpr int RJ = K / 32, HALF = N > 1 ? 2 : 1;   // two tokens at a time: registers
+    constexpr int RJ = K / 32, GROUP = K == 64 || N == 1 ? N : 2;   // tokens at a time: registers
     const int rg = lane >> 2, mine = local + (lane & 3) * 4 + (lane >> 3);   // the lane's column, within the CTA's
-    auto dots = [&](const float (&vec)[M][K], float (&out)[N]) {   // S^T vec_t at the lane's column
+    float e[N], q[N], d[N];   // S^T (e G), S^T (q G) of the lane's column
+    auto products = [&](const float (&vec)[M][K], float (&out)[N]) {
 #pragma unroll
-        for (int h = 0; h < N; h += HALF) {
-            float p[4 * HALF];
+        for (int h = 0; h < N; h += GROUP) {
+            float p[4 * GROUP];
 #pragma unroll
-            for (int i = 0; i < 4 * HALF; ++i) p[i] = 0.f;
+            for (int i = 0; i < 4 * GROUP; ++i) p[i] = 0.f;
 #pragma unroll
             for (int j = 0; j < RJ; ++j)
 #pragma unroll
-                for (int t = 0; t < HALF; ++t) {
+                for (int t = 0; t < GROUP; ++t) {
                     const float4 x4 = *reinterpret_cast<const float4 *>(&vec[h + t][4 * (rg + 8 * j)]);
                     const float x[4] = {x4.x, x4.y, x4.z, x4.w};
 #pragma unroll
@@ -217,54 +227,50 @@ __device__ __forceinline__ void consume(const Block<K, V> &in, float (&s)[K / 32
 #pragma unroll
                         for (int c = 0; c < 4; ++c) p[4 * t + c] = fmaf(x[i], s[j][i][c], p[4 * t + c]);
                 }
-            column_sums<HALF>(p, lane);
+            column_sums<GROUP>(p, lane);
 #pragma unroll
-            for (int t = 0; t < HALF; ++t) out[h + t] = p[t];
+            for (int t = 0; t < GROUP; ++t) out[h + t] = p[t];
         }
     };
-    float p[N], d[N];
-    dots(in.e, p);
+    products(in.e, e);
+    if constexpr (OUT) products(in.q, q);
 #pragma unroll
     for (int t = 0; t < N; ++t) {
-        d[t] = in.u[t][mine] - p[t];
+        d[t] = in.u[t][mine] - e[t];
 #pragma unroll
         for (int i = 0; i < t; ++i) d[t] = fmaf(-in.coef[t * (t - 1) / 2 + i], d[i], d[t]);
     }
-    if (o) {
-        dots(in.q, p);
+    asm volatile("" ::: "memory");   // the loads below stay below: registers
+#pragma unroll
+    for (int j = 0; j < RJ; ++j) {
+        const float4 g4 = *reinterpret_cast<const float4 *>(&in.g[4 * (rg + 8 * j)]);
+        const float g[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[j][i][c] *= g[i];
+    }
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        float dd[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) dd[c] = __shfl_sync(0xffffffffu, d[t], (lane & 3) | (8 * c));
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) {
+            const float4 k4 = *reinterpret_cast<const float4 *>(&in.k[t][4 * (rg + 8 * j)]);
+            const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[j][i][c] = fmaf(kk[i], dd[c], s[j][i][c]);
+        }
+    }
+    if constexpr (OUT) {
 #pragma unroll
         for (int t = 0; t < N; ++t) {
 #pragma unroll
-            for (int i = 0; i <= t; ++i) p[t] = fmaf(in.coef[6 + t * (t + 1) / 2 + i], d[i], p[t]);
-            if (t < n && (t & 1) == (rg & 1)) store_tok(o + ((size_t)(t0 + t) * H + head) * V + col0 + mine, p[t]);
-        }
-    }
-#pragma unroll
-    for (int h = 0; h < N; h += HALF) {
-        float dd[HALF][4];
-#pragma unroll
-        for (int t = 0; t < HALF; ++t)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) dd[t][c] = __shfl_sync(0xffffffffu, d[h + t], (lane & 3) | (8 * c));
-#pragma unroll
-        for (int j = 0; j < RJ; ++j) {
-            if (h == 0) {
-                const float4 g4 = *reinterpret_cast<const float4 *>(&in.g[4 * (rg + 8 * j)]);
-                const float g[4] = {g4.x, g4.y, g4.z, g4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) s[j][i][c] *= g[i];
-            }
-#pragma unroll
-            for (int t = 0; t < HALF; ++t) {
-                const float4 k4 = *reinterpret_cast<const float4 *>(&in.k[h + t][4 * (rg + 8 * j)]);
-                const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) s[j][i][c] = fmaf(kk[i], dd[t][c], s[j][i][c]);
-            }
+            for (int i = 0; i <= t; ++i) q[t] = fmaf(in.coef[6 + t * (t + 1) / 2 + i], d[i], q[t]);
+            if (t < n && (t & 1) == (rg & 1)) store_tok(o + ((size_t)(t0 + t) * H + head) * V + col0 + mine, q[t]);
         }
     }
 }
@@ -278,18 +284,18 @@ template <int K, int V>
 struct Shared {
     Block<K, V> ring[RING];
     Item item[DEPTH];
-    // item: known; state: landed; done: consumers finished; free: storer and producers finished with it
-    unsigned long long known[DEPTH], landed[DEPTH], done[DEPTH], free[DEPTH], full[RING], empty[RING];
+    // item: known; state: landed; done: consumers finished; read: producers and storer finished with it
+    unsigned long long known[DEPTH], landed[DEPTH], done[DEPTH], read[DEPTH], full[RING], empty[RING];
 };
 
 template <int K, int V>
-constexpr size_t smem_bytes(int cols) { return sizeof(Shared<K, V>) + sizeof(float) * (size_t)DEPTH * K * cols; }
+constexpr size_t smem_bytes(int cols) { return sizeof(Shared<K, V>) + (cols < V ? 0 : sizeof(float) * (size_t)DEPTH * K * V); }
 
 // warps: consumers (16 columns each), PRODUCERS, scout, storer
 template <int K, int V>
 constexpr int EXTRA_WARPS = PRODUCERS<K, V> + 2;
 
-template <typename Tok, int K, int V>
+template <typename Tok, int K, int V, bool OUT>
 __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kernel(
     const Tok *__restrict__ q, const Tok *__restrict__ k, const Tok *__restrict__ v, const float *__restrict__ alpha,
     const Tok *__restrict__ b, const Tok *__restrict__ w, float *S, long long slot_stride, int num_slots,
@@ -302,6 +308,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
     float *buffers = reinterpret_cast<float *>(raw + sizeof(Shared<K, V>));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cols = V / splits, consumers = cols / 16;
+    const bool whole = splits == 1;
     const long long items = (long long)batch * H * splits;
     auto bar = [&](unsigned long long &x) { return smem_u32(&x); };
 
@@ -310,7 +317,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
             mbar_init(bar(sh.known[d]), 1);
             mbar_init(bar(sh.landed[d]), 1);
             mbar_init(bar(sh.done[d]), consumers);
-            mbar_init(bar(sh.free[d]), 1 + NP);
+            mbar_init(bar(sh.read[d]), NP + 1);
         }
         for (int r = 0; r < RING; ++r) {
             mbar_init(bar(sh.full[r]), 1);
@@ -322,18 +329,15 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
 
     bool ok = true;   // every wait is bounded; a warp whose wait ran out reports it and leaves
     auto wait = [&](unsigned long long &x, int phase) { return ok = ok && mbar_wait(bar(x), phase & 1, WAIT_LIMIT); };
-    int g = 0;        // token blocks so far
-    int it = 0;
-    for (long long at = blockIdx.x; at < items && ok; at += gridDim.x, ++it) {
-        const int d = it % DEPTH, turn = it / DEPTH;
-        const int split = (int)(at % splits), head = (int)(at / splits % H), seq = (int)(at / splits / H);
-        const int col0 = split * cols;
-        const size_t state = (size_t)head * K * V + col0;
-        float *buffer = buffers + (size_t)d * K * cols;
+    auto state_of = [&](long long at, int slot) {   // the item's part of a slot
+        const int split = (int)(at % splits), head = (int)(at / splits % H);
+        return S + (size_t)slot * slot_stride + (size_t)head * K * V + split * cols;
+    };
 
-        if (warp == consumers + NP) {   // scout
+    if (warp == consumers + NP) {   // scout
+        auto look = [&](long long at) {
+            const int seq = (int)(at / splits / H), hi = cu[seq + 1];
             Item x = {cu[seq], 0, slots_in[seq], slots_out[seq]};
-            const int hi = cu[seq + 1];
             unsigned bad = 0;
             if (x.lo < 0 || hi < x.lo || hi > total) bad = DEV_RANGE;
             else if (x.from < -1 || x.from >= num_slots || x.to < -1 || x.to >= num_slots) bad = DEV_SLOT;
@@ -351,105 +355,114 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
             x.n = hi - x.lo;
             if (bad && lane == 0) atomicOr(status, bad);
             if (bad || (x.n == 0 && x.from == x.to)) x = {0, 0, -1, -1};
-            if (!wait(sh.free[d], turn + 1)) break;
+            return x;
+        };
+        for (int it = 0;; ++it) {
+            const long long at = blockIdx.x + (long long)it * gridDim.x;
+            if (at >= items) break;
+            const int d = it % DEPTH;
+            const Item x = look(at);
+            // the storer is done with the buffer, the producers with the words of the item that was there
+            if (!wait(sh.read[d], it / DEPTH + 1)) break;
             if (lane == 0) {
                 sh.item[d] = x;
                 mbar_arrive(bar(sh.known[d]));
-                mbar_arrive_expect_tx(bar(sh.landed[d]), x.from >= 0 ? (uint32_t)(4 * K * cols) : 0u);
-            }
-            __syncwarp();
-            if (x.from >= 0) {
-                const float *src = S + (size_t)x.from * slot_stride + state;
-                if (cols == V) {
-                    if (lane == 0) bulk_g2s(smem_u32(buffer), src, 4 * K * V, bar(sh.landed[d]));
-                } else {
-                    for (int r = lane; r < K; r += 32)
-                        bulk_g2s(smem_u32(buffer + r * cols), src + (size_t)r * V, 4 * cols, bar(sh.landed[d]));
+                if (whole) {
+                    mbar_arrive_expect_tx(bar(sh.landed[d]), x.from >= 0 ? (uint32_t)(4 * K * V) : 0u);
+                    if (x.from >= 0)
+                        bulk_g2s(smem_u32(buffers + (size_t)d * K * V), state_of(at, x.from), 4 * K * V, bar(sh.landed[d]));
                 }
             }
-            continue;
         }
-        if (!wait(sh.known[d], turn)) break;
-        const Item x = sh.item[d];
-        const int blocks = (x.n + M - 1) / M;
-        if (warp == consumers + NP + 1) {   // storer
-            if (!wait(sh.done[d], turn)) break;
-            if (x.to >= 0) {
-                float *dst = S + (size_t)x.to * slot_stride + state;
-                if (cols == V) {
-                    if (lane == 0) bulk_s2g(dst, smem_u32(buffer), 4 * K * V);
-                } else {
-                    for (int r = lane; r < K; r += 32)
-                        bulk_s2g(dst + (size_t)r * V, smem_u32(buffer + r * cols), 4 * cols);
+    } else {
+        int g = 0;        // token blocks so far
+        int it = 0;
+        for (long long at = blockIdx.x; at < items && ok; at += gridDim.x, ++it) {
+            const int d = it % DEPTH, turn = it / DEPTH;
+            const int split = (int)(at % splits), head = (int)(at / splits % H), col0 = split * cols;
+            if (!wait(sh.known[d], turn)) break;
+            const Item x = sh.item[d];
+            const int blocks = (x.n + M - 1) / M;
+            if (warp >= consumers && warp < consumers + NP) {   // producers
+                for (int i = 0; i < blocks; ++i, ++g) {
+                    if (g % NP != warp - consumers) continue;
+                    if (!wait(sh.empty[g % RING], g / RING + 1)) break;
+                    produce<Tok, K, V>(sh.ring[g % RING], q, k, v, alpha, b, w, index, x.lo + i * M,
+                                       min(M, x.n - i * M), H, head, col0, cols, lane);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(sh.full[g % RING]));
                 }
-                bulk_commit();
-                bulk_wait_read_all();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(sh.free[d]));
-        } else if (warp >= consumers) {            // producers
-            for (int i = 0; i < blocks; ++i, ++g) {
-                if (g % NP != warp - consumers) continue;
-                if (!wait(sh.empty[g % RING], g / RING + 1)) break;
-                produce<Tok, K, V>(sh.ring[g % RING], q, k, v, alpha, b, w, index, x.lo + i * M, min(M, x.n - i * M), H,
-                                   head, col0, cols, lane);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sh.full[g % RING]));
-            }
-            if (lane == 0) mbar_arrive(bar(sh.free[d]));
-        } else {                                   // consumers
-            float s[RJ][4][4];
-            float *mine = buffer + warp * 16 + (lane & 3) * 4;
-            const int rg = lane >> 2;
-            if (!wait(sh.landed[d], turn)) break;
-#pragma unroll
-            for (int j = 0; j < RJ; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (x.from >= 0) y = *reinterpret_cast<const float4 *>(mine + (4 * (rg + 8 * j) + i) * cols);
-                    s[j][i][0] = y.x; s[j][i][1] = y.y; s[j][i][2] = y.z; s[j][i][3] = y.w;
+                if (lane == 0) mbar_arrive(bar(sh.read[d]));
+            } else if (warp > consumers + NP) { // storer
+                if (!wait(sh.done[d], turn)) break;
+                if (lane == 0) {
+                    if (x.to >= 0 && whole) bulk_s2g(state_of(at, x.to), smem_u32(buffers + (size_t)d * K * V), 4 * K * V);
+                    bulk_commit();
+                    bulk_wait_read_all();
+                    mbar_arrive(bar(sh.read[d]));
                 }
-#pragma unroll 1
-            for (int i = 0; i < blocks; ++i, ++g) {
-                if (!wait(sh.full[g % RING], g / RING)) break;
-                const int t0 = x.lo + i * M, n = x.n - i * M;
-                const Block<K, V> &in = sh.ring[g % RING];
-                if (n >= 3) consume<Tok, K, V, M>(in, s, o, t0, n, H, head, col0, warp * 16, lane);
-                else if (n == 2) consume<Tok, K, V, 2>(in, s, o, t0, n, H, head, col0, warp * 16, lane);
-                else consume<Tok, K, V, 1>(in, s, o, t0, n, H, head, col0, warp * 16, lane);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sh.empty[g % RING]));
-            }
-            if (x.to >= 0) {
+            } else {                            // consumers
+                float s[RJ][4][4];
+                const int rg = lane >> 2, pitch = V;
+                const size_t part = warp * 16 + (lane & 3) * 4 + (size_t)(4 * rg) * pitch;
+                float *buffer = buffers + (size_t)d * K * V + part;
+                if (whole && !wait(sh.landed[d], turn)) break;
 #pragma unroll
                 for (int j = 0; j < RJ; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<float4 *>(mine + (4 * (rg + 8 * j) + i) * cols) =
-                            make_float4(s[j][i][0], s[j][i][1], s[j][i][2], s[j][i][3]);
-                fence_async_smem();   // the storer's bulk copy reads it
+                    for (int i = 0; i < 4; ++i) {
+                        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (x.from >= 0) {
+                            if (whole) y = *reinterpret_cast<const float4 *>(buffer + (32 * j + i) * pitch);
+                            else y = ld_stream(reinterpret_cast<const float4 *>(state_of(at, x.from) + part + (32 * j + i) * pitch));
+                        }
+                        s[j][i][0] = y.x; s[j][i][1] = y.y; s[j][i][2] = y.z; s[j][i][3] = y.w;
+                    }
+#pragma unroll 1
+                for (int i = 0; i < blocks; ++i, ++g) {
+                    if (!wait(sh.full[g % RING], g / RING)) break;
+                    const int t0 = x.lo + i * M, n = x.n - i * M;
+                    const Block<K, V> &in = sh.ring[g % RING];
+                    if (n >= 3) consume<Tok, K, V, M, OUT>(in, s, o, t0, n, H, head, col0, warp * 16, lane);
+                    else if (n == 2) consume<Tok, K, V, 2, OUT>(in, s, o, t0, n, H, head, col0, warp * 16, lane);
+                    else consume<Tok, K, V, 1, OUT>(in, s, o, t0, n, H, head, col0, warp * 16, lane);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(sh.empty[g % RING]));
+                }
+                if (x.to >= 0 && ok) {
+#pragma unroll
+                    for (int j = 0; j < RJ; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 y = make_float4(s[j][i][0], s[j][i][1], s[j][i][2], s[j][i][3]);
+                            if (whole) *reinterpret_cast<float4 *>(buffer + (32 * j + i) * pitch) = y;
+                            else st_stream(reinterpret_cast<float4 *>(state_of(at, x.to) + part + (32 * j + i) * pitch), y);
+                        }
+                    fence_async_smem();   // the storer's bulk copy reads it
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(sh.done[d]));
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(sh.done[d]));
         }
     }
-    if (!ok && lane == 0) atomicOr(status, DEV_WAIT);
-    if (!ok && warp == consumers + NP)   // no copy may still be on its way into this CTA's memory
-        for (int d = 0; d < DEPTH; ++d) mbar_wait(bar(sh.landed[d]), (it / DEPTH) & 1, WAIT_LIMIT);
+    if (!ok) {   // reported; no copy may still be on its way into this CTA's memory when it ends
+        if (lane == 0) atomicOr(status, DEV_WAIT);
+        for (int d = 0; d < DEPTH; ++d) mbar_wait(bar(sh.landed[d]), 0, WAIT_LIMIT);
+    }
 }
 
-template <typename Tok, int K, int V>
-int launch_t(const void *q, const void *k, const void *v, const float *alpha, const void *b, const void *w, float *S,
-             long long slot_stride, int num_slots, const int *slots_in, const int *slots_out, const int *cu,
-             const int *index, void *o, int batch, int H, int total, int rows, unsigned *status, cudaStream_t st) {
+template <typename Tok, int K, int V, bool OUT>
+int launch_out(const void *q, const void *k, const void *v, const float *alpha, const void *b, const void *w, float *S,
+               long long slot_stride, int num_slots, const int *slots_in, const int *slots_out, const int *cu,
+               const int *index, void *o, int batch, int H, int total, int rows, unsigned *status, cudaStream_t st) {
     constexpr size_t most = smem_bytes<K, V>(V);
+    constexpr int threads = 2 * V + 32 * EXTRA_WARPS<K, V>;
     static const int per_sm = [] {
         int n = 0;
-        if (cudaFuncSetAttribute(recurrent_kernel<Tok, K, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) !=
-                cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, recurrent_kernel<Tok, K, V>, 2 * V + 32 * EXTRA_WARPS<K, V>,
-                                                          most) != cudaSuccess)
+        const auto kern = recurrent_kernel<Tok, K, V, OUT>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, most) != cudaSuccess)
             return 0;
         return n;
     }();
@@ -458,10 +471,20 @@ int launch_t(const void *q, const void *k, const void *v, const float *alpha, co
     int splits = 1;
     while (splits < V / 16 && (long long)batch * H * splits * 2 <= 148) splits *= 2;
     const long long items = (long long)batch * H * splits, grid = items < 148 * per_sm ? items : 148 * per_sm;
-    recurrent_kernel<Tok, K, V><<<(unsigned)grid, V * 2 / splits + 32 * EXTRA_WARPS<K, V>, smem_bytes<K, V>(V / splits), st>>>(
+    recurrent_kernel<Tok, K, V, OUT><<<(unsigned)grid, 2 * V / splits + 32 * EXTRA_WARPS<K, V>,
+                                       smem_bytes<K, V>(V / splits), st>>>(
         (const Tok *)q, (const Tok *)k, (const Tok *)v, alpha, (const Tok *)b, (const Tok *)w, S, slot_stride,
         num_slots, slots_in, slots_out, cu, index, (Tok *)o, batch, H, splits, total, rows, status);
     return launch_status();
+}
+
+template <typename Tok, int K, int V>
+int launch_t(const void *q, const void *k, const void *v, const float *alpha, const void *b, const void *w, float *S,
+             long long slot_stride, int num_slots, const int *slots_in, const int *slots_out, const int *cu,
+             const int *index, void *o, int batch, int H, int total, int rows, unsigned *status, cudaStream_t st) {
+    return (o ? launch_out<Tok, K, V, true> : launch_out<Tok, K, V, false>)(q, k, v, alpha, b, w, S, slot_stride, num_slots,
+                                                                         slots_in, slots_out, cu, index, o, batch, H,
+                                                                         total, rows, status, st);
 }
 
 }  // namespace rec
