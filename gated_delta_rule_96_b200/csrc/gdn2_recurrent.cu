@@ -49,39 +49,6 @@ struct Block {
     float coef[16];                          // A10 A20 A21 A30 A31 A32, P00 P10 P11 P20 .. P33
 };
 
-// N consecutive token elements, as they are stored and as fp32
-template <typename Tok, int N>
-struct Raw {
-    static constexpr int W = N * (int)sizeof(Tok) / 4;
-    uint32_t r[W];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < W; ++i) r[i] = 0u;
-    }
-    __device__ __forceinline__ void load(const Tok *p) {
-        if constexpr (W == 4) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p);
-            r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
-        } else if constexpr (W == 2) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(p);
-            r[0] = v.x; r[1] = v.y;
-        } else {
-            r[0] = *reinterpret_cast<const uint32_t *>(p);
-        }
-    }
-    __device__ __forceinline__ void get(float (&x)[N]) const {
-        if constexpr (sizeof(Tok) == 4) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < W; ++i) {   // bf16 is the upper half of an fp32
-                x[2 * i] = __uint_as_float(r[i] << 16);
-                x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
-            }
-        }
-    }
-};
 template <int CPL>
 __device__ __forceinline__ void store_f32(float *p, const float (&x)[CPL]) {
     if constexpr (CPL == 4) *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);

@@ -11,24 +11,52 @@ constexpr unsigned DEV_RANGE = 0x100u, DEV_SLOT = 0x200u, DEV_PARENT = 0x400u, D
                    DEV_CONFLICT = 0x1000u,
                    DEV_WAIT = 0x2000u;   // a bounded wait ran out
 
-__device__ __forceinline__ float warp_sum32(float x) {
+// N consecutive token elements, as they are stored and as fp32
+template <typename Tok, int N>
+struct Raw {
+    static constexpr int W = N * (int)sizeof(Tok) / 4;
+    uint32_t r[W];
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-    return x;
-}
+        for (int i = 0; i < W; ++i) r[i] = 0u;
+    }
+    __device__ __forceinline__ void load(const Tok *p) {   // N * sizeof(Tok) <= 16 bytes, aligned to them
+        if constexpr (W == 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
+        } else if constexpr (W == 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            r[0] = v.x; r[1] = v.y;
+        } else {
+            r[0] = *reinterpret_cast<const uint32_t *>(p);
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[N]) const {
+        if constexpr (sizeof(Tok) == 4) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) {   // bf16 is the upper half of an fp32
+                x[2 * i] = __uint_as_float(r[i] << 16);
+                x[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+            }
+        }
+    }
+};
 
-// Sums of eight values over the 8 lanes of a row group (lane & 7): on return lane j holds the total of
-// x[j].  Each step halves the values a lane still carries, 7 shuffles instead of 24.
+// Sums of eight values over the 8 row groups (lane >> 2, the column groups on the low bits): on return row
+// group j holds the total of x[j].  Each step halves the values a lane still carries, 7 shuffles instead of 24.
 __device__ __forceinline__ float scatter_sum8(const float (&x)[8], int lane) {
     float a[4], b[2];
-    const bool up4 = lane & 4, up2 = lane & 2, up1 = lane & 1;
+    const bool up4 = lane & 16, up2 = lane & 8, up1 = lane & 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        a[i] = (up4 ? x[i + 4] : x[i]) + __shfl_xor_sync(0xffffffffu, up4 ? x[i] : x[i + 4], 4);
+        a[i] = (up4 ? x[i + 4] : x[i]) + __shfl_xor_sync(0xffffffffu, up4 ? x[i] : x[i + 4], 16);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        b[i] = (up2 ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up2 ? a[i] : a[i + 2], 2);
-    return (up1 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up1 ? b[0] : b[1], 1);
+        b[i] = (up2 ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up2 ? a[i] : a[i + 2], 8);
+    return (up1 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up1 ? b[0] : b[1], 4);
 }
 
 }  // namespace gdn2
