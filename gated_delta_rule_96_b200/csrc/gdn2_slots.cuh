@@ -45,6 +45,41 @@ struct Raw {
     }
 };
 
+// Two fp32 in one register pair: half the issue slots of the scalar form at the same rate of the FMA pipe
+// (measured 71 against 67 TFLOP/s), for kernels that the issue slots bound.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// four consecutive floats as two pairs
+__device__ __forceinline__ void load2(const float *p, f32x2 (&x)[2]) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p);
+    x[0] = v.x;
+    x[1] = v.y;
+}
+
 // Sums of eight values over the 8 row groups (lane >> 2, the column groups on the low bits): on return row
 // group j holds the total of x[j].  Each step halves the values a lane still carries, 7 shuffles instead of 24.
 __device__ __forceinline__ float scatter_sum8(const float (&x)[8], int lane) {

@@ -9,14 +9,15 @@
 //   o_n     = S^T (q_n G_n) + sum over ancestors i and n itself of P[n,i] delta_i,   P[n,i] = sum_c q_n (G_n / G_i) k_i
 // G_n / G_i is the product of the decays below i down to n, so walking from n to its root with a running
 // product gives A, P, e_n G_n and q_n G_n without a division, a logarithm or a masked entry: decays of any
-// size (zero included) are exact, and what sits on another branch is never touched.
+// size (zero included) are exact, and what sits on another branch is never touched.  The deltas are then
+// eliminated (eliminate()), which leaves o_n as a sum over n's path alone.
 #include "gdn2_tree.cuh"
 
 namespace gdn2 {
 namespace tree {
 
 // The kernel on CUDA cores, any type and size.  One block per (column range, head, sequence); the first
-// cols / 16 warps own 16 columns of the state each, every warp takes part in the walk.
+// cols / 16 warps own 16 columns of the state each, every warp takes part in the rest.
 template <typename Tok, int K, int V>
 __global__ void __launch_bounds__(256) tree_kernel(const Tok *__restrict__ q, const Tok *__restrict__ k,
                                                    const Tok *__restrict__ v, const float *__restrict__ alpha,
@@ -31,9 +32,10 @@ __global__ void __launch_bounds__(256) tree_kernel(const Tok *__restrict__ q, co
     const int head = blockIdx.x / splits, col0 = blockIdx.x % splits * cols, seq = blockIdx.y;
     float *sk = smem, *sa = sk + max_nodes * K, *se = sa + max_nodes * K, *sq = se + max_nodes * K;
     float *sr = sq + max_nodes * K, *ss = sr + max_nodes * cols;
-    float2 *ap = reinterpret_cast<float2 *>(ss + max_nodes * cols);
-    int *sp = reinterpret_cast<int *>(ap + pairs(max_nodes));
-    unsigned char *anc = reinterpret_cast<unsigned char *>(sp + max_nodes), *depth = anc + pairs(max_nodes);
+    float *cA = ss + max_nodes * cols, *cP = cA + pairs(max_nodes);
+    int *sp = reinterpret_cast<int *>(cP + pairs(max_nodes));
+    unsigned short *where = reinterpret_cast<unsigned short *>(sp + max_nodes);
+    unsigned char *anc = reinterpret_cast<unsigned char *>(where + pairs(max_nodes)), *depth = anc + pairs(max_nodes);
 
     const int lo = cu[seq], hi = cu[seq + 1], slot = slots[seq];
     unsigned bad = 0;
@@ -89,26 +91,27 @@ __global__ void __launch_bounds__(256) tree_kernel(const Tok *__restrict__ q, co
         rw.get(y);
         *reinterpret_cast<float4 *>(sr + 4 * i) = make_float4(x[0] * y[0], x[1] * y[1], x[2] * y[2], x[3] * y[3]);
     }
-    if (tid < n) {
-        int above = 0;
-        for (int i = sp[tid]; i >= 0; i = sp[i]) ++above;
-        depth[tid] = (unsigned char)above;
+    __syncthreads();
+    for (int n0 = warp * 4; n0 < n; n0 += nt / 8) {
+        const int node = n0 + (lane >> 3);
+        f32x2 e[RJ][2], g[RJ][2];
+        Rows<Tok, K> rows;
+        rows.load(b, q, lo, H, head, node, n, lane);
+        const int above = walk<Tok, K>(rows, sk, sa, sp, cA, cP, anc, where, node, n, lane, e, g);
+        if (node < n) {
+            if ((lane & 7) == 0) depth[node] = (unsigned char)above;
+#pragma unroll
+            for (int j = 0; j < RJ; ++j) {
+                *reinterpret_cast<ulonglong2 *>(se + node * K + 4 * ((lane & 7) + 8 * j)) = make_ulonglong2(e[j][0], e[j][1]);
+                *reinterpret_cast<ulonglong2 *>(sq + node * K + 4 * ((lane & 7) + 8 * j)) = make_ulonglong2(g[j][0], g[j][1]);
+            }
+        }
     }
     __syncthreads();
     for (int n0 = warp * 4; n0 < n; n0 += nt / 8) {
         const int node = n0 + (lane >> 3);
-        float e[RJ][4], g[RJ][4];
-        walk<Tok, K>(k, b, q, sk, sa, sp, ap, anc, lo, H, head, node, n, lane, e, g);
-        if (node < n)
-#pragma unroll
-            for (int j = 0; j < RJ; ++j) {
-                *reinterpret_cast<float4 *>(se + node * K + 4 * ((lane & 7) + 8 * j)) =
-                    make_float4(e[j][0], e[j][1], e[j][2], e[j][3]);
-                *reinterpret_cast<float4 *>(sq + node * K + 4 * ((lane & 7) + 8 * j)) =
-                    make_float4(g[j][0], g[j][1], g[j][2], g[j][3]);
-            }
+        eliminate(cA, cP, where, cP, node, n, node < n ? depth[node] : 0, lane);
     }
-    __syncthreads();
 
     // S^T (e G) and S^T (q G) of every node
     if (owner)
@@ -137,31 +140,19 @@ __global__ void __launch_bounds__(256) tree_kernel(const Tok *__restrict__ q, co
         }
     __syncthreads();
 
-    // delta and o, node by node (a parent comes before its children), a column a thread
-    if (tid < cols) {
-        const size_t first = ((size_t)lo * H + head) * V + col0 + tid;
-        for (int t = 0; t < n; ++t) {
-            float d = sr[t * cols + tid], x = ss[t * cols + tid];
-            const int base = pairs(t), above = depth[t];   // ancestors
-            for (int j = 1; j <= above; j += 4) {
-                float2 c[4];
-                float di[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {   // past the root: the root again, with zero coefficients
-                    const int at = base + min(j + i, above);
-                    c[i] = ap[at];
-                    if (j + i > above) c[i] = make_float2(0.f, 0.f);
-                    di[i] = sr[anc[at] * cols + tid];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    d = fmaf(-c[i].x, di[i], d);
-                    x = fmaf(c[i].y, di[i], x);
-                }
-            }
-            sr[t * cols + tid] = d;
-            store_tok(o + first + (size_t)t * H * V, fmaf(ap[base].y, d, x));
+    // o: four columns a thread, the nodes in turn over the block
+    const size_t first = ((size_t)lo * H + head) * V + col0;
+    for (int i = tid; i < n * (cols / 4); i += nt) {
+        const int node = i / (cols / 4), col = i % (cols / 4) * 4, base = pairs(node), above = depth[node];
+        float4 x = *reinterpret_cast<const float4 *>(ss + 4 * i);
+#pragma unroll 4
+        for (int j = 0; j <= above; ++j) {
+            const float c = cP[base + j];
+            const float4 r = *reinterpret_cast<const float4 *>(sr + anc[base + j] * cols + col);
+            x.x = fmaf(c, r.x, x.x); x.y = fmaf(c, r.y, x.y); x.z = fmaf(c, r.z, x.z); x.w = fmaf(c, r.w, x.w);
         }
+        Tok *out = o + first + (size_t)node * H * V + col;
+        store_tok(out, x.x); store_tok(out + 1, x.y); store_tok(out + 2, x.z); store_tok(out + 3, x.w);
     }
 }
 
@@ -170,7 +161,7 @@ int launch_t(const void *q, const void *k, const void *v, const float *alpha, co
              const float *S, long long slot_stride, int num_slots, const int *slots, const int *cu, const int *parents,
              void *o, int batch, int H, int total, int max_nodes, unsigned *status, cudaStream_t st) {
     const auto smem = [&](int n, int cols) {
-        return sizeof(float) * (size_t)n * (4 * K + 2 * cols) + (sizeof(float2) + 1) * (size_t)pairs(n) +
+        return sizeof(float) * (size_t)n * (4 * K + 2 * cols) + (2 * sizeof(float) + sizeof(short) + 1) * (size_t)pairs(n) +
                (sizeof(int) + 1) * (size_t)n;
     };
     static const bool ok = cudaFuncSetAttribute(tree_kernel<Tok, K, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -6,15 +6,14 @@
 // for the state and the tokens from five nodes on.  Both factors are split into two bf16, x = hi + lo (16
 // significant bits, relative error 2^-17): three tcgen05 products hi hi + hi lo + lo hi keep the error far
 // below the rounding of the bf16 output, where one product of bf16 operands would double that rounding.
-//   state group  (4 warps)  S from HBM to registers, a column a thread, split, into tensor memory: the A
+//   state group  (8 warps)  S from HBM to registers, half a column a thread, split, into tensor memory: the A
 //                           operand S^T, lane = value column, two buffers
-//   walk group   (8 warps)  eight lanes a node up to its root: the coefficients A and P to shared memory, the
-//                           rows e G and q G, split, into the B operand's swizzled images
-//   column group (8 warps)  u - S^T (e G) and S^T (q G) from tensor memory (lane = value column) to shared
-//                           memory, then delta and o level by level of the tree, a column a thread, the two
-//                           warpgroups taking the nodes of a level in turn
-//   lead warp               reads and checks the items, orders their nodes by level, brings the tokens'
-//                           lines into L2 ahead of the groups, and issues the products
+//   walk group   (8 warps)  eight lanes a node up to its root, then the elimination: the coefficients to shared
+//                           memory, and the rows e G and q G, split, into the B operand's swizzled images
+//   column group (8 warps)  R = u - S^T (e G) and S^T (q G) from tensor memory (lane = value column) to shared
+//                           memory, then o = S^T (q G) + C R, a node a warp and four columns a lane
+//   lead warp               reads and checks the items, brings the tokens' lines into L2 ahead of the groups,
+//                           and issues the products
 #include "gdn2_tree.cuh"
 #include "tc_ptx.cuh"
 
@@ -24,29 +23,30 @@ namespace tree {
 using namespace gdn2::tc;
 
 constexpr int D = 128;
-constexpr int COLUMN_WARPS = 8, STATE_WARPS = 4, WALK_WARPS = 8;   // in this order; then the lead warp
+constexpr int COLUMN_WARPS = 8, STATE_WARPS = 8, WALK_WARPS = 8;   // in this order; then the lead warp
 constexpr int LEAD = COLUMN_WARPS + STATE_WARPS + WALK_WARPS, TC_THREADS = 32 * (LEAD + 1);
 constexpr int METAS = 4;
-constexpr uint32_t BAR_COLUMN = 1, BAR_WALK = 2, WAIT_LIMIT = 1u << 24;
+constexpr uint32_t BAR_COLUMN = 1, BAR_WALK = 2, BAR_STATE = 3, WAIT_LIMIT = 1u << 24;
 constexpr uint32_t TM_S = 0, TM_D = 256, TM_COLS = 512;   // S: two buffers of hi (64 columns) and lo (64)
 
-// An item: its nodes lo .. lo+n-1, the state's slot, parents and depths, the nodes ordered by level.
+// An item: its nodes lo .. lo+n-1, their parents, the state's slot.
 struct Meta {
-    int lo, n, slot, head, levels;
-    unsigned char depth[MAX_NODES], order[MAX_NODES], start[MAX_NODES + 1];
+    int lo, n, slot, head;
     signed char parent[MAX_NODES];
 };
 
-struct Coef {
-    float2 ap[MAX_NODES * (MAX_NODES + 1) / 2];       // {A, P}, as walk() lays them out
-    unsigned char anc[MAX_NODES * (MAX_NODES + 1) / 2];   // the ancestor of each
+struct Coef {   // eliminate()'s, whom each is for, and how many ancestors a node has
+    float c[MAX_PAIRS];
+    unsigned char anc[MAX_PAIRS], above[MAX_NODES];
 };
 
 struct TcShared {
     unsigned char b_hi[2 * MAX_NODES * D * 2], b_lo[2 * MAX_NODES * D * 2];   // [e G; q G], swizzled
     __nv_bfloat16 k[MAX_NODES][D];
     float alpha[MAX_NODES][D];
-    float delta[MAX_NODES][D], out[MAX_NODES][D];     // by node and value column
+    float r[MAX_NODES][D], x[MAX_NODES][D];   // u, then R; S^T (q G); by node and value column
+    float a[MAX_PAIRS];
+    unsigned short where[MAX_PAIRS];
     Coef coef[2];
     Meta meta[METAS];
     unsigned long long meta_full[METAS], meta_free[METAS], s_full[2], s_free[2], coef_full[2], coef_free[2], b_full,
@@ -103,15 +103,16 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
     const uint32_t tmem = sh.tmem;
 
     // Every wait is bounded, and every thread of a group gets the same verdict, so that none is left at one of
-    // the group's barriers.  Phases count the items that have nodes (c); the others only pass their meta on.
+    // the group's barriers.  One warp of a group polls, the others sleep at the barrier.  Phases count the items
+    // that have nodes (c); the others only pass their meta on.
     const auto wait = [&](unsigned long long &x, int phase) {
         const bool ok = mbar_wait(bar(x), phase & 1, WAIT_LIMIT) && !*abort;
         if (!ok) *abort = 1u;
         return ok;
     };
     const auto group_wait = [&](unsigned long long &x, int phase, uint32_t id) {
-        const bool ok = !group_or(id, 256, !(mbar_wait(bar(x), phase & 1, WAIT_LIMIT) && !*abort));
-        if (!ok) *abort = 1u;
+        const bool polls = (warp & 7) == 0, ok = !group_or(id, 256, polls && !wait(x, phase));
+        fence_after();
         return ok;
     };
     const auto warp_wait = [&](unsigned long long &x, int phase) { return !__any_sync(0xffffffffu, !wait(x, phase)); };
@@ -138,39 +139,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                 if (lane == 0) atomicOr(status, bad);
                 n = 0;
             }
-            __syncwarp();
-            for (int i = lane; i < n; i += 32) {
-                int depth = 0;
-                for (int p = m.parent[i]; p >= 0; p = m.parent[p]) ++depth;
-                m.depth[i] = (unsigned char)depth;
-            }
-            __syncwarp();
-            int deepest = 0;
-            for (int i = lane; i < n; i += 32) {
-                const int mine = m.depth[i];
-                int rank = 0, above = 0;   // nodes before this one in the order, nodes of the levels above
-                for (int j = 0; j < n; ++j) {
-                    const int other = m.depth[j];
-                    above += other < mine;
-                    rank += other == mine && j < i;
-                }
-                m.order[above + rank] = (unsigned char)i;
-                if (rank == 0) m.start[mine] = (unsigned char)above;   // every level has one first node
-                deepest = max(deepest, mine);
-            }
-            deepest = __reduce_max_sync(0xffffffffu, deepest);
-            if (lane == 0) {
-                m.lo = lo, m.n = n, m.slot = slot, m.head = head, m.levels = deepest + 1;
-                if (n > 0) m.start[deepest + 1] = (unsigned char)n;
-            }
-            for (int i = lane; i < n; i += 32) {
-                const size_t row = ((size_t)(lo + i) * H + head) * D;
-                bulk_prefetch_l2(k + row, 2 * D);
-                bulk_prefetch_l2(alpha + row, 4 * D);
-                bulk_prefetch_l2(b + row, 2 * D);
-                bulk_prefetch_l2(q + row, 2 * D);
-                bulk_prefetch_l2(v + row, 2 * D);
-                bulk_prefetch_l2(w + row, 2 * D);
+            if (lane == 0) m.lo = lo, m.n = n, m.slot = slot, m.head = head;
+            // a line a lane (bulk prefetches of whole rows took 60 cycles each, 24,000 for 64 nodes)
+            for (int i = lane; i < 2 * n; i += 32) {
+                const size_t row = ((size_t)(lo + i / 2) * H + head) * D + i % 2 * 64;
+                prefetch_l2(k + row);
+                prefetch_l2(b + row);
+                prefetch_l2(q + row);
+                prefetch_l2(v + row);
+                prefetch_l2(w + row);
+                prefetch_l2(alpha + row);
+                prefetch_l2(alpha + row + 32);
             }
             __syncwarp();
             return n;
@@ -190,10 +169,16 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                 fence_after();
                 if (lane == 0) {
                     const uint32_t idesc = idesc_bf16(128, 2 * rows, 0, 0), s = tmem + TM_S + (c & 1) * 128;
-                    const uint32_t hi = smem_u32(sh.b_hi), lo = smem_u32(sh.b_lo);
-                    for (int j = 0; j < 8; ++j) mma_ts(tmem + TM_D, s + 8 * j, desc_kmajor(hi, 2 * MAX_NODES, j), idesc, j > 0);
-                    for (int j = 0; j < 8; ++j) mma_ts(tmem + TM_D, s + 8 * j, desc_kmajor(lo, 2 * MAX_NODES, j), idesc, 1);
-                    for (int j = 0; j < 8; ++j) mma_ts(tmem + TM_D, s + 64 + 8 * j, desc_kmajor(hi, 2 * MAX_NODES, j), idesc, 1);
+                    const auto products = [&](uint32_t a, uint64_t desc, uint32_t acc) {   // eight steps of 16 channels
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)   // the address field counts 16 bytes: 32 bytes a step, 16 KB a half
+                            mma_ts(tmem + TM_D, a + 8 * j, desc + (j >> 2) * (2 * MAX_NODES * 128 >> 4) + (j & 3) * 2, idesc, acc | (j > 0));
+                    };
+                    const uint64_t hi = desc_kmajor(smem_u32(sh.b_hi), 2 * MAX_NODES, 0),
+                                   lo = desc_kmajor(smem_u32(sh.b_lo), 2 * MAX_NODES, 0);
+                    products(s, hi, 0);
+                    products(s, lo, 1);
+                    products(s + 64, hi, 1);
                     mma_commit(bar(sh.s_free[c & 1]));
                     mma_commit(bar(sh.b_free));
                     mma_commit(bar(sh.d_full));
@@ -224,54 +209,46 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                     rw.load(w + at);
                     rv.get(x);
                     rw.get(y);
-                    float *to = &sh.delta[0][0] + 8 * i;
+                    float *to = &sh.r[0][0] + 8 * i;
                     *reinterpret_cast<float4 *>(to) = make_float4(x[0] * y[0], x[1] * y[1], x[2] * y[2], x[3] * y[3]);
                     *reinterpret_cast<float4 *>(to + 4) = make_float4(x[4] * y[4], x[5] * y[5], x[6] * y[6], x[7] * y[7]);
                 }
                 if (!group_wait(sh.d_full, c, BAR_COLUMN)) break;
-                fence_after();
                 const int rows = (n + 7) / 8 * 8;
                 for (int i0 = 0; i0 < n; i0 += 32) {   // one warpgroup each of the two products
-                    uint32_t x[32];
-                    tmem_ld32(tmem + lanes + TM_D + half * rows + i0, x);
+                    uint32_t y[32];
+                    tmem_ld32(tmem + lanes + TM_D + half * rows + i0, y);
                     wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i0 + i < n) {
-                            if (half) sh.out[i0 + i][col] = __uint_as_float(x[i]);
-                            else sh.delta[i0 + i][col] -= __uint_as_float(x[i]);
-                        }
+                    for (int i = 0; i < 32; ++i) {   // the rows behind the last node are not read
+                        if (half) sh.x[i0 + i][col] = __uint_as_float(y[i]);
+                        else sh.r[i0 + i][col] -= __uint_as_float(y[i]);
+                    }
                 }
                 fence_before();
                 arrive(sh.d_free);
                 if (!group_wait(sh.coef_full[c & 1], c >> 1, BAR_COLUMN)) break;
                 const Coef &coef = sh.coef[c & 1];
-                const int levels = m.levels;
-                for (int l = 0; l < levels; ++l) {
-                    const int end = m.start[l + 1];
-                    for (int r = m.start[l] + half; r < end; r += 2) {
-                        const int node = m.order[r], base = pairs(node);
-                        float d = sh.delta[node][col], x = sh.out[node][col];
-                        for (int j = 1; j <= l; j += 4) {
-                            float2 ap[4];
-                            float di[4];
+                for (int node = warp; node < n; node += COLUMN_WARPS) {   // four columns a lane
+                    const int base = pairs(node), above = coef.above[node];
+                    f32x2 x[2];
+                    load2(&sh.x[node][4 * lane], x);
+                    for (int j = 0; j <= above; j += 4) {
+                        const float4 c4 = *reinterpret_cast<const float4 *>(coef.c + base + j);
+                        const uchar4 a4 = *reinterpret_cast<const uchar4 *>(coef.anc + base + j);
+                        const float cc[4] = {c4.x, c4.y, c4.z, c4.w};
+                        const int from[4] = {a4.x, a4.y, a4.z, a4.w};
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {   // past the root: the root again, with zero coefficients
-                                const int at = base + min(j + i, l);
-                                ap[i] = coef.ap[at];
-                                if (j + i > l) ap[i] = make_float2(0.f, 0.f);
-                                di[i] = sh.delta[coef.anc[at]][col];
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                d = fmaf(-ap[i].x, di[i], d);
-                                x = fmaf(ap[i].y, di[i], x);
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            f32x2 r[2];
+                            load2(&sh.r[from[i]][4 * lane], r);
+                            x[0] = fma2(pack2(cc[i], cc[i]), r[0], x[0]);
+                            x[1] = fma2(pack2(cc[i], cc[i]), r[1], x[1]);
                         }
-                        sh.delta[node][col] = d;
-                        o[first + (size_t)node * H * D + col] = __float2bfloat16_rn(fmaf(coef.ap[base].y, d, x));
                     }
-                    if (l + 1 < levels) group_sync(BAR_COLUMN, 256);
+                    const float2 x0 = unpack2(x[0]), x1 = unpack2(x[1]);
+                    *reinterpret_cast<uint2 *>(o + first + (size_t)node * H * D + 4 * lane) =
+                        make_uint2(pack_bf16(x0.x, x0.y), pack_bf16(x1.x, x1.y));
                 }
                 arrive(sh.coef_free[c & 1]);
                 ++c;
@@ -279,34 +256,33 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
             arrive(sh.meta_free[it % METAS]);
         }
     } else if (warp < COLUMN_WARPS + STATE_WARPS) {
-        const int col = tid - 32 * COLUMN_WARPS;
+        const int col = tid & 127, half = (warp - COLUMN_WARPS) >> 2;   // rows 64 half .. of the state
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
-            if (!warp_wait(sh.meta_full[it % METAS], it / METAS)) break;
+            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_STATE)) break;
             const Meta &m = sh.meta[it % METAS];
             const int n = m.n, slot = m.slot, head = m.head;
             arrive(sh.meta_free[it % METAS]);
             if (n == 0) continue;
-            const float *src = S + (size_t)(slot < 0 ? 0 : slot) * slot_stride + (size_t)head * D * D + col;
-            float x[2][32];   // two quarters of the column in flight
-            const auto fetch = [&](int part) {
+            const float *src = S + (size_t)(slot < 0 ? 0 : slot) * slot_stride + ((size_t)head * D + 64 * half) * D + col;
+            const uint32_t to = tmem + lanes + TM_S + (c & 1) * 128 + 32 * half;
+            bool ok = true;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[part & 1][i] = slot < 0 ? 0.f : __ldcs(src + (size_t)(32 * part + i) * D);
-            };
-            fetch(0);
-            if (!warp_wait(sh.s_free[c & 1], (c >> 1) + 1)) break;
-            fence_after();
-            const uint32_t to = tmem + lanes + TM_S + (c & 1) * 128;
+            for (int part = 0; part < 2; ++part) {
+                float x[32];
 #pragma unroll
-            for (int part = 0; part < 4; ++part) {
-                if (part < 3) fetch(part + 1);
+                for (int i = 0; i < 32; ++i) x[i] = slot < 0 ? 0.f : __ldcs(src + (size_t)(32 * part + i) * D);
+                if (part == 0) {
+                    if (!(ok = group_wait(sh.s_free[c & 1], (c >> 1) + 1, BAR_STATE))) break;
+                }
                 uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) split2(x[part & 1][2 * i], x[part & 1][2 * i + 1], hi[i], lo[i]);
+                for (int i = 0; i < 16; ++i) split2(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
                 tmem_st16(to + 16 * part, hi);
                 tmem_st16(to + 64 + 16 * part, lo);
             }
+            if (!ok) break;
             wait_st();
             fence_before();
             arrive(sh.s_full[c & 1]);
@@ -327,35 +303,54 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                     cp_async16(smem_u32(&sh.alpha[node][at]), alpha + first + (size_t)node * H * D + at);
                     if (!(i & 1)) cp_async16(smem_u32(&sh.k[node][at]), k + first + (size_t)node * H * D + at);
                 }
+                // the second half from the other end: late nodes are deep, and a warp has both
+                const int node_of[2] = {4 * ww + (lane >> 3), 63 - 4 * ww - (lane >> 3)};
+                Rows<__nv_bfloat16, D> tok;
+                tok.load(b, q, lo, H, head, node_of[0], n, lane);
                 cp_async_wait();
                 if (!group_wait(sh.coef_free[c & 1], (c >> 1) + 1, BAR_WALK)) break;
                 Coef &coef = sh.coef[c & 1];
                 bool ok = true;
-                for (int n0 = 0; n0 < n; n0 += 4 * WALK_WARPS) {
-                    const int node = n0 + 4 * ww + (lane >> 3);
-                    float e[4][4], g[4][4];
-                    walk<__nv_bfloat16, D>(k, b, q, &sh.k[0][0], &sh.alpha[0][0], m.parent, coef.ap, coef.anc, lo, H, head,
-                                           node, n, lane, e, g);
-                    if (n0 == 0 && !(ok = group_wait(sh.b_free, c + 1, BAR_WALK))) break;   // the products before
-                    if (node < n)
+#pragma unroll 1
+                for (int round = 0; round < 2; ++round) {
+                    if (32 * round >= n) break;
+                    const int node = round ? node_of[1] : node_of[0];
+                    f32x2 e[4][2], g[4][2];
+                    const int up = walk<__nv_bfloat16, D>(tok, &sh.k[0][0], &sh.alpha[0][0], m.parent, sh.a, coef.c, coef.anc,
+                                                          sh.where, node, n, lane, e, g);
+                    if (round == 0) {
+                        if (!(ok = group_wait(sh.b_free, c + 1, BAR_WALK))) break;   // the products before
+                        if (n > 32) tok.load(b, q, lo, H, head, node_of[1], n, lane);
+                    }
+                    if (node < n) {
+                        if (sub == 0) coef.above[node] = (unsigned char)up;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            uint32_t hi[2], lo2[2];
                             const uint32_t at = sw_off(node, 4 * (sub + 8 * j), 2 * MAX_NODES),
                                            at2 = sw_off(rows + node, 4 * (sub + 8 * j), 2 * MAX_NODES);
-                            split2(e[j][0], e[j][1], hi[0], lo2[0]);
-                            split2(e[j][2], e[j][3], hi[1], lo2[1]);
-                            *reinterpret_cast<uint2 *>(sh.b_hi + at) = make_uint2(hi[0], hi[1]);
-                            *reinterpret_cast<uint2 *>(sh.b_lo + at) = make_uint2(lo2[0], lo2[1]);
-                            split2(g[j][0], g[j][1], hi[0], lo2[0]);
-                            split2(g[j][2], g[j][3], hi[1], lo2[1]);
-                            *reinterpret_cast<uint2 *>(sh.b_hi + at2) = make_uint2(hi[0], hi[1]);
-                            *reinterpret_cast<uint2 *>(sh.b_lo + at2) = make_uint2(lo2[0], lo2[1]);
+                            const auto put = [&](uint32_t to, const f32x2 (&x)[2]) {
+                                const float2 x0 = unpack2(x[0]), x1 = unpack2(x[1]);
+                                uint2 hi, lo2;
+                                split2(x0.x, x0.y, hi.x, lo2.x);
+                                split2(x1.x, x1.y, hi.y, lo2.y);
+                                *reinterpret_cast<uint2 *>(sh.b_hi + to) = hi;
+                                *reinterpret_cast<uint2 *>(sh.b_lo + to) = lo2;
+                            };
+                            put(at, e[j]);
+                            put(at2, g[j]);
                         }
+                    }
                 }
                 if (!ok) break;
                 fence_async_smem();
                 arrive(sh.b_full);
+                group_sync(BAR_WALK, 256);   // every walk is done
+#pragma unroll 1
+                for (int round = 0; round < 2; ++round) {
+                    const int node = round ? node_of[1] : node_of[0];
+                    if (32 * round >= n) break;
+                    eliminate(sh.a, coef.c, sh.where, coef.c, node, n, node < n ? coef.above[node] : 0, lane);
+                }
                 arrive(sh.coef_full[c & 1]);
                 ++c;
             }

@@ -79,6 +79,27 @@ def test_tree(dtype, K, V, sizes):
     assert torch.isnan(o[rows:]).all()           # rows of no tree stay as they were
 
 
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_tree_many_items(seed):
+    """More (sequence, head) pairs than the GPU has SMs: trees of every size, empty and malformed ones between."""
+    torch, g = cuda_or_skip()
+    rng, H, B = np.random.default_rng(seed), 13, 48
+    sizes = [int(n) for n in rng.choice([0, 1, 2, 7, 8, 9, 31, 32, 33, 40, 64], B)]
+    cu, parents = np.concatenate([[0], np.cumsum(sizes)]), sum((random_tree(rng, n, 1 + 2 * (i % 8)) for i, n in enumerate(sizes)), [])
+    x, pool, slots = tokens(torch, seed, cu[-1], H, 128, 128, "bf16"), make_pool(torch, seed, 60, H, 128, 128), rng.integers(-1, 60, B)
+    ref = op.tree(*(f64(a) for a in x), f64(pool), slots, cu, parents)
+    bad = [i for i in range(B) if sizes[i] and i % 7 == 3]
+    for i in bad:
+        parents[cu[i + 1] - 1] = sizes[i]
+    o, ws = torch.full_like(x[2], float("nan")), g.new_workspace(0)
+    g.gdn2_tree_fwd(*x, pool, i32(torch, slots), i32(torch, cu), i32(torch, parents), o, 64, workspace=ws)
+    assert g.gdn2_workspace_status(ws) == (g.DEV_PARENT if bad else 0)
+    left = sorted(r for i in bad for r in range(cu[i], cu[i + 1]))
+    kept = sorted(set(range(cu[-1])) - set(left))
+    assert torch.isnan(o[left]).all()
+    close(o[kept], ref[kept], "bf16")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shape", ["chain", "star", "roots", "twos"])
 @pytest.mark.parametrize("n", [6, 64])
@@ -185,6 +206,29 @@ def test_recurrent(dtype, K, V, H, sizes):
         assert torch.isnan(o[rows:]).all()
         idle = [s for s in range(2 * n + 1) if s not in dst]
         assert torch.equal(p[idle], pool[idle])
+
+
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 64)])
+def test_recurrent_many_items(K, V):
+    """More (sequence, head) pairs than the GPU has SMs, runs of every length between empty ones, a conflict."""
+    torch, g = cuda_or_skip()
+    rng, H, B = np.random.default_rng(K), 11, 60
+    sizes = [int(n) for n in rng.choice([0, 1, 2, 3, 4, 5, 8, 21, 50], B)]
+    cu, slots = np.concatenate([[0], np.cumsum(sizes)]), rng.permutation(2 * B + 1)
+    src, dst = slots[:B].copy(), slots[B:2 * B].copy()
+    src[3], dst[4], dst[10], src[11] = -1, -1, src[10], src[12]
+    dst[20] = dst[21]
+    x, pool = tokens(torch, K, cu[-1], H, K, V, "bf16"), make_pool(torch, K, 2 * B + 1, H, K, V)
+    out = [20, 21]
+    cu_ok = [i for i in range(B) if i not in out]
+    ref, after = op.recurrent(*(f64(a) for a in x), f64(pool), src, [d if i not in out else -1 for i, d in enumerate(dst)], cu)
+    o, ws = torch.full_like(x[2], float("nan")), g.new_workspace(0)
+    g.gdn2_recurrent_fwd(*x, pool, i32(torch, src), i32(torch, dst), i32(torch, cu), None, o, workspace=ws)
+    assert g.gdn2_workspace_status(ws) == g.DEV_CONFLICT
+    kept = sorted(r for i in cu_ok for r in range(cu[i], cu[i + 1]))
+    close(o[kept], ref[kept], "bf16")
+    close(pool, after, "f32")
+    assert torch.isnan(o[sorted(set(range(cu[-1])) - set(kept))]).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
