@@ -7,10 +7,11 @@
 // u = w v, the states need not be formed:
 //   delta_n = u_n - S^T (e_n G_n) - sum over proper ancestors i of A[n,i] delta_i,   A[n,i] = sum_c e_n (G_n / G_i) k_i
 //   o_n     = S^T (q_n G_n) + sum over ancestors i and n itself of P[n,i] delta_i,   P[n,i] = sum_c q_n (G_n / G_i) k_i
-// G_n / G_i is the product of the decays below i down to n, so walking from n to its root with a running
-// product gives A, P, e_n G_n and q_n G_n without a division, a logarithm or a masked entry: decays of any
-// size (zero included) are exact, and what sits on another branch is never touched.  The deltas are then
-// eliminated (eliminate()), which leaves o_n as a sum over n's path alone.
+// G_n / G_i is the product of the decays below i down to n.  While every G on n's path is in fp32's range, A and P
+// are products of e_n G_n and q_n G_n with k_i / G_i; where one is not (long or hard decays, zero included) the
+// decays are multiplied in on the way up instead, without a division.  Which it is goes by the path alone, and
+// nothing of another branch is touched.  The deltas are then eliminated (eliminate()), which leaves o_n as a sum
+// over n's path alone.
 #include "gdn2_tree.cuh"
 
 namespace gdn2 {
@@ -30,12 +31,12 @@ __global__ void __launch_bounds__(256) tree_kernel(const Tok *__restrict__ q, co
     extern __shared__ __align__(16) float smem[];
     const int cols = V / splits, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
     const int head = blockIdx.x / splits, col0 = blockIdx.x % splits * cols, seq = blockIdx.y;
-    float *sk = smem, *sa = sk + max_nodes * K, *se = sa + max_nodes * K, *sq = se + max_nodes * K;
+    float *sk = smem, *sa = sk + max_nodes * K, *se = sa + max_nodes * K, *sq = se + max_nodes * K;   // sk: k / G
     float *sr = sq + max_nodes * K, *ss = sr + max_nodes * cols;
     float *cA = ss + max_nodes * cols, *cP = cA + pairs(max_nodes);
     int *sp = reinterpret_cast<int *>(cP + pairs(max_nodes));
-    unsigned short *where = reinterpret_cast<unsigned short *>(sp + max_nodes);
-    unsigned char *anc = reinterpret_cast<unsigned char *>(where + pairs(max_nodes)), *depth = anc + pairs(max_nodes);
+    unsigned char *anc = reinterpret_cast<unsigned char *>(sp + max_nodes), *depth = anc + pairs(max_nodes),
+                  *fine = depth + max_nodes;
 
     const int lo = cu[seq], hi = cu[seq + 1], slot = slots[seq];
     unsigned bad = 0;
@@ -68,18 +69,10 @@ __global__ void __launch_bounds__(256) tree_kernel(const Tok *__restrict__ q, co
     const int n = hi - lo;
     if (n == 0) return;
 
-    // k and alpha of all nodes, four channels a thread at a time
 #pragma unroll 4
-    for (int i = tid; i < n * (K / 4); i += nt) {
-        const size_t at = ((size_t)(lo + i / (K / 4)) * H + head) * K + i % (K / 4) * 4;
-        Raw<Tok, 4> x;
-        float y[4];
-        x.load(k + at);
-        const float4 a = *reinterpret_cast<const float4 *>(alpha + at);
-        x.get(y);
-        *reinterpret_cast<float4 *>(sk + 4 * i) = make_float4(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<float4 *>(sa + 4 * i) = a;
-    }
+    for (int i = tid; i < n * (K / 4); i += nt)   // alpha of all nodes, four channels a thread at a time
+        *reinterpret_cast<float4 *>(sa + 4 * i) = *reinterpret_cast<const float4 *>(
+            alpha + ((size_t)(lo + i / (K / 4)) * H + head) * K + i % (K / 4) * 4);
 #pragma unroll 4
     for (int i = tid; i < n * (cols / 4); i += nt) {   // u, until the product is taken off it
         const size_t at = ((size_t)(lo + i / (cols / 4)) * H + head) * V + col0 + i % (cols / 4) * 4;
@@ -93,24 +86,52 @@ __global__ void __launch_bounds__(256) tree_kernel(const Tok *__restrict__ q, co
     }
     __syncthreads();
     for (int n0 = warp * 4; n0 < n; n0 += nt / 8) {
-        const int node = n0 + (lane >> 3);
-        f32x2 e[RJ][2], g[RJ][2];
-        Rows<Tok, K> rows;
-        rows.load(b, q, lo, H, head, node, n, lane);
-        const int above = walk<Tok, K>(rows, sk, sa, sp, cA, cP, anc, where, node, n, lane, e, g);
+        const int node = n0 + (lane >> 3), sub = lane & 7;
+        const size_t row = ((size_t)(lo + (node < n ? node : 0)) * H + head) * K + 4 * sub;
+        Raw<Tok, 4> rk[RJ], rb[RJ], rq[RJ];
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) rk[j].load(k + row + 32 * j), rb[j].load(b + row + 32 * j), rq[j].load(q + row + 32 * j);
+        f32x2 G[RJ][2];
+        const int above = climb<K>(sa, sp, anc, node, n, lane, G);
+        const bool good = in_range<K>(G, lane);
         if (node < n) {
-            if ((lane & 7) == 0) depth[node] = (unsigned char)above;
+            if (sub == 0) depth[node] = (unsigned char)above, fine[node] = good;
 #pragma unroll
             for (int j = 0; j < RJ; ++j) {
-                *reinterpret_cast<ulonglong2 *>(se + node * K + 4 * ((lane & 7) + 8 * j)) = make_ulonglong2(e[j][0], e[j][1]);
-                *reinterpret_cast<ulonglong2 *>(sq + node * K + 4 * ((lane & 7) + 8 * j)) = make_ulonglong2(g[j][0], g[j][1]);
+                const int at = node * K + 4 * (sub + 8 * j);
+                const float2 g0 = unpack2(G[j][0]), g1 = unpack2(G[j][1]);
+                float kk[4], bb[4], qq[4];
+                rk[j].get(kk);
+                rb[j].get(bb);
+                rq[j].get(qq);
+                *reinterpret_cast<float4 *>(se + at) = make_float4(bb[0] * kk[0] * g0.x, bb[1] * kk[1] * g0.y,
+                                                                   bb[2] * kk[2] * g1.x, bb[3] * kk[3] * g1.y);
+                *reinterpret_cast<float4 *>(sq + at) = make_float4(qq[0] * g0.x, qq[1] * g0.y, qq[2] * g1.x, qq[3] * g1.y);
+                *reinterpret_cast<float4 *>(sk + at) =
+                    make_float4(__fdividef(kk[0], g0.x), __fdividef(kk[1], g0.y), __fdividef(kk[2], g1.x), __fdividef(kk[3], g1.y));
             }
         }
     }
     __syncthreads();
     for (int n0 = warp * 4; n0 < n; n0 += nt / 8) {
+        const int node = n0 + (lane >> 3), sub = lane & 7, above = node < n ? depth[node] : -1;
+        bool good = true;
+        for (int j = sub; j <= above; j += 8) good = good && fine[anc[pairs(node) + j]];
+        good = (__ballot_sync(0xffffffffu, good) >> (lane & 24) & 0xffu) == 0xffu;
+        f32x2 e[RJ][2], g[RJ][2];
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) {
+            load2(se + (node < n ? node : 0) * K + 4 * (sub + 8 * j), e[j]);
+            load2(sq + (node < n ? node : 0) * K + 4 * (sub + 8 * j), g[j]);
+        }
+        couple<K>(sk, anc, cA, cP, node < n && good, node, above, lane, e, g);
+        if (__any_sync(0xffffffffu, node < n && !good))
+            couple_far<Tok, K>(q, k, b, alpha, anc, cA, cP, node < n && !good, lo, H, head, node, above, lane);
+    }
+    __syncthreads();
+    for (int n0 = warp * 4; n0 < n; n0 += nt / 8) {
         const int node = n0 + (lane >> 3);
-        eliminate(cA, cP, where, cP, node, n, node < n ? depth[node] : 0, lane);
+        eliminate(cA, cP, anc, cP, node, n, node < n ? depth[node] : 0, lane);
     }
 
     // S^T (e G) and S^T (q G) of every node
@@ -161,8 +182,8 @@ int launch_t(const void *q, const void *k, const void *v, const float *alpha, co
              const float *S, long long slot_stride, int num_slots, const int *slots, const int *cu, const int *parents,
              void *o, int batch, int H, int total, int max_nodes, unsigned *status, cudaStream_t st) {
     const auto smem = [&](int n, int cols) {
-        return sizeof(float) * (size_t)n * (4 * K + 2 * cols) + (2 * sizeof(float) + sizeof(short) + 1) * (size_t)pairs(n) +
-               (sizeof(int) + 1) * (size_t)n;
+        return sizeof(float) * (size_t)n * (4 * K + 2 * cols) + (2 * sizeof(float) + 1) * (size_t)pairs(n) +
+               (sizeof(int) + 2) * (size_t)n;
     };
     static const bool ok = cudaFuncSetAttribute(tree_kernel<Tok, K, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                 (int)smem(MAX_NODES, V)) == cudaSuccess;

@@ -1,4 +1,4 @@
-// What the two kernels for drafted trees share (sm_100a): the walk from a node to its root.
+// What the two kernels for drafted trees share (sm_100a): paths to the root and the coefficients along them.
 #pragma once
 
 #include "gdn2_internal.h"
@@ -20,19 +20,10 @@ __host__ __device__ constexpr int pairs(int node) { return 4 * (node / 4 + 1) * 
 constexpr int MAX_PAIRS = pairs(MAX_NODES);
 static_assert(pairs(0) == 0 && pairs(1) == 4 && pairs(4) == 16 && pairs(5) == 24 && pairs(64) == 2176, "row starts");
 
-// The walk to the root and what follows it take eight lanes a node, four nodes a warp; all lanes of a warp make
-// the calls, with node >= n for none.
+// What follows takes eight lanes a node, four nodes a warp; all lanes of a warp make the calls, with node >= n
+// for none.
 
-// The token rows b and q of a lane: channels 4 (sub + 8 j) + c, sub = lane & 7.
-template <typename Tok, int K>
-struct Rows {
-    Raw<Tok, 4> b[K / 32], q[K / 32];
-    __device__ __forceinline__ void load(const Tok *pb, const Tok *pq, int lo, int H, int head, int node, int n, int lane) {
-        const size_t row = ((size_t)(lo + (node < n ? node : 0)) * H + head) * K + 4 * (lane & 7);
-#pragma unroll
-        for (int j = 0; j < K / 32; ++j) b[j].load(pb + row + 32 * j), q[j].load(pq + row + 32 * j);
-    }
-};
+// A lane's channels are 4 (sub + 8 j) + c, sub = lane & 7.
 
 // Sums of eight values over the eight lanes of a node: on return lane `sub` holds the total of x[sub].
 __device__ __forceinline__ float node_sums(const float (&x)[8], int lane) {
@@ -47,82 +38,130 @@ __device__ __forceinline__ float node_sums(const float (&x)[8], int lane) {
     return (up1 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up1 ? b[0] : b[1], 1);
 }
 
-// From a node to its root, four ancestors at a time.  On return e and g are e_n G_n and q_n G_n at the lane's
-// channels, the node's rows of A and P (cA, cP), of anc (whom each is for) and of where (the start of that one's
-// row) are written, and the number of ancestors is returned.  sk, sa: k and alpha of all nodes in shared memory.
-// Four operations a channel for each pair (node, ancestor), two channels an instruction, the decays multiplied
-// in as the walk goes up, and seven shuffles for four pairs.
-template <typename Tok, int K, typename SharedTok, typename Parent>
-__device__ __forceinline__ int walk(const Rows<Tok, K> &rows, const SharedTok *sk, const float *sa, const Parent *parent,
-                                    float *cA, float *cP, unsigned char *anc, unsigned short *where, int node, int n,
-                                    int lane, f32x2 (&e)[K / 32][2], f32x2 (&g)[K / 32][2]) {
-    constexpr int RJ = K / 32;
+// The path from a node to its root, whom to anc, and G_n, the product of its decays, at the lane's channels; the
+// number of ancestors is returned.  sa: alpha of all nodes in shared memory.
+template <int K, typename Parent>
+__device__ __forceinline__ int climb(const float *sa, const Parent *parent, unsigned char *anc, int node, int n, int lane,
+                                     f32x2 (&G)[K / 32][2]) {
     const int sub = lane & 7;
-    const auto key = [&](int at, int j, f32x2 (&x)[2]) {
-        Raw<SharedTok, 4> r;
-        float y[4];
-        r.load(sk + at * K + 4 * (sub + 8 * j));
-        r.get(y);
-        x[0] = pack2(y[0], y[1]);
-        x[1] = pack2(y[2], y[3]);
-    };
-    int at = node < n ? node : -1, above = -1;
+    int at = node < n ? node : -1, above = -1, root = 0, out = pairs(at < 0 ? 0 : at);
 #pragma unroll
-    for (int j = 0; j < RJ; ++j) {
-        f32x2 kk[2];
-        float x[4];
-        key(at < 0 ? 0 : at, j, kk);
-        rows.b[j].get(x);
-        e[j][0] = mul2(pack2(x[0], x[1]), kk[0]);
-        e[j][1] = mul2(pack2(x[2], x[3]), kk[1]);
-        rows.q[j].get(x);
-        g[j][0] = pack2(x[0], x[1]);
-        g[j][1] = pack2(x[2], x[3]);
-    }
-    int out = pairs(at < 0 ? 0 : at), root = 0;
+    for (int j = 0; j < K / 32; ++j) G[j][0] = G[j][1] = pack2(1.f, 1.f);
     while (__any_sync(0xffffffffu, at >= 0)) {
-        float x[8];   // A and P of four pairs
         const bool some = at >= 0;
         int whom = 0;
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            x[s] = x[4 + s] = 0.f;
             if (at >= 0) {
                 const int up = parent[at];
-                f32x2 a[2] = {0ull, 0ull}, p[2] = {0ull, 0ull};
 #pragma unroll
-                for (int j = 0; j < RJ; ++j) {
-                    f32x2 kk[2], aa[2];
-                    key(at, j, kk);
+                for (int j = 0; j < K / 32; ++j) {
+                    f32x2 aa[2];
                     load2(sa + at * K + 4 * (sub + 8 * j), aa);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        a[c] = fma2(e[j][c], kk[c], a[c]);
-                        p[c] = fma2(g[j][c], kk[c], p[c]);
-                        e[j][c] = mul2(e[j][c], aa[c]);
-                        g[j][c] = mul2(g[j][c], aa[c]);
-                    }
+                    G[j][0] = mul2(G[j][0], aa[0]);
+                    G[j][1] = mul2(G[j][1], aa[1]);
                 }
-                const float2 ya = unpack2(add2(a[0], a[1])), yp = unpack2(add2(p[0], p[1]));
-                x[s] = ya.x + ya.y;
-                x[4 + s] = yp.x + yp.y;
                 root = at;
                 at = up;
                 ++above;
             }
             if (s == (sub & 3)) whom = root;
         }
-        const float sum = node_sums(x, lane);
         if (some) {
-            (sub < 4 ? cA : cP)[out + (sub & 3)] = sum;   // the node's own A is not used
-            if (sub < 4) {
-                anc[out + sub] = (unsigned char)whom;
-                where[out + sub] = (unsigned short)pairs(whom);
-            }
+            if (sub < 4) anc[out + sub] = (unsigned char)whom;   // behind the root: the root again
             out += 4;
         }
     }
     return above;
+}
+
+// Whether G_n and 1 / G_n can stand for themselves: at all the node's channels in [2^-100, 2^100].
+template <int K>
+__device__ __forceinline__ bool in_range(const f32x2 (&G)[K / 32][2], int lane) {
+    bool fine = true;
+#pragma unroll
+    for (int j = 0; j < K / 32; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const float2 x = unpack2(G[j][c]);
+            fine = fine && x.x >= 0x1p-100f && x.x <= 0x1p100f && x.y >= 0x1p-100f && x.y <= 0x1p100f;   // false for a NaN
+        }
+    return (__ballot_sync(0xffffffffu, fine) >> (lane & 24) & 0xffu) == 0xffu;
+}
+
+// A and P of a node's path, to cA and cP, where all its G are in range:  A[n,i] = sum_c (e_n G_n) (k_i / G_i), two
+// operations a channel, no chain from one ancestor to the next.  sk: k_i / G_i of all nodes in shared memory; e, g:
+// e_n G_n and q_n G_n.  `go`: whether this node takes part (its own eight lanes alike).
+template <int K>
+__device__ __forceinline__ void couple(const float *sk, const unsigned char *anc, float *cA, float *cP, bool go, int node,
+                                       int above, int lane, const f32x2 (&e)[K / 32][2], const f32x2 (&g)[K / 32][2]) {
+    const int sub = lane & 7, base = pairs(go ? node : 0), most = __reduce_max_sync(0xffffffffu, go ? above : -1);
+#pragma unroll 1
+    for (int h = 0; h <= most; h += 4) {
+        float x[8];
+        const bool some = go && h <= above;
+        const uchar4 whom = some ? *reinterpret_cast<const uchar4 *>(anc + base + h) : make_uchar4(0, 0, 0, 0);
+        const int at[4] = {whom.x, whom.y, whom.z, whom.w};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            f32x2 a[2] = {0ull, 0ull}, p[2] = {0ull, 0ull};
+#pragma unroll
+            for (int j = 0; j < K / 32; ++j) {
+                f32x2 kk[2];
+                load2(sk + at[s] * K + 4 * (sub + 8 * j), kk);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    a[c] = fma2(e[j][c], kk[c], a[c]);
+                    p[c] = fma2(g[j][c], kk[c], p[c]);
+                }
+            }
+            const float2 ya = unpack2(add2(a[0], a[1])), yp = unpack2(add2(p[0], p[1]));
+            x[s] = ya.x + ya.y;
+            x[4 + s] = yp.x + yp.y;
+        }
+        const float sum = node_sums(x, lane);
+        if (some) (sub < 4 ? cA : cP)[base + h + (sub & 3)] = sum;   // the node's own A is not used
+    }
+}
+
+// The same with the decays multiplied in one by one on the way up, from the tokens in HBM: for decays whose
+// product leaves the range (zero among them), exact for any.
+template <typename Tok, int K>
+__device__ __noinline__ void couple_far(const Tok *q, const Tok *k, const Tok *b, const float *alpha,
+                                        const unsigned char *anc, float *cA, float *cP, bool go, int lo, int H, int head,
+                                        int node, int above, int lane) {
+    const int sub = lane & 7, base = pairs(go ? node : 0), most = __reduce_max_sync(0xffffffffu, go ? above : -1);
+    const auto row = [&](int i) { return ((size_t)(lo + i) * H + head) * K + 4 * sub; };
+    float e[K / 32][4], g[K / 32][4];
+#pragma unroll
+    for (int j = 0; j < K / 32; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const size_t at = row(go ? node : 0) + 32 * j + c;
+            e[j][c] = ld_tok(b + at) * ld_tok(k + at);
+            g[j][c] = ld_tok(q + at);
+        }
+    for (int i = 0; i <= most; ++i) {
+        const bool some = go && i <= above;
+        const size_t at = row(some ? anc[base + i] : 0);
+        float a = 0.f, p = 0.f;
+#pragma unroll
+        for (int j = 0; j < K / 32; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float kk = ld_tok(k + at + 32 * j + c), aa = alpha[at + 32 * j + c];
+                a = fmaf(e[j][c], kk, a);
+                p = fmaf(g[j][c], kk, p);
+                e[j][c] *= aa;
+                g[j][c] *= aa;
+            }
+#pragma unroll
+        for (int m = 4; m > 0; m >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, m);
+            p += __shfl_xor_sync(0xffffffffu, p, m);
+        }
+        if (some && sub == 0) cA[base + i] = a, cP[base + i] = p;
+    }
 }
 
 // The deltas eliminated: with p_0 = n, p_1, ... the path from n to its root and R[i] = u_i - S^T (e_i G_i),
@@ -130,9 +169,9 @@ __device__ __forceinline__ int walk(const Rows<Tok, K> &rows, const SharedTok *s
 // A node's C needs no other node's, so the columns' work has no order among the nodes left: one product for
 // each pair, in place of two and a barrier for each level of the tree.  Lane `sub` takes j = 8 h + sub; the
 // coefficients of a finished j go to the others by a shuffle, those of finished blocks of eight through
-// shared memory.  All walks of the item must be done; cC may be cP.
-__device__ __forceinline__ void eliminate(const float *cA, const float *cP, const unsigned short *where, float *cC,
-                                          int node, int n, int above, int lane) {
+// shared memory.  The A and P of all nodes must be there; cC may be cP.
+__device__ __forceinline__ void eliminate(const float *cA, const float *cP, const unsigned char *anc, float *cC, int node,
+                                          int n, int above, int lane) {
     const int sub = lane & 7, base = node < n ? pairs(node) : 0;
     if (node >= n) above = -1;
     const int most = __reduce_max_sync(0xffffffffu, above);
@@ -141,10 +180,10 @@ __device__ __forceinline__ void eliminate(const float *cA, const float *cP, cons
         const bool mine = j <= above;
         float c = mine ? cP[base + j] : 0.f, up[8];
 #pragma unroll
-        for (int m = 0; m < 8; ++m) up[m] = mine && m < sub ? cA[where[base + h + m] + sub - m] : 0.f;
+        for (int m = 0; m < 8; ++m) up[m] = mine && m < sub ? cA[pairs(anc[base + h + m]) + sub - m] : 0.f;
         if (mine)
 #pragma unroll 4
-            for (int m = 0; m < h; ++m) c = fmaf(-cC[base + m], cA[where[base + m] + j - m], c);
+            for (int m = 0; m < h; ++m) c = fmaf(-cC[base + m], cA[pairs(anc[base + m]) + j - m], c);
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
             const float done = __shfl_sync(0xffffffffu, c, (lane & 24) | m);

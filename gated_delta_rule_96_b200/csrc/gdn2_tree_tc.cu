@@ -6,10 +6,11 @@
 // for the state and the tokens from five nodes on.  Both factors are split into two bf16, x = hi + lo (16
 // significant bits, relative error 2^-17): three tcgen05 products hi hi + hi lo + lo hi keep the error far
 // below the rounding of the bf16 output, where one product of bf16 operands would double that rounding.
-//   state group  (8 warps)  S from HBM to registers, half a column a thread, split, into tensor memory: the A
-//                           operand S^T, lane = value column, two buffers
-//   walk group   (8 warps)  eight lanes a node up to its root, then the elimination: the coefficients to shared
-//                           memory, and the rows e G and q G, split, into the B operand's swizzled images
+//   loader warp             S by bulk copies, 32 rows at a time, into two staging buffers
+//   state group  (4 warps)  a column a thread from there, split, into tensor memory: the A operand S^T, lane =
+//                           value column, two buffers
+//   path group   (16 warps) eight lanes a node up to its root: the rows e G and q G, split, into the B operand's
+//                           swizzled images, k / G and the coefficients to shared memory
 //   column group (8 warps)  R = u - S^T (e G) and S^T (q G) from tensor memory (lane = value column) to shared
 //                           memory, then o = S^T (q G) + C R, a node a warp and four columns a lane
 //   lead warp               reads and checks the items, brings the tokens' lines into L2 ahead of the groups,
@@ -23,10 +24,11 @@ namespace tree {
 using namespace gdn2::tc;
 
 constexpr int D = 128;
-constexpr int COLUMN_WARPS = 8, STATE_WARPS = 8, WALK_WARPS = 8;   // in this order; then the lead warp
-constexpr int LEAD = COLUMN_WARPS + STATE_WARPS + WALK_WARPS, TC_THREADS = 32 * (LEAD + 1);
+constexpr int COLUMN_WARPS = 8, STATE_WARPS = 4, PATH_WARPS = 16;   // in this order; then loader and lead
+constexpr int LOADER = COLUMN_WARPS + STATE_WARPS + PATH_WARPS, LEAD = LOADER + 1, TC_THREADS = 32 * (LEAD + 1);
+constexpr int STAGE_ROWS = 32, STAGES = 2;   // of the state
 constexpr int METAS = 4;
-constexpr uint32_t BAR_COLUMN = 1, BAR_WALK = 2, BAR_STATE = 3, WAIT_LIMIT = 1u << 24;
+constexpr uint32_t BAR_COLUMN = 1, BAR_PATH = 2, BAR_STATE = 3, WAIT_LIMIT = 1u << 24;
 constexpr uint32_t TM_S = 0, TM_D = 256, TM_COLS = 512;   // S: two buffers of hi (64 columns) and lo (64)
 
 // An item: its nodes lo .. lo+n-1, their parents, the state's slot.
@@ -42,15 +44,15 @@ struct Coef {   // eliminate()'s, whom each is for, and how many ancestors a nod
 
 struct TcShared {
     unsigned char b_hi[2 * MAX_NODES * D * 2], b_lo[2 * MAX_NODES * D * 2];   // [e G; q G], swizzled
-    __nv_bfloat16 k[MAX_NODES][D];
-    float alpha[MAX_NODES][D];
+    float stage[STAGES][STAGE_ROWS][D];
+    float alpha[MAX_NODES][D];                // then k / G
     float r[MAX_NODES][D], x[MAX_NODES][D];   // u, then R; S^T (q G); by node and value column
     float a[MAX_PAIRS];
-    unsigned short where[MAX_PAIRS];
     Coef coef[2];
     Meta meta[METAS];
-    unsigned long long meta_full[METAS], meta_free[METAS], s_full[2], s_free[2], coef_full[2], coef_free[2], b_full,
-        b_free, d_full, d_free;
+    unsigned char fine[MAX_NODES];            // whether a node's G is in range
+    unsigned long long meta_full[METAS], meta_free[METAS], stage_full[STAGES], stage_free[STAGES], s_full[2], s_free[2],
+        coef_full[2], coef_free[2], b_full, b_free, d_full, d_free;
     uint32_t tmem, abort;
 };
 static_assert(sizeof(TcShared) + 1024 <= 227 * 1024, "shared memory of an SM");
@@ -60,12 +62,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
 }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// x = hi + lo, two values at a time as packed bf16 (the first in the low half).  A value that is not finite
-// stays in hi alone: inf - inf would put a NaN into lo.
+// x = hi + lo, two values at a time as packed bf16 (the first in the low half).  An infinity leaves a NaN in lo:
+// what it meets is not finite either way.
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
     hi = pack_bf16(x, y);
-    const float hx = __uint_as_float(hi << 16), hy = __uint_as_float(hi & 0xffff0000u);
-    lo = pack_bf16(fabsf(hx) < INFINITY ? x - hx : 0.f, fabsf(hy) < INFINITY ? y - hy : 0.f);
+    lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
 }
 
 __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
@@ -82,14 +83,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
     volatile uint32_t *abort = &sh.abort;
 
     if (tid == 0) {
-        for (int i = 0; i < METAS; ++i) mbar_init(bar(sh.meta_full[i]), 1), mbar_init(bar(sh.meta_free[i]), LEAD);
+        for (int i = 0; i < METAS; ++i) mbar_init(bar(sh.meta_full[i]), 1), mbar_init(bar(sh.meta_free[i]), LEAD);   // a warp each, but the lead
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(sh.s_full[i]), STATE_WARPS);
             mbar_init(bar(sh.s_free[i]), 1);
-            mbar_init(bar(sh.coef_full[i]), WALK_WARPS);
+            mbar_init(bar(sh.coef_full[i]), PATH_WARPS);
             mbar_init(bar(sh.coef_free[i]), COLUMN_WARPS);
         }
-        mbar_init(bar(sh.b_full), WALK_WARPS);
+        for (int i = 0; i < STAGES; ++i) mbar_init(bar(sh.stage_full[i]), 1), mbar_init(bar(sh.stage_free[i]), STATE_WARPS);
+        mbar_init(bar(sh.b_full), PATH_WARPS);
         mbar_init(bar(sh.b_free), 1);
         mbar_init(bar(sh.d_full), 1);
         mbar_init(bar(sh.d_free), COLUMN_WARPS);
@@ -110,8 +112,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
         if (!ok) *abort = 1u;
         return ok;
     };
-    const auto group_wait = [&](unsigned long long &x, int phase, uint32_t id) {
-        const bool polls = (warp & 7) == 0, ok = !group_or(id, 256, polls && !wait(x, phase));
+    const int poller = warp < COLUMN_WARPS ? 0 : warp < COLUMN_WARPS + STATE_WARPS ? COLUMN_WARPS : COLUMN_WARPS + STATE_WARPS;
+    const auto group_wait = [&](unsigned long long &x, int phase, uint32_t id, uint32_t threads) {
+        const bool ok = !group_or(id, threads, warp == poller && !wait(x, phase));
         fence_after();
         return ok;
     };
@@ -194,14 +197,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
-            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_COLUMN)) break;
+            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_COLUMN, 32 * COLUMN_WARPS)) break;
             const Meta &m = sh.meta[it % METAS];
             const int n = m.n;
             if (n > 0) {
                 const size_t first = ((size_t)m.lo * H + m.head) * D;
                 // u, eight columns a thread at a time (group_wait's barrier is behind the last item's reads)
 #pragma unroll 4
-                for (int i = tid; i < n * (D / 8); i += 256) {
+                for (int i = tid; i < n * (D / 8); i += 32 * COLUMN_WARPS) {
                     const size_t at = first + (size_t)(i / (D / 8)) * H * D + i % (D / 8) * 8;
                     Raw<__nv_bfloat16, 8> rv, rw;
                     float x[8], y[8];
@@ -213,7 +216,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                     *reinterpret_cast<float4 *>(to) = make_float4(x[0] * y[0], x[1] * y[1], x[2] * y[2], x[3] * y[3]);
                     *reinterpret_cast<float4 *>(to + 4) = make_float4(x[4] * y[4], x[5] * y[5], x[6] * y[6], x[7] * y[7]);
                 }
-                if (!group_wait(sh.d_full, c, BAR_COLUMN)) break;
+                if (!group_wait(sh.d_full, c, BAR_COLUMN, 32 * COLUMN_WARPS)) break;
                 const int rows = (n + 7) / 8 * 8;
                 for (int i0 = 0; i0 < n; i0 += 32) {   // one warpgroup each of the two products
                     uint32_t y[32];
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                 }
                 fence_before();
                 arrive(sh.d_free);
-                if (!group_wait(sh.coef_full[c & 1], c >> 1, BAR_COLUMN)) break;
+                if (!group_wait(sh.coef_full[c & 1], c >> 1, BAR_COLUMN, 32 * COLUMN_WARPS)) break;
                 const Coef &coef = sh.coef[c & 1];
                 for (int node = warp; node < n; node += COLUMN_WARPS) {   // four columns a lane
                     const int base = pairs(node), above = coef.above[node];
@@ -256,26 +259,26 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
             arrive(sh.meta_free[it % METAS]);
         }
     } else if (warp < COLUMN_WARPS + STATE_WARPS) {
-        const int col = tid & 127, half = (warp - COLUMN_WARPS) >> 2;   // rows 64 half .. of the state
+        const int col = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
-            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_STATE)) break;
+            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_STATE, 32 * STATE_WARPS)) break;
             const Meta &m = sh.meta[it % METAS];
-            const int n = m.n, slot = m.slot, head = m.head;
+            const int n = m.n, slot = m.slot;
             arrive(sh.meta_free[it % METAS]);
             if (n == 0) continue;
-            const float *src = S + (size_t)(slot < 0 ? 0 : slot) * slot_stride + ((size_t)head * D + 64 * half) * D + col;
-            const uint32_t to = tmem + lanes + TM_S + (c & 1) * 128 + 32 * half;
+            if (!group_wait(sh.s_free[c & 1], (c >> 1) + 1, BAR_STATE, 32 * STATE_WARPS)) break;
+            const uint32_t to = tmem + lanes + TM_S + (c & 1) * 128;
             bool ok = true;
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
+#pragma unroll 1
+            for (int part = 0; part < D / STAGE_ROWS; ++part) {
+                const int g = c * (D / STAGE_ROWS) + part, stage = g % STAGES;
+                if (!(ok = group_wait(sh.stage_full[stage], g / STAGES, BAR_STATE, 32 * STATE_WARPS))) break;
                 float x[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = slot < 0 ? 0.f : __ldcs(src + (size_t)(32 * part + i) * D);
-                if (part == 0) {
-                    if (!(ok = group_wait(sh.s_free[c & 1], (c >> 1) + 1, BAR_STATE))) break;
-                }
+                for (int i = 0; i < 32; ++i) x[i] = slot < 0 ? 0.f : sh.stage[stage][i][col];
+                arrive(sh.stage_free[stage]);
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) split2(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
@@ -288,46 +291,80 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
             arrive(sh.s_full[c & 1]);
             ++c;
         }
+    } else if (warp == LOADER) {
+        for (int it = 0;; ++it) {
+            const long long at = blockIdx.x + (long long)it * gridDim.x;
+            if (at >= items) break;
+            if (!warp_wait(sh.meta_full[it % METAS], it / METAS)) break;
+            const Meta &m = sh.meta[it % METAS];
+            const int n = m.n, slot = m.slot, head = m.head;
+            arrive(sh.meta_free[it % METAS]);
+            if (n == 0) continue;
+            bool ok = true;
+            for (int part = 0; part < D / STAGE_ROWS && ok; ++part) {
+                const int g = c * (D / STAGE_ROWS) + part, stage = g % STAGES;
+                ok = warp_wait(sh.stage_free[stage], g / STAGES + 1);
+                if (ok && lane == 0) {
+                    constexpr uint32_t bytes = sizeof(sh.stage[0]);
+                    mbar_arrive_expect_tx(bar(sh.stage_full[stage]), slot < 0 ? 0 : bytes);
+                    if (slot >= 0)
+                        bulk_g2s(smem_u32(&sh.stage[stage][0][0]),
+                                 S + (size_t)slot * slot_stride + ((size_t)head * D + STAGE_ROWS * part) * D, bytes,
+                                 bar(sh.stage_full[stage]));
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            ++c;
+        }
     } else {
-        const int t = tid - 32 * (COLUMN_WARPS + STATE_WARPS), ww = t >> 5, sub = lane & 7;
+        constexpr int THREADS = 32 * PATH_WARPS;
+        const int t = tid - 32 * (COLUMN_WARPS + STATE_WARPS), sub = lane & 7, node = t >> 3;
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
-            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_WALK)) break;
+            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_PATH, THREADS)) break;
             const Meta &m = sh.meta[it % METAS];
             const int n = m.n;
             if (n > 0) {
                 const int lo = m.lo, head = m.head, rows = (n + 7) / 8 * 8;
                 const size_t first = ((size_t)lo * H + head) * D;
-                for (int i = t; i < n * (D / 4); i += 256) {   // group_wait's barrier is behind the last walk
-                    const int node = i / (D / 4), at = i % (D / 4) * 4;
-                    cp_async16(smem_u32(&sh.alpha[node][at]), alpha + first + (size_t)node * H * D + at);
-                    if (!(i & 1)) cp_async16(smem_u32(&sh.k[node][at]), k + first + (size_t)node * H * D + at);
-                }
-                // the second half from the other end: late nodes are deep, and a warp has both
-                const int node_of[2] = {4 * ww + (lane >> 3), 63 - 4 * ww - (lane >> 3)};
-                Rows<__nv_bfloat16, D> tok;
-                tok.load(b, q, lo, H, head, node_of[0], n, lane);
-                cp_async_wait();
-                if (!group_wait(sh.coef_free[c & 1], (c >> 1) + 1, BAR_WALK)) break;
-                Coef &coef = sh.coef[c & 1];
-                bool ok = true;
-#pragma unroll 1
-                for (int round = 0; round < 2; ++round) {
-                    if (32 * round >= n) break;
-                    const int node = round ? node_of[1] : node_of[0];
-                    f32x2 e[4][2], g[4][2];
-                    const int up = walk<__nv_bfloat16, D>(tok, &sh.k[0][0], &sh.alpha[0][0], m.parent, sh.a, coef.c, coef.anc,
-                                                          sh.where, node, n, lane, e, g);
-                    if (round == 0) {
-                        if (!(ok = group_wait(sh.b_free, c + 1, BAR_WALK))) break;   // the products before
-                        if (n > 32) tok.load(b, q, lo, H, head, node_of[1], n, lane);
-                    }
-                    if (node < n) {
-                        if (sub == 0) coef.above[node] = (unsigned char)up;
+                for (int i = t; i < n * (D / 4); i += THREADS)   // group_wait's barrier is behind the last item's reads
+                    cp_async16(smem_u32(&sh.alpha[0][0]) + 16 * i, alpha + first + (size_t)(i / (D / 4)) * H * D + i % (D / 4) * 4);
+                Raw<__nv_bfloat16, 4> rk[4], rb[4], rq[4];
+                {
+                    const size_t row = first + (size_t)(node < n ? node : 0) * H * D + 4 * sub;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t at = sw_off(node, 4 * (sub + 8 * j), 2 * MAX_NODES),
-                                           at2 = sw_off(rows + node, 4 * (sub + 8 * j), 2 * MAX_NODES);
+                    for (int j = 0; j < 4; ++j)
+                        rk[j].load(k + row + 32 * j), rb[j].load(b + row + 32 * j), rq[j].load(q + row + 32 * j);
+                }
+                cp_async_wait();
+                if (!group_wait(sh.coef_free[c & 1], (c >> 1) + 1, BAR_PATH, THREADS)) break;
+                Coef &coef = sh.coef[c & 1];
+                f32x2 e[4][2], g[4][2];
+                int above;
+                {
+                    f32x2 G[4][2];
+                    above = climb<D>(&sh.alpha[0][0], m.parent, coef.anc, node, n, lane, G);
+                    const bool good = in_range<D>(G, lane);
+                    if (node < n && sub == 0) coef.above[node] = (unsigned char)above, sh.fine[node] = good;
+                    if (!group_wait(sh.b_free, c + 1, BAR_PATH, THREADS)) break;   // the products before; all have climbed
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float kk[4], bb[4], qq[4];
+                        rk[j].get(kk);
+                        rb[j].get(bb);
+                        rq[j].get(qq);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const f32x2 k2 = pack2(kk[2 * h], kk[2 * h + 1]);
+                            e[j][h] = mul2(mul2(pack2(bb[2 * h], bb[2 * h + 1]), k2), G[j][h]);
+                            g[j][h] = mul2(pack2(qq[2 * h], qq[2 * h + 1]), G[j][h]);
+                        }
+                        if (node < n) {
+                            const float2 g0 = unpack2(G[j][0]), g1 = unpack2(G[j][1]);
+                            *reinterpret_cast<float4 *>(&sh.alpha[node][4 * (sub + 8 * j)]) =
+                                make_float4(__fdividef(kk[0], g0.x), __fdividef(kk[1], g0.y), __fdividef(kk[2], g1.x),
+                                            __fdividef(kk[3], g1.y));
                             const auto put = [&](uint32_t to, const f32x2 (&x)[2]) {
                                 const float2 x0 = unpack2(x[0]), x1 = unpack2(x[1]);
                                 uint2 hi, lo2;
@@ -336,21 +373,23 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                                 *reinterpret_cast<uint2 *>(sh.b_hi + to) = hi;
                                 *reinterpret_cast<uint2 *>(sh.b_lo + to) = lo2;
                             };
-                            put(at, e[j]);
-                            put(at2, g[j]);
+                            put(sw_off(node, 4 * (sub + 8 * j), 2 * MAX_NODES), e[j]);
+                            put(sw_off(rows + node, 4 * (sub + 8 * j), 2 * MAX_NODES), g[j]);
                         }
                     }
                 }
-                if (!ok) break;
                 fence_async_smem();
                 arrive(sh.b_full);
-                group_sync(BAR_WALK, 256);   // every walk is done
-#pragma unroll 1
-                for (int round = 0; round < 2; ++round) {
-                    const int node = round ? node_of[1] : node_of[0];
-                    if (32 * round >= n) break;
-                    eliminate(sh.a, coef.c, sh.where, coef.c, node, n, node < n ? coef.above[node] : 0, lane);
-                }
+                group_sync(BAR_PATH, THREADS);   // every k / G is there
+                bool good = true;
+                for (int j = sub; j <= above; j += 8) good = good && sh.fine[coef.anc[pairs(node) + j]];
+                good = (__ballot_sync(0xffffffffu, good) >> (lane & 24) & 0xffu) == 0xffu;
+                couple<D>(&sh.alpha[0][0], coef.anc, sh.a, coef.c, node < n && good, node, above, lane, e, g);
+                if (__any_sync(0xffffffffu, node < n && !good))
+                    couple_far<__nv_bfloat16, D>(q, k, b, alpha, coef.anc, sh.a, coef.c, node < n && !good, lo, H, head, node,
+                                                 above, lane);
+                group_sync(BAR_PATH, THREADS);   // every A and P is there
+                eliminate(sh.a, coef.c, coef.anc, coef.c, node, n, above, lane);
                 arrive(sh.coef_full[c & 1]);
                 ++c;
             }
