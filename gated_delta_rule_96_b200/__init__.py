@@ -417,123 +417,66 @@ def _gate_code(act) -> int:
     return GATES[act]
 
 
-def _check_f32(named):
-    import torch
-    for name, t in named:
-        if t is not None and t.dtype != torch.float32:
-            raise TypeError(f"{name} must be float32")
+_native_module = None
 
 
-def _check_i32(named):
-    import torch
-    for name, t in named:
-        if t is not None and (t.dtype != torch.int32 or t.dim() != 1):
-            raise TypeError(f"{name} must be a one-dimensional int32 tensor")
+def _native():
+    """The binding's native half (_gdn2_torch.so, built with the library): the checks and the marshalling of the
+    calls whose kernels take a few microseconds.  It calls the same libgdn2.so."""
+    global _native_module
+    if _native_module is None:
+        import torch  # noqa: F401  (its libraries come first)
+        load_library()
+        try:
+            from . import _gdn2_torch as native
+        except ImportError as e:
+            raise RuntimeError(f"{os.path.join(_HERE, '_gdn2_torch.so')} cannot be loaded ({e}); run "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+        native.bind(library_path(), GDN2Error)
+        _native_module = native
+    return _native_module
 
 
 def _rows(t) -> int:
     """Rows of a tensor whose last axis is the channels."""
-    rows = 1
-    for n in t.shape[:-1]:
-        rows *= n
-    return rows
+    return t.numel() // t.shape[-1] if t.shape[-1] else 0
+
+
+def _gated_workspace(o):
+    return new_workspace(gdn2_gated_norm_bwd_workspace_bytes(_rows(o), o.shape[-1]), o.device)
+
+
+def _add_workspace(h):
+    return new_workspace(gdn2_add_norm_bwd_workspace_bytes(_rows(h), h.shape[-1]), h.device)
 
 
 def gdn2_gated_norm_fwd(o, gate, weight, y, act="silu", eps=1e-6, stream=None) -> None:
     """y = RMSNorm(o) * weight * act(gate) over the last axis (include/gdn2.h, gdn2_gated_norm_fwd):
     o, gate, y of one shape and the token dtype, weight [d_v] fp32, act "silu" or "sigmoid"."""
-    _check_cuda(o, gate, weight, y)
-    dt, code = _dtype_code(o), _gate_code(act)
-    _check_f32((("weight", weight),))
-    _check_dtypes(o, (("gate", gate), ("y", y)))
-    _check_shapes((("gate", gate, o.shape), ("y", y, o.shape), ("weight", weight, o.shape[-1:])))
-    with _on_device(o):
-        rc = load_library().gdn2_gated_norm_fwd(_ptr(o), _ptr(gate), _ptr(weight), _ptr(y), _rows(o), o.shape[-1], code,
-                                                float(eps), dt, _stream(stream))
-    if rc != 0:
-        raise GDN2Error(rc, "gdn2_gated_norm_fwd")
+    _given(y)
+    _native().gated_norm_fwd(o, gate, weight, y, _gate_code(act), eps, stream)
 
 
 def gdn2_gated_norm_bwd(o, gate, weight, dy, do, dgate, dweight, act="silu", eps=1e-6, workspace=None,
                         stream=None) -> None:
     """Gradients of gdn2_gated_norm_fwd (include/gdn2.h): do, dgate in the token dtype, dweight fp32."""
-    _check_cuda(o, gate, weight, dy, do, dgate, dweight, workspace)
-    dt, code = _dtype_code(o), _gate_code(act)
-    _check_f32((("weight", weight), ("dweight", dweight)))
-    _check_dtypes(o, (("gate", gate), ("dy", dy), ("do", do), ("dgate", dgate)))
-    shp, d_v = o.shape, o.shape[-1]
-    _check_shapes((("gate", gate, shp), ("dy", dy, shp), ("do", do, shp), ("dgate", dgate, shp),
-                   ("weight", weight, (d_v,)), ("dweight", dweight, (d_v,))))
-    if workspace is None:
-        workspace = new_workspace(gdn2_gated_norm_bwd_workspace_bytes(_rows(o), d_v), o.device)
-    with _on_device(o):
-        rc = load_library().gdn2_gated_norm_bwd(*(_ptr(t) for t in (o, gate, weight, dy, do, dgate, dweight)), _rows(o),
-                                                d_v, code, float(eps), dt, _ptr(workspace),
-                                                workspace.numel() * workspace.element_size(), _stream(stream))
-    if rc != 0:
-        raise GDN2Error(rc, "gdn2_gated_norm_bwd")
+    _given(do, dgate, dweight)
+    _native().gated_norm_bwd(o, gate, weight, dy, do, dgate, dweight, _gate_code(act), eps,
+                             _gated_workspace(o) if workspace is None else workspace, stream)
 
 
 def gdn2_add_norm_fwd(x, residual, scale, weight, h, y, eps=1e-6, stream=None) -> None:
     """h = residual + scale * x, y = RMSNorm(h) * weight over the last axis (include/gdn2.h,
     gdn2_add_norm_fwd).  residual, scale and h may be None (zero, one, not stored)."""
-    _check_cuda(x, residual, scale, weight, h, y)
-    dt, width = _dtype_code(x), x.shape[-1]
-    _check_f32((("scale", scale), ("weight", weight)))
-    _check_dtypes(x, (("residual", residual), ("h", h), ("y", y)))
-    _check_shapes((("residual", residual, x.shape), ("h", h, x.shape), ("y", y, x.shape), ("scale", scale, (width,)),
-                   ("weight", weight, (width,))))
-    with _on_device(x):
-        rc = load_library().gdn2_add_norm_fwd(*(_ptr(t) for t in (x, residual, scale, weight, h, y)), _rows(x), width,
-                                              float(eps), dt, _stream(stream))
-    if rc != 0:
-        raise GDN2Error(rc, "gdn2_add_norm_fwd")
+    _native().add_norm_fwd(x, residual, scale, weight, h, y, False, eps, stream)
 
 
 def gdn2_add_norm_bwd(h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweight, eps=1e-6, workspace=None,
                       stream=None) -> None:
     """Gradients of gdn2_add_norm_fwd at the stored h (include/gdn2.h).  dh may be None (zero); without a
     scale, x, dx and dscale are not used (dx equals dresidual)."""
-    _check_cuda(h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweight, workspace)
-    dt, shp, width = _dtype_code(h), h.shape, h.shape[-1]
-    _check_f32((("scale", scale), ("weight", weight), ("dscale", dscale), ("dweight", dweight)))
-    _check_dtypes(h, (("x", x), ("dy", dy), ("dh", dh), ("dresidual", dresidual), ("dx", dx)))
-    _check_shapes((("x", x, shp), ("dy", dy, shp), ("dh", dh, shp), ("dresidual", dresidual, shp), ("dx", dx, shp),
-                   ("scale", scale, (width,)), ("weight", weight, (width,)), ("dscale", dscale, (width,)),
-                   ("dweight", dweight, (width,))))
-    if workspace is None:
-        workspace = new_workspace(gdn2_add_norm_bwd_workspace_bytes(_rows(h), width), h.device)
-    with _on_device(h):
-        rc = load_library().gdn2_add_norm_bwd(*(_ptr(t) for t in (h, x, scale, weight, dy, dh, dresidual, dx, dscale,
-                                                                  dweight)), _rows(h), width, float(eps), dt,
-                                              _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                              _stream(stream))
-    if rc != 0:
-        raise GDN2Error(rc, "gdn2_add_norm_bwd")
-
-
-def _check_pool(S, H, K, V, device) -> int:
-    """The slot stride of a state cache [slots, H, d_k, d_v]: each slot contiguous, the slots any
-    distance apart (one layer's part of a larger pool)."""
-    import torch
-    if not S.is_cuda or S.device != device:
-        raise ValueError(f"the state cache must be a CUDA tensor on {device}")
-    if S.dtype != torch.float32:
-        raise TypeError("the state cache must be float32")
-    if S.dim() != 4 or tuple(S.shape[1:]) != (H, K, V):
-        raise ValueError(f"the state cache has shape {tuple(S.shape)}, expected (slots, {H}, {K}, {V})")
-    return _slot_stride(S)
-
-
-def _slot_stride(S) -> int:
-    floats = 1
-    for n in S.shape[1:]:
-        floats *= n
-    if S.shape[0] == 0 or floats == 0:
-        return floats
-    if not S[0].is_contiguous() or (S.shape[0] > 1 and S.stride(0) < floats):
-        raise ValueError("each slot of the state cache must be contiguous and overlap no other")
-    return S.stride(0) if S.shape[0] > 1 else floats
+    _native().add_norm_bwd(h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweight, eps,
+                           _add_workspace(h) if workspace is None else workspace, stream)
 
 
 def gdn2_tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, o, max_nodes, workspace=None,
@@ -541,28 +484,11 @@ def gdn2_tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, o, max_node
     """Read-out of every node of every drafted tree over the state cache S [slots, H, d_k, d_v], which is
     unchanged (include/gdn2.h, gdn2_tree_fwd).  q, k, b, alpha [total, H, d_k]; v, w, o [total, H, d_v];
     slots [batch], cu_nodes [batch + 1], parents [total] int32 on the device; max_nodes: the most nodes of
-    a tree, at most TREE_MAX_NODES.  Malformed indices are reported in the workspace's status."""
-    _check_cuda(q, k, v, alpha, b, w, slots, cu_nodes, parents, o, workspace)
-    total, H, K = q.shape
-    V = v.shape[-1]
-    dt = _dtype_code(q)
-    _check_f32((("alpha", alpha),))
-    _check_dtypes(q, (("k", k), ("b", b), ("v", v), ("w", w), ("o", o)))
-    tk, tv = (total, H, K), (total, H, V)
-    _check_shapes((("k", k, tk), ("b", b, tk), ("alpha", alpha, tk), ("v", v, tv), ("w", w, tv), ("o", o, tv)))
-    _check_i32((("slots", slots), ("cu_nodes", cu_nodes), ("parents", parents)))
-    batch = slots.shape[0]
-    _check_shapes((("cu_nodes", cu_nodes, (batch + 1,)), ("parents", parents, (total,))))
-    stride = _check_pool(S, H, K, V, q.device)
-    if workspace is None:
-        workspace = new_workspace(0, q.device)
-    with _on_device(q):
-        rc = load_library().gdn2_tree_fwd(*(_ptr(t) for t in (q, k, v, alpha, b, w, S)), stride, S.shape[0],
-                                          *(_ptr(t) for t in (slots, cu_nodes, parents, o)), batch, H, total,
-                                          int(max_nodes), K, V, dt, _ptr(workspace),
-                                          workspace.numel() * workspace.element_size(), _stream(stream))
-    if rc != 0:
-        raise GDN2Error(rc, "gdn2_tree_fwd")
+    a tree, at most TREE_MAX_NODES.  The slots of S may lie any distance apart (one layer's part of a larger
+    pool).  Malformed indices are reported in the workspace's status."""
+    _given(o)
+    _native().tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, o, max_nodes,
+                       new_workspace(0, q.device) if workspace is None else workspace, stream)
 
 
 def gdn2_recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index, o, workspace=None,
@@ -572,27 +498,8 @@ def gdn2_recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, 
     [rows, H, d_v]; slots_in, slots_out [batch] and cu_tokens [batch + 1] int32 on the device; index [total]
     int32 or None (entry t is row t); o [total, H, d_v] or None (not wanted).  Malformed indices are reported
     in the workspace's status."""
-    _check_cuda(q, k, v, alpha, b, w, slots_in, slots_out, cu_tokens, index, o, workspace)
-    rows, H, K = q.shape
-    V = v.shape[-1]
-    dt = _dtype_code(q)
-    _check_f32((("alpha", alpha),))
-    _check_dtypes(q, (("k", k), ("b", b), ("v", v), ("w", w), ("o", o)))
-    tk, tv = (rows, H, K), (rows, H, V)
-    _check_i32((("slots_in", slots_in), ("slots_out", slots_out), ("cu_tokens", cu_tokens), ("index", index)))
-    batch, total = slots_in.shape[0], rows if index is None else index.shape[0]
-    _check_shapes((("k", k, tk), ("b", b, tk), ("alpha", alpha, tk), ("v", v, tv), ("w", w, tv),
-                   ("o", o, (total, H, V)), ("slots_out", slots_out, (batch,)), ("cu_tokens", cu_tokens, (batch + 1,))))
-    stride = _check_pool(S, H, K, V, q.device)
-    if workspace is None:
-        workspace = new_workspace(0, q.device)
-    with _on_device(q):
-        rc = load_library().gdn2_recurrent_fwd(*(_ptr(t) for t in (q, k, v, alpha, b, w, S)), stride, S.shape[0],
-                                               *(_ptr(t) for t in (slots_in, slots_out, cu_tokens, index, o)), batch,
-                                               H, total, rows, K, V, dt, _ptr(workspace),
-                                               workspace.numel() * workspace.element_size(), _stream(stream))
-    if rc != 0:
-        raise GDN2Error(rc, "gdn2_recurrent_fwd")
+    _native().recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index, o, False,
+                            new_workspace(0, q.device) if workspace is None else workspace, stream)
 
 
 def gdn2_state_copy(dst, src, dst_index, src_index, workspace=None, stream=None) -> None:
@@ -600,27 +507,13 @@ def gdn2_state_copy(dst, src, dst_index, src_index, workspace=None, stream=None)
     (include/gdn2.h, gdn2_state_copy): fork, compact, reorder and clear slots of a state cache.  dst, src:
     fp32 caches [slots, ...] with equal slot shapes, one cache or two that do not overlap; the indices int32
     on the device, at most STATE_COPY_MAX_PAIRS."""
-    _check_cuda(dst_index, src_index, workspace)
-    _check_i32((("dst_index", dst_index), ("src_index", src_index)))
-    _check_shapes((("src_index", src_index, dst_index.shape),))
-    _check_f32((("dst", dst), ("src", src)))
-    for t in (dst, src):
-        if not t.is_cuda or t.device != dst_index.device:
-            raise ValueError(f"the state caches must be CUDA tensors on {dst_index.device}")
-    if dst.dim() < 2 or tuple(dst.shape[1:]) != tuple(src.shape[1:]):
-        raise ValueError(f"slots of shape {tuple(dst.shape[1:])} and {tuple(src.shape[1:])}: expected equal ones")
-    floats = 1
-    for n in dst.shape[1:]:
-        floats *= n
-    if workspace is None:
-        workspace = new_workspace(0, dst.device)
-    with _on_device(dst):
-        rc = load_library().gdn2_state_copy(_ptr(dst), _slot_stride(dst), dst.shape[0], _ptr(src), _slot_stride(src),
-                                            src.shape[0], _ptr(dst_index), _ptr(src_index), dst_index.shape[0], floats,
-                                            _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                            _stream(stream))
-    if rc != 0:
-        raise GDN2Error(rc, "gdn2_state_copy")
+    _native().state_copy(dst, src, dst_index, src_index,
+                         new_workspace(0, dst.device) if workspace is None else workspace, stream)
+
+
+def _given(*outputs):
+    if any(t is None for t in outputs):
+        raise TypeError("the outputs must be tensors")
 
 
 def gdn2_gemm_phase_probe(mode, reps, nctas, workspace, stream=None) -> None:
@@ -666,26 +559,18 @@ def decode_step(q, k, v, alpha, b, w, S, stream=None):
 
 def gated_norm_fwd(o, gate, weight, act="silu", eps=1e-6, stream=None):
     """Allocating convenience wrapper: returns y."""
-    import torch
-    y = torch.empty_like(o)
-    gdn2_gated_norm_fwd(o, gate, weight, y, act=act, eps=eps, stream=stream)
-    return y
+    return _native().gated_norm_fwd(o, gate, weight, None, _gate_code(act), eps, stream)
 
 
 def gated_norm_bwd(o, gate, weight, dy, act="silu", eps=1e-6, workspace=None, stream=None):
     """Allocating convenience wrapper: returns (do, dgate, dweight)."""
-    import torch
-    do, dgate, dweight = torch.empty_like(o), torch.empty_like(gate), torch.empty_like(weight)
-    gdn2_gated_norm_bwd(o, gate, weight, dy, do, dgate, dweight, act=act, eps=eps, workspace=workspace, stream=stream)
-    return do, dgate, dweight
+    return _native().gated_norm_bwd(o, gate, weight, dy, None, None, None, _gate_code(act), eps,
+                                    _gated_workspace(o) if workspace is None else workspace, stream)
 
 
 def add_norm_fwd(x, residual, scale, weight, eps=1e-6, stream=None):
     """Allocating convenience wrapper: returns (y, h)."""
-    import torch
-    y, h = torch.empty_like(x), torch.empty_like(x)
-    gdn2_add_norm_fwd(x, residual, scale, weight, h, y, eps=eps, stream=stream)
-    return y, h
+    return _native().add_norm_fwd(x, residual, scale, weight, None, None, True, eps, stream)
 
 
 def add_norm_bwd(h, x, scale, weight, dy, dh=None, eps=1e-6, workspace=None, stream=None):
@@ -701,21 +586,15 @@ def add_norm_bwd(h, x, scale, weight, dy, dh=None, eps=1e-6, workspace=None, str
 
 def tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, max_nodes, workspace=None, stream=None):
     """Allocating convenience wrapper of gdn2_tree_fwd: returns o (rows of no tree hold no values)."""
-    import torch
-    o = torch.empty_like(v)
-    gdn2_tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, o, max_nodes, workspace=workspace, stream=stream)
-    return o
+    return _native().tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, None, max_nodes,
+                              new_workspace(0, q.device) if workspace is None else workspace, stream)
 
 
 def recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index=None, workspace=None, stream=None):
     """Allocating convenience wrapper of gdn2_recurrent_fwd: updates S, returns o by entry (entries of no
     sequence hold no values)."""
-    import torch
-    total = q.shape[0] if index is None else index.shape[0]
-    o = torch.empty((total, *v.shape[1:]), dtype=v.dtype, device=v.device)
-    gdn2_recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index, o, workspace=workspace,
-                       stream=stream)
-    return o
+    return _native().recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index, None, True,
+                                   new_workspace(0, q.device) if workspace is None else workspace, stream)
 
 
 def _recurrence_function():

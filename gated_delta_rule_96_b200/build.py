@@ -1,4 +1,5 @@
-"""Build libgdn2.so (the C-ABI library) in-tree with nvcc for sm_100a."""
+"""Build libgdn2.so (the C-ABI library) in-tree with nvcc for sm_100a, and _gdn2_torch.so (the native half of
+the Python binding) with the host compiler."""
 from __future__ import annotations
 
 import glob
@@ -11,6 +12,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgdn2.so")
+TORCH_SOURCE = os.path.join(CSRC, "gdn2_torch.cpp")
+TORCH_LIB = os.path.join(HERE, "_gdn2_torch.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -56,5 +59,31 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     return LIB
 
 
+def build_torch(force: bool = False, verbose: bool = False) -> str:
+    """The native half of the binding, against the installed torch; it loads libgdn2.so at run time."""
+    if not force and not _stale(TORCH_LIB, [TORCH_SOURCE, os.path.join(INCLUDE, "gdn2.h")]):
+        return TORCH_LIB
+    import shutil
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    nvcc = shutil.which(os.environ.get("NVCC", "nvcc")) or "/usr/local/cuda/bin/nvcc"
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    tmp = TORCH_LIB + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), TORCH_SOURCE, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath," + os.path.join(root, "lib")]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.check_call(cmd)
+    os.replace(tmp, TORCH_LIB)
+    return TORCH_LIB
+
+
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose=True))
+    print(build_torch(force="--force" in sys.argv, verbose=True))

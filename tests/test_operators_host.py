@@ -1,12 +1,11 @@
 """Argument checks of the norms and of the operators over a state cache, on the CPU: the C entry points
-refuse before they touch the device, and the binding marshals its tensors in the declared order."""
+refuse before they touch the device, and the binding names what is wrong with a tensor."""
 import ctypes
 
 import pytest
 import torch
 
 import gated_delta_rule_96_b200 as g
-from tests.test_binding_host import addr, rec  # noqa: F401  (the recorder fixture)
 
 P = ctypes.c_void_p
 F = P(0x10000)       # never dereferenced: every call below fails validation first or has nothing to do
@@ -100,78 +99,95 @@ def test_workspace_sizes():
     assert g.gdn2_add_norm_bwd_workspace_bytes(1 << 40, 8192) <= 256 + 592 * 2 * 8192 * 4
 
 
-def test_norm_marshalling(rec):  # noqa: F811
-    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
-    o, gate, y, dy, do, dg = (bf(2, 3, 4, 64) for _ in range(6))
-    w, dw = torch.ones(64), torch.zeros(64)
-    g.gdn2_gated_norm_fwd(o, gate, w, y, act="sigmoid", eps=1e-5)
-    name, a = rec.calls[-1]
-    assert name == "gdn2_gated_norm_fwd" and [addr(p) for p in a[:4]] == [t.data_ptr() for t in (o, gate, w, y)]
-    assert a[4:7] == (24, 64, 1) and a[7] == 1e-5 and a[8] == g.GDN2_BF16
-    g.gdn2_gated_norm_bwd(o, gate, w, dy, do, dg, dw)
-    name, a = rec.calls[-1]
-    assert [addr(p) for p in a[:7]] == [t.data_ptr() for t in (o, gate, w, dy, do, dg, dw)]
-    assert a[7:10] == (24, 64, 0) and a[13] >= g.gdn2_gated_norm_bwd_workspace_bytes(24, 64)
-    with pytest.raises(ValueError):
-        g.gdn2_gated_norm_fwd(o, gate, w, y, act="tanh")
-    with pytest.raises(TypeError):
-        g.gdn2_gated_norm_fwd(o, gate.float(), w, y)
-    with pytest.raises(ValueError):
-        g.gdn2_gated_norm_fwd(o, gate, torch.ones(128), y)
+# The binding: types and shapes are refused first, wherever the tensors are, then tensors that are not on the GPU.
 
-    x, r, h, y, dy, dh, dr, dx = (torch.zeros(5, 96) for _ in range(8))
-    s, w, ds, dw = (torch.ones(96) for _ in range(4))
-    g.gdn2_add_norm_fwd(x, None, s, w, None, y)
-    _, a = rec.calls[-1]
-    assert [addr(p) for p in a[:6]] == [x.data_ptr(), None, s.data_ptr(), w.data_ptr(), None, y.data_ptr()]
-    assert a[6:8] == (5, 96) and a[9] == g.GDN2_F32
-    g.gdn2_add_norm_bwd(h, x, s, w, dy, None, dr, dx, ds, dw)
-    _, a = rec.calls[-1]
-    assert [addr(p) for p in a[:10]] == [h.data_ptr(), x.data_ptr(), s.data_ptr(), w.data_ptr(), dy.data_ptr(), None,
-                                         dr.data_ptr(), dx.data_ptr(), ds.data_ptr(), dw.data_ptr()]
-    with pytest.raises(ValueError):
-        g.gdn2_add_norm_fwd(x, r[:4], s, w, h, y)
-    with pytest.raises(TypeError):
-        g.gdn2_add_norm_bwd(h, x, s, w.bfloat16(), dy, None, dr, dx, ds, dw)
+BF = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+I32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+NO_CUDA = "must be CUDA tensors"
 
 
-def test_slot_marshalling(rec, monkeypatch):  # noqa: F811
-    monkeypatch.setattr(g, "_check_pool", lambda S, H, K, V, device: g._slot_stride(S))
-    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
-    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
-    n, H, K, V = 6, 2, 128, 64
-    q, k, b, v, w, o = bf(n, H, K), bf(n, H, K), bf(n, H, K), bf(n, H, V), bf(n, H, V), bf(n, H, V)
-    alpha, pool = torch.zeros(n, H, K), torch.zeros(4, 3, H, K, V)
-    layer = pool[:, 1]                       # one layer's part: slots a layer apart
-    slots, cu, par = i32(3, 0), i32(0, 4, 6), i32(-1, 0, 0, 1, -1, -1)
-    g.gdn2_tree_fwd(q, k, v, alpha, b, w, layer, slots, cu, par, o, 4)
-    name, a = rec.calls[-1]
-    assert name == "gdn2_tree_fwd"
-    assert [addr(p) for p in a[:7]] == [t.data_ptr() for t in (q, k, v, alpha, b, w, layer)]
-    assert a[7:9] == (3 * H * K * V, 4) and [addr(p) for p in a[9:13]] == [t.data_ptr() for t in (slots, cu, par, o)]
-    assert a[13:20] == (2, H, n, 4, K, V, g.GDN2_BF16) and a[21] >= 256
-    index = i32(5, 4, 0)
-    cu = i32(0, 1, 3)
-    o = bf(3, H, V)
-    g.gdn2_recurrent_fwd(q, k, v, alpha, b, w, layer, slots, slots, cu, index, o)
-    _, a = rec.calls[-1]
-    assert [addr(p) for p in a[9:14]] == [t.data_ptr() for t in (slots, slots, cu, index, o)]
-    assert a[14:21] == (2, H, 3, n, K, V, g.GDN2_BF16)
-    with pytest.raises(ValueError):
-        g.gdn2_recurrent_fwd(q, k, v, alpha, b, w, layer, slots, slots, cu, None, o)     # o is not one row an entry
-    with pytest.raises(TypeError):
-        g.gdn2_recurrent_fwd(q, k, v, alpha, b, w, layer, slots.long(), slots, cu, index, o)
-    with pytest.raises(ValueError):
-        g.gdn2_tree_fwd(q, k, v, alpha, b, w, layer, slots, cu[:2], par, bf(n, H, V), 4)
+def norm_args(**change):
+    a = dict(o=BF(2, 3, 64), gate=BF(2, 3, 64), weight=torch.ones(64), y=BF(2, 3, 64))
+    return g.gdn2_gated_norm_fwd(**(a | change))
 
 
-def test_slot_stride_refuses_overlap():
-    pool = torch.zeros(4, 2, 64, 64)
-    assert g._slot_stride(pool) == 2 * 64 * 64 and g._slot_stride(pool[::2]) == 4 * 64 * 64
-    with pytest.raises(ValueError):
-        g._slot_stride(pool[:1].expand(4, 2, 64, 64))
-    with pytest.raises(ValueError):
-        g._slot_stride(pool.transpose(2, 3))
+def norm_bwd_args(**change):
+    a = dict(o=BF(6, 64), gate=BF(6, 64), weight=torch.ones(64), dy=BF(6, 64), do=BF(6, 64), dgate=BF(6, 64),
+             dweight=torch.ones(64), workspace=torch.zeros(256, dtype=torch.uint8))
+    return g.gdn2_gated_norm_bwd(**(a | change))
+
+
+def add_args(**change):
+    a = dict(x=torch.zeros(5, 96), residual=None, scale=None, weight=torch.ones(96), h=None, y=torch.zeros(5, 96))
+    return g.gdn2_add_norm_fwd(**(a | change))
+
+
+def add_bwd_args(**change):
+    z, one = torch.zeros(5, 96), torch.ones(96)
+    a = dict(h=z, x=z, scale=one, weight=one, dy=z, dh=None, dresidual=z, dx=z, dscale=one, dweight=one,
+             workspace=torch.zeros(256, dtype=torch.uint8))
+    return g.gdn2_add_norm_bwd(**(a | change))
+
+
+def token_args(n=6, H=2, K=128, V=64):
+    return dict(q=BF(n, H, K), k=BF(n, H, K), v=BF(n, H, V), alpha=torch.zeros(n, H, K), b=BF(n, H, K), w=BF(n, H, V),
+                S=torch.zeros(4, 3, H, K, V)[:, 1], workspace=torch.zeros(256, dtype=torch.uint8))
+
+
+def tree_args(**change):
+    a = token_args() | dict(slots=I32(3, 0), cu_nodes=I32(0, 4, 6), parents=I32(-1, 0, 0, 1, -1, -1), o=BF(6, 2, 64),
+                            max_nodes=4)
+    return g.gdn2_tree_fwd(**(a | change))
+
+
+def recurrent_args(**change):
+    a = token_args() | dict(slots_in=I32(3, 0), slots_out=I32(1, 0), cu_tokens=I32(0, 1, 3), index=I32(5, 4, 0), o=BF(3, 2, 64))
+    return g.gdn2_recurrent_fwd(**(a | change))
+
+
+def copy_args(**change):
+    a = dict(dst=torch.zeros(4, 2, 64), src=torch.zeros(9, 2, 64), dst_index=I32(0, 1), src_index=I32(5, -1),
+             workspace=torch.zeros(256, dtype=torch.uint8))
+    return g.gdn2_state_copy(**(a | change))
+
+
+@pytest.mark.parametrize("call,change,error,text", [
+    (norm_args, {}, ValueError, NO_CUDA), (norm_args, {"act": "tanh"}, ValueError, "act must be one of"),
+    (norm_args, {"gate": torch.zeros(2, 3, 64)}, TypeError, "gate must be bfloat16"),
+    (norm_args, {"weight": torch.ones(128)}, ValueError, "weight has shape"),
+    (norm_args, {"weight": BF(64)}, TypeError, "weight must be float32"),
+    (norm_args, {"o": torch.zeros(2, 3, 64, dtype=torch.float16)}, TypeError, "bfloat16 or float32"),
+    (norm_args, {"y": None}, TypeError, "outputs"), (norm_args, {"y": BF(6, 64)}, ValueError, "y has shape"),
+    (norm_args, {"o": 3}, TypeError, "o must be a tensor"), (norm_args, {"eps": "a"}, TypeError, "real number"),
+    (norm_bwd_args, {}, ValueError, NO_CUDA), (norm_bwd_args, {"dweight": BF(64)}, TypeError, "dweight must be float32"),
+    (norm_bwd_args, {"dgate": BF(6, 32)}, ValueError, "dgate has shape"),
+    (norm_bwd_args, {"do": None}, TypeError, "outputs"),
+    (add_args, {}, ValueError, NO_CUDA), (add_args, {"residual": torch.zeros(4, 96)}, ValueError, "residual has shape"),
+    (add_args, {"h": BF(5, 96)}, TypeError, "h must be float32"), (add_args, {"y": None}, TypeError, "y must be a tensor"),
+    (add_args, {"scale": torch.ones(95)}, ValueError, "scale has shape"),
+    (add_bwd_args, {}, ValueError, NO_CUDA), (add_bwd_args, {"weight": BF(96)}, TypeError, "weight must be float32"),
+    (add_bwd_args, {"dh": torch.zeros(5, 95)}, ValueError, "dh has shape"),
+    (tree_args, {}, ValueError, NO_CUDA), (tree_args, {"cu_nodes": I32(0, 4)}, ValueError, "cu_nodes has shape"),
+    (tree_args, {"parents": I32(-1)}, ValueError, "parents has shape"),
+    (tree_args, {"slots": torch.zeros(2, dtype=torch.int64)}, TypeError, "slots must be a one-dimensional int32"),
+    (tree_args, {"S": torch.zeros(4, 2, 64, 128)}, ValueError, "S has shape"),
+    (tree_args, {"S": BF(4, 2, 128, 64)}, TypeError, "S must be float32"),
+    (tree_args, {"S": torch.zeros(1, 2, 128, 64).expand(4, 2, 128, 64)}, ValueError, "must not overlap"),
+    (tree_args, {"S": torch.zeros(4, 2, 64, 128).transpose(2, 3)}, ValueError, "must be contiguous"),
+    (tree_args, {"k": BF(6, 2, 64)}, ValueError, "k has shape"), (tree_args, {"v": BF(6, 2)}, ValueError, "v has shape"),
+    (tree_args, {"alpha": BF(6, 2, 128)}, TypeError, "alpha must be float32"), (tree_args, {"o": None}, TypeError, "outputs"),
+    (tree_args, {"max_nodes": 1 << 40}, ValueError, "max_nodes"), (tree_args, {"max_nodes": 1.5}, TypeError, "integer"),
+    (recurrent_args, {}, ValueError, NO_CUDA), (recurrent_args, {"index": None}, ValueError, "o has shape"),
+    (recurrent_args, {"o": None}, ValueError, NO_CUDA),
+    (recurrent_args, {"slots_out": I32(1)}, ValueError, "slots_out has shape"),
+    (recurrent_args, {"cu_tokens": I32(0, 1)}, ValueError, "cu_tokens has shape"),
+    (copy_args, {}, ValueError, NO_CUDA), (copy_args, {"src": torch.zeros(9, 2, 32)}, ValueError, "src has shape"),
+    (copy_args, {"src_index": I32(0)}, ValueError, "src_index has shape"),
+    (copy_args, {"dst": torch.zeros(4)}, ValueError, "dst has shape"), (copy_args, {"dst": BF(4, 2, 64)}, TypeError, "float32"),
+])
+def test_binding_refuses(call, change, error, text):
+    with pytest.raises(error, match=text):
+        call(**change)
 
 
 def test_cpu_tensors_are_refused():
