@@ -40,7 +40,7 @@ template <int K, int V>
 constexpr int PRODUCERS = K == 128 && V == 128 ? 2 : 4;
 constexpr int DEPTH = 2;       // state buffers: one worked on, one on its way in or out
 constexpr int RING = 6;        // token blocks ahead
-constexpr uint32_t WAIT_LIMIT = 1u << 26;
+constexpr uint32_t WAIT_LIMIT = 1u << 21;   // polls, a second or more
 
 template <int K, int V>
 struct Block {
@@ -270,6 +270,8 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
     const int *__restrict__ index, Tok *__restrict__ o, int batch, int H, int splits, int total, int rows,
     unsigned *status) {
     constexpr int RJ = K / 32, NP = PRODUCERS<K, V>;
+    // a producer waits for a ring slot's last use by its parity: it must not be two uses ahead of the consumers
+    static_assert(RING >= NP, "each producer's blocks are NP apart");
     extern __shared__ __align__(128) unsigned char raw[];
     Shared<K, V> &sh = *reinterpret_cast<Shared<K, V> *>(raw);
     float *buffers = reinterpret_cast<float *>(raw + sizeof(Shared<K, V>));

@@ -21,7 +21,7 @@ namespace copy {
 using namespace gdn2::tc;
 
 constexpr int THREADS = 128, RANGE = 256, GROUP = 12;   // 16-byte vectors of a piece, pairs of a block
-constexpr uint32_t WAIT_LIMIT = 1u << 24;
+constexpr uint32_t WAIT_LIMIT = 1u << 20;
 
 // Shared memory: mbarrier (16 bytes), RANGE zeros, the states, the pairs, the table of destinations.
 struct Layout {

@@ -20,7 +20,7 @@ namespace tree {
 // The kernel on CUDA cores, any type and size.  One block per (column range, head, sequence); the first
 // cols / 16 warps own 16 columns of the state each, every warp takes part in the rest.
 template <typename Tok, int K, int V>
-__global__ void __launch_bounds__(256) tree_kernel(const Tok *__restrict__ q, const Tok *__restrict__ k,
+__global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q, const Tok *__restrict__ k,
                                                    const Tok *__restrict__ v, const float *__restrict__ alpha,
                                                    const Tok *__restrict__ b, const Tok *__restrict__ w,
                                                    const float *__restrict__ S, long long slot_stride, int num_slots,
@@ -43,32 +43,40 @@ __global__ void __launch_bounds__(256) tree_kernel(const Tok *__restrict__ q, co
     if (lo < 0 || hi < lo || hi > total || hi - lo > max_nodes) bad = DEV_RANGE;
     else if (slot < -1 || slot >= num_slots) bad = DEV_SLOT;
 
-    // the block's slice of the state is on its way first: rows 4 (rg + 8 j) + i, columns c0 .. c0 + 3
-    const int rg = lane >> 2, c0 = warp * 16 + (lane & 3) * 4;
-    const bool owner = warp * 16 < cols;
+    // Everything that needs no more than the item's place is on its way before the first barrier.
+    // The warp's slice of the state: rows 4 (rg + 8 j) + i, columns c0 .. c0 + 3; where there are more warps than
+    // column groups they share the nodes.
+    const int groups = cols / 16, shares = (nt >> 5) / groups;
+    const int rg = lane >> 2, c0 = warp % groups * 16 + (lane & 3) * 4;
     float s[RJ][4][4];
 #pragma unroll
     for (int j = 0; j < RJ; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (owner && slot >= 0 && !bad)
+            if (slot >= 0 && !bad)
                 x = ld_stream(reinterpret_cast<const float4 *>(S + (size_t)slot * slot_stride + (size_t)head * K * V +
                                                                (size_t)(4 * (rg + 8 * j) + i) * V + col0 + c0));
             s[j][i][0] = x.x; s[j][i][1] = x.y; s[j][i][2] = x.z; s[j][i][3] = x.w;
         }
-    if (!bad && tid < hi - lo) {
+    const int n = bad ? 0 : hi - lo;
+    if (tid < n) {
         const int p = parents[lo + tid];
         if (p < -1 || p >= tid) bad = DEV_PARENT;
         sp[tid] = p;
     }
-    if (__syncthreads_or(bad != 0)) {
-        if (bad) atomicOr(status, bad);
-        return;
-    }
-    const int n = hi - lo;
-    if (n == 0) return;
-
+    Raw<Tok, 4> rk[RJ], rb[RJ], rq[RJ];   // of the lane's node
+    const auto fetch = [&](int node) {
+        const size_t row = ((size_t)(lo + node) * H + head) * K + 4 * (lane & 7);
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) {
+            rk[j].clear();
+            rb[j].clear();
+            rq[j].clear();
+            if (node < n) rk[j].load(k + row + 32 * j), rb[j].load(b + row + 32 * j), rq[j].load(q + row + 32 * j);
+        }
+    };
+    fetch(warp * 4 + (lane >> 3));
 #pragma unroll 4
     for (int i = tid; i < n * (K / 4); i += nt)   // alpha of all nodes, four channels a thread at a time
         *reinterpret_cast<float4 *>(sa + 4 * i) = *reinterpret_cast<const float4 *>(
@@ -84,18 +92,21 @@ __global__ void __launch_bounds__(256) tree_kernel(const Tok *__restrict__ q, co
         rw.get(y);
         *reinterpret_cast<float4 *>(sr + 4 * i) = make_float4(x[0] * y[0], x[1] * y[1], x[2] * y[2], x[3] * y[3]);
     }
+    if (__syncthreads_or(bad != 0)) {
+        if (bad) atomicOr(status, bad);
+        return;
+    }
+    if (n == 0) return;
+    if (tid < n) depth[tid] = (unsigned char)list_path(sp, anc, tid);
     __syncthreads();
     for (int n0 = warp * 4; n0 < n; n0 += nt / 8) {
         const int node = n0 + (lane >> 3), sub = lane & 7;
-        const size_t row = ((size_t)(lo + (node < n ? node : 0)) * H + head) * K + 4 * sub;
-        Raw<Tok, 4> rk[RJ], rb[RJ], rq[RJ];
-#pragma unroll
-        for (int j = 0; j < RJ; ++j) rk[j].load(k + row + 32 * j), rb[j].load(b + row + 32 * j), rq[j].load(q + row + 32 * j);
+        if (n0 >= nt / 8) fetch(node);
         f32x2 G[RJ][2];
-        const int above = climb<K>(sa, sp, anc, node, n, lane, G);
+        climb<K>(sa, anc, node < n, node, node < n ? depth[node] : -1, lane, G);
         const bool good = in_range<K>(G, lane);
         if (node < n) {
-            if (sub == 0) depth[node] = (unsigned char)above, fine[node] = good;
+            if (sub == 0) fine[node] = good;
 #pragma unroll
             for (int j = 0; j < RJ; ++j) {
                 const int at = node * K + 4 * (sub + 8 * j);
@@ -131,34 +142,33 @@ __global__ void __launch_bounds__(256) tree_kernel(const Tok *__restrict__ q, co
     __syncthreads();
     for (int n0 = warp * 4; n0 < n; n0 += nt / 8) {
         const int node = n0 + (lane >> 3);
-        eliminate(cA, cP, anc, cP, node, n, node < n ? depth[node] : 0, lane);
+        eliminate(cA, cP, anc, cP, node < n, node, node < n ? depth[node] : 0, lane);
     }
 
     // S^T (e G) and S^T (q G) of every node
-    if (owner)
 #pragma unroll 2
-        for (int t = 0; t < n; ++t) {
-            float p[8];
+    for (int t = warp / groups; t < n; t += shares) {
+        float p[8];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) p[c] = 0.f;
+        for (int c = 0; c < 8; ++c) p[c] = 0.f;
 #pragma unroll
-            for (int j = 0; j < RJ; ++j) {
-                const float4 e4 = *reinterpret_cast<const float4 *>(se + t * K + 4 * (rg + 8 * j));
-                const float4 q4 = *reinterpret_cast<const float4 *>(sq + t * K + 4 * (rg + 8 * j));
-                const float ee[4] = {e4.x, e4.y, e4.z, e4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
+        for (int j = 0; j < RJ; ++j) {
+            const float4 e4 = *reinterpret_cast<const float4 *>(se + t * K + 4 * (rg + 8 * j));
+            const float4 q4 = *reinterpret_cast<const float4 *>(sq + t * K + 4 * (rg + 8 * j));
+            const float ee[4] = {e4.x, e4.y, e4.z, e4.w}, qq[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        p[c] = fmaf(ee[i], s[j][i][c], p[c]);
-                        p[4 + c] = fmaf(qq[i], s[j][i][c], p[4 + c]);
-                    }
-            }
-            const float sum = scatter_sum8(p, lane);   // of p[rg]
-            const int at = t * cols + c0 + (rg & 3);
-            if (rg < 4) sr[at] -= sum;
-            else ss[at] = sum;
+                for (int c = 0; c < 4; ++c) {
+                    p[c] = fmaf(ee[i], s[j][i][c], p[c]);
+                    p[4 + c] = fmaf(qq[i], s[j][i][c], p[4 + c]);
+                }
         }
+        const float sum = scatter_sum8(p, lane);   // of p[rg]
+        const int at = t * cols + c0 + (rg & 3);
+        if (rg < 4) sr[at] -= sum;
+        else ss[at] = sum;
+    }
     __syncthreads();
 
     // o: four columns a thread, the nodes in turn over the block
@@ -198,8 +208,15 @@ int launch_t(const void *q, const void *k, const void *v, const float *alpha, co
     return launch_status();
 }
 
-// The tensor-core kernel where it is faster: TODO
-bool use_tc(int batch, int H, int max_nodes) { return max_nodes > 4; }
+// Which kernel: the tensor-core one's period for an item hardly depends on its nodes (5.3 us an SM for one, 12.5
+// for 64), this one's grows with them and is half of it for one; H16, us, this / that:
+//   one user      8 nodes  7.0 / 9.0   16 nodes   8.6 / 10.1   32 nodes  14.8 / 12.7   64 nodes  27.7 / 17.7
+//   4 users       8 nodes  9.3 / 9.9   16 nodes  12.3 / 10.4
+//   32 users      8 nodes 24.9 / 28.2  16 nodes  38.1 / 32.0   32 nodes  77.0 / 42.5
+//   128 users     8 nodes 96.3 / 91.8  16 nodes 144.3 / 103.2  64 nodes 609.1 / 190.7
+bool use_tc(int batch, int H, int max_nodes) {
+    return max_nodes > 16 || (max_nodes > 8 && (long long)batch * H > 32);
+}
 
 }  // namespace tree
 

@@ -20,8 +20,8 @@ __host__ __device__ constexpr int pairs(int node) { return 4 * (node / 4 + 1) * 
 constexpr int MAX_PAIRS = pairs(MAX_NODES);
 static_assert(pairs(0) == 0 && pairs(1) == 4 && pairs(4) == 16 && pairs(5) == 24 && pairs(64) == 2176, "row starts");
 
-// What follows takes eight lanes a node, four nodes a warp; all lanes of a warp make the calls, with node >= n
-// for none.
+// What follows the paths takes eight lanes a node, four nodes a warp; all lanes of a warp make the calls, and
+// `go` says whether the lane's node takes part (its eight lanes alike).
 
 // A lane's channels are 4 (sub + 8 j) + c, sub = lane & 7.
 
@@ -38,41 +38,43 @@ __device__ __forceinline__ float node_sums(const float (&x)[8], int lane) {
     return (up1 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up1 ? b[0] : b[1], 1);
 }
 
-// The path from a node to its root, whom to anc, and G_n, the product of its decays, at the lane's channels; the
-// number of ancestors is returned.  sa: alpha of all nodes in shared memory.
-template <int K, typename Parent>
-__device__ __forceinline__ int climb(const float *sa, const Parent *parent, unsigned char *anc, int node, int n, int lane,
-                                     f32x2 (&G)[K / 32][2]) {
-    const int sub = lane & 7;
-    int at = node < n ? node : -1, above = -1, root = 0, out = pairs(at < 0 ? 0 : at);
+// One thread lists the path from a node to its root; the number of ancestors is returned.
+template <typename Parent>
+__device__ __forceinline__ int list_path(const Parent *parent, unsigned char *anc, int node) {
+    int out = pairs(node), at = node, above = -1;
+    for (int up = node; up >= 0; up = parent[up]) {
+        at = up;
+        anc[out++] = (unsigned char)at;
+        ++above;
+    }
+    while (out & 3) anc[out++] = (unsigned char)at;   // behind the root: the root again
+    return above;
+}
+
+// G_n, the product of the decays on a node's path, at the lane's channels.  sa: alpha of all nodes in shared
+// memory.
+template <int K>
+__device__ __forceinline__ void climb(const float *sa, const unsigned char *anc, bool go, int node, int above, int lane,
+                                      f32x2 (&G)[K / 32][2]) {
+    const int sub = lane & 7, base = pairs(go ? node : 0), most = __reduce_max_sync(0xffffffffu, go ? above : -1);
 #pragma unroll
     for (int j = 0; j < K / 32; ++j) G[j][0] = G[j][1] = pack2(1.f, 1.f);
-    while (__any_sync(0xffffffffu, at >= 0)) {
-        const bool some = at >= 0;
-        int whom = 0;
+#pragma unroll 1
+    for (int h = 0; h <= most; h += 4) {
+        if (!go || h > above) continue;
+        const uchar4 whom = *reinterpret_cast<const uchar4 *>(anc + base + h);
+        const int at[4] = {whom.x, whom.y, whom.z, whom.w};
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            if (at >= 0) {
-                const int up = parent[at];
+        for (int s = 0; s < 4; ++s)
+            if (h + s <= above)
 #pragma unroll
                 for (int j = 0; j < K / 32; ++j) {
                     f32x2 aa[2];
-                    load2(sa + at * K + 4 * (sub + 8 * j), aa);
+                    load2(sa + at[s] * K + 4 * (sub + 8 * j), aa);
                     G[j][0] = mul2(G[j][0], aa[0]);
                     G[j][1] = mul2(G[j][1], aa[1]);
                 }
-                root = at;
-                at = up;
-                ++above;
-            }
-            if (s == (sub & 3)) whom = root;
-        }
-        if (some) {
-            if (sub < 4) anc[out + sub] = (unsigned char)whom;   // behind the root: the root again
-            out += 4;
-        }
     }
-    return above;
 }
 
 // Whether G_n and 1 / G_n can stand for themselves: at all the node's channels in [2^-100, 2^100].
@@ -90,8 +92,8 @@ __device__ __forceinline__ bool in_range(const f32x2 (&G)[K / 32][2], int lane) 
 }
 
 // A and P of a node's path, to cA and cP, where all its G are in range:  A[n,i] = sum_c (e_n G_n) (k_i / G_i), two
-// operations a channel, no chain from one ancestor to the next.  sk: k_i / G_i of all nodes in shared memory; e, g:
-// e_n G_n and q_n G_n.  `go`: whether this node takes part (its own eight lanes alike).
+// operations a channel, no chain from one ancestor to the next, and seven shuffles for four pairs.  sk: k_i / G_i of
+// all nodes in shared memory; e, g: e_n G_n and q_n G_n.
 template <int K>
 __device__ __forceinline__ void couple(const float *sk, const unsigned char *anc, float *cA, float *cP, bool go, int node,
                                        int above, int lane, const f32x2 (&e)[K / 32][2], const f32x2 (&g)[K / 32][2]) {
@@ -170,23 +172,37 @@ __device__ __noinline__ void couple_far(const Tok *q, const Tok *k, const Tok *b
 // each pair, in place of two and a barrier for each level of the tree.  Lane `sub` takes j = 8 h + sub; the
 // coefficients of a finished j go to the others by a shuffle, those of finished blocks of eight through
 // shared memory.  The A and P of all nodes must be there; cC may be cP.
-__device__ __forceinline__ void eliminate(const float *cA, const float *cP, const unsigned char *anc, float *cC, int node,
-                                          int n, int above, int lane) {
-    const int sub = lane & 7, base = node < n ? pairs(node) : 0;
-    if (node >= n) above = -1;
+__device__ __forceinline__ void eliminate(const float *cA, const float *cP, const unsigned char *anc, float *cC, bool go,
+                                          int node, int above, int lane) {
+    const int sub = lane & 7, team = lane & 24, base = pairs(go ? node : 0);
+    if (!go) above = -1;
     const int most = __reduce_max_sync(0xffffffffu, above);
+    const auto row = [&](int j) { return j <= above ? pairs(anc[base + j]) : 0; };   // of an ancestor's own A
+#pragma unroll 1
     for (int h = 0; h <= most; h += 8) {
         const int j = h + sub;
         const bool mine = j <= above;
         float c = mine ? cP[base + j] : 0.f, up[8];
-#pragma unroll
-        for (int m = 0; m < 8; ++m) up[m] = mine && m < sub ? cA[pairs(anc[base + h + m]) + sub - m] : 0.f;
-        if (mine)
-#pragma unroll 4
-            for (int m = 0; m < h; ++m) c = fmaf(-cC[base + m], cA[pairs(anc[base + m]) + j - m], c);
+        const int start = row(j);
 #pragma unroll
         for (int m = 0; m < 8; ++m) {
-            const float done = __shfl_sync(0xffffffffu, c, (lane & 24) | m);
+            const int from = __shfl_sync(0xffffffffu, start, team | m);
+            up[m] = mine && m < sub ? cA[from + sub - m] : 0.f;
+        }
+#pragma unroll 1
+        for (int f = 0; f < h; f += 8) {   // finished blocks
+            const int first = row(f + sub);
+            const float done = f + sub <= above ? cC[base + f + sub] : 0.f;
+#pragma unroll
+            for (int m = 0; m < 8; ++m) {
+                const int from = __shfl_sync(0xffffffffu, first, team | m);
+                const float x = __shfl_sync(0xffffffffu, done, team | m);
+                if (mine) c = fmaf(-x, cA[from + j - f - m], c);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            const float done = __shfl_sync(0xffffffffu, c, team | m);
             if (m < sub) c = fmaf(-done, up[m], c);
         }
         if (j <= (above | 3)) cC[base + j] = mine ? c : 0.f;   // with the zeros that fill the row up

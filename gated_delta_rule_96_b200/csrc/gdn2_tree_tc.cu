@@ -27,19 +27,16 @@ constexpr int D = 128;
 constexpr int COLUMN_WARPS = 8, STATE_WARPS = 4, PATH_WARPS = 16;   // in this order; then loader and lead
 constexpr int LOADER = COLUMN_WARPS + STATE_WARPS + PATH_WARPS, LEAD = LOADER + 1, TC_THREADS = 32 * (LEAD + 1);
 constexpr int STAGE_ROWS = 32, STAGES = 2;   // of the state
-constexpr int METAS = 4;
-constexpr uint32_t BAR_COLUMN = 1, BAR_PATH = 2, BAR_STATE = 3, WAIT_LIMIT = 1u << 24;
+constexpr int METAS = 3;
+constexpr uint32_t BAR_COLUMN = 1, BAR_PATH = 2, BAR_STATE = 3, WAIT_LIMIT = 1u << 20;
 constexpr uint32_t TM_S = 0, TM_D = 256, TM_COLS = 512;   // S: two buffers of hi (64 columns) and lo (64)
 
-// An item: its nodes lo .. lo+n-1, their parents, the state's slot.
+// An item: its nodes lo .. lo+n-1, the state's slot, the nodes' parents, paths and numbers of ancestors, and the
+// nodes by that number, the deepest first (so that the nodes of a warp take about as many steps).
 struct Meta {
     int lo, n, slot, head;
     signed char parent[MAX_NODES];
-};
-
-struct Coef {   // eliminate()'s, whom each is for, and how many ancestors a node has
-    float c[MAX_PAIRS];
-    unsigned char anc[MAX_PAIRS], above[MAX_NODES];
+    unsigned char anc[MAX_PAIRS], above[MAX_NODES], order[MAX_NODES];
 };
 
 struct TcShared {
@@ -47,8 +44,7 @@ struct TcShared {
     float stage[STAGES][STAGE_ROWS][D];
     float alpha[MAX_NODES][D];                // then k / G
     float r[MAX_NODES][D], x[MAX_NODES][D];   // u, then R; S^T (q G); by node and value column
-    float a[MAX_PAIRS];
-    Coef coef[2];
+    float a[MAX_PAIRS], c[2][MAX_PAIRS];      // A; P, then C
     Meta meta[METAS];
     unsigned char fine[MAX_NODES];            // whether a node's G is in range
     unsigned long long meta_full[METAS], meta_free[METAS], stage_full[STAGES], stage_free[STAGES], s_full[2], s_free[2],
@@ -67,6 +63,12 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_al
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
     hi = pack_bf16(x, y);
     lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+}
+
+__device__ __forceinline__ float inverse(float x) {   // to one unit of fp32
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
@@ -143,6 +145,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                 n = 0;
             }
             if (lane == 0) m.lo = lo, m.n = n, m.slot = slot, m.head = head;
+            __syncwarp();
+            int above[2] = {-1, -1};
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                if (lane + 32 * r < n) m.above[lane + 32 * r] = (unsigned char)(above[r] = list_path(m.parent, m.anc, lane + 32 * r));
+            int place = 0;
+            for (int l = __reduce_max_sync(0xffffffffu, max(above[0], above[1])); l >= 0; --l)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const unsigned here = __ballot_sync(0xffffffffu, above[r] == l);
+                    if (above[r] == l) m.order[place + __popc(here & ((1u << lane) - 1))] = (unsigned char)(lane + 32 * r);
+                    place += __popc(here);
+                }
             // a line a lane (bulk prefetches of whole rows took 60 cycles each, 24,000 for 64 nodes)
             for (int i = lane; i < 2 * n; i += 32) {
                 const size_t row = ((size_t)(lo + i / 2) * H + head) * D + i % 2 * 64;
@@ -231,27 +246,40 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                 fence_before();
                 arrive(sh.d_free);
                 if (!group_wait(sh.coef_full[c & 1], c >> 1, BAR_COLUMN, 32 * COLUMN_WARPS)) break;
-                const Coef &coef = sh.coef[c & 1];
-                for (int node = warp; node < n; node += COLUMN_WARPS) {   // four columns a lane
-                    const int base = pairs(node), above = coef.above[node];
-                    f32x2 x[2];
-                    load2(&sh.x[node][4 * lane], x);
-                    for (int j = 0; j <= above; j += 4) {
-                        const float4 c4 = *reinterpret_cast<const float4 *>(coef.c + base + j);
-                        const uchar4 a4 = *reinterpret_cast<const uchar4 *>(coef.anc + base + j);
+                // half a warp takes a node: eight columns a lane, 4 l and 64 + 4 l and the three after each
+                for (int i = 2 * warp; i < n; i += 2 * COLUMN_WARPS) {
+                    const bool real = i + (lane >> 4) < n;
+                    const int node = m.order[real ? i + (lane >> 4) : i], base = pairs(node), above = m.above[node];
+                    const int at = 4 * (lane & 15), most = __reduce_max_sync(0xffffffffu, above);
+                    f32x2 x[4];
+                    load2(&sh.x[node][at], reinterpret_cast<f32x2 (&)[2]>(x[0]));
+                    load2(&sh.x[node][64 + at], reinterpret_cast<f32x2 (&)[2]>(x[2]));
+                    for (int j = 0; j <= most; j += 4) {
+                        if (j > above) continue;
+                        const float4 c4 = *reinterpret_cast<const float4 *>(&sh.c[c & 1][base + j]);
+                        const uchar4 a4 = *reinterpret_cast<const uchar4 *>(m.anc + base + j);
                         const float cc[4] = {c4.x, c4.y, c4.z, c4.w};
                         const int from[4] = {a4.x, a4.y, a4.z, a4.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            f32x2 r[2];
-                            load2(&sh.r[from[i]][4 * lane], r);
-                            x[0] = fma2(pack2(cc[i], cc[i]), r[0], x[0]);
-                            x[1] = fma2(pack2(cc[i], cc[i]), r[1], x[1]);
+                        for (int s = 0; s < 4; ++s) {
+                            f32x2 y[2], z[2];
+                            const f32x2 c2 = pack2(cc[s], cc[s]);
+                            load2(&sh.r[from[s]][at], y);
+                            load2(&sh.r[from[s]][64 + at], z);
+                            x[0] = fma2(c2, y[0], x[0]);
+                            x[1] = fma2(c2, y[1], x[1]);
+                            x[2] = fma2(c2, z[0], x[2]);
+                            x[3] = fma2(c2, z[1], x[3]);
                         }
                     }
-                    const float2 x0 = unpack2(x[0]), x1 = unpack2(x[1]);
-                    *reinterpret_cast<uint2 *>(o + first + (size_t)node * H * D + 4 * lane) =
-                        make_uint2(pack_bf16(x0.x, x0.y), pack_bf16(x1.x, x1.y));
+                    if (real) {
+                        __nv_bfloat16 *out = o + first + (size_t)node * H * D + at;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float2 x0 = unpack2(x[2 * h]), x1 = unpack2(x[2 * h + 1]);
+                            *reinterpret_cast<uint2 *>(out + 64 * h) = make_uint2(pack_bf16(x0.x, x0.y), pack_bf16(x1.x, x1.y));
+                        }
+                    }
                 }
                 arrive(sh.coef_free[c & 1]);
                 ++c;
@@ -319,7 +347,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
         }
     } else {
         constexpr int THREADS = 32 * PATH_WARPS;
-        const int t = tid - 32 * (COLUMN_WARPS + STATE_WARPS), sub = lane & 7, node = t >> 3;
+        const int t = tid - 32 * (COLUMN_WARPS + STATE_WARPS), sub = lane & 7;
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
             if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_PATH, THREADS)) break;
@@ -330,23 +358,28 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                 const size_t first = ((size_t)lo * H + head) * D;
                 for (int i = t; i < n * (D / 4); i += THREADS)   // group_wait's barrier is behind the last item's reads
                     cp_async16(smem_u32(&sh.alpha[0][0]) + 16 * i, alpha + first + (size_t)(i / (D / 4)) * H * D + i % (D / 4) * 4);
+                const bool go = (t >> 3) < n;
+                const int node = go ? m.order[t >> 3] : 0, above = go ? m.above[node] : -1;
                 Raw<__nv_bfloat16, 4> rk[4], rb[4], rq[4];
                 {
-                    const size_t row = first + (size_t)(node < n ? node : 0) * H * D + 4 * sub;
+                    const size_t row = first + (size_t)node * H * D + 4 * sub;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        rk[j].load(k + row + 32 * j), rb[j].load(b + row + 32 * j), rq[j].load(q + row + 32 * j);
+                    for (int j = 0; j < 4; ++j) {
+                        rk[j].clear();
+                        rb[j].clear();
+                        rq[j].clear();
+                        if (go) rk[j].load(k + row + 32 * j), rb[j].load(b + row + 32 * j), rq[j].load(q + row + 32 * j);
+                    }
                 }
                 cp_async_wait();
                 if (!group_wait(sh.coef_free[c & 1], (c >> 1) + 1, BAR_PATH, THREADS)) break;
-                Coef &coef = sh.coef[c & 1];
+                float *coef = sh.c[c & 1];
                 f32x2 e[4][2], g[4][2];
-                int above;
                 {
                     f32x2 G[4][2];
-                    above = climb<D>(&sh.alpha[0][0], m.parent, coef.anc, node, n, lane, G);
+                    climb<D>(&sh.alpha[0][0], m.anc, go, node, above, lane, G);
                     const bool good = in_range<D>(G, lane);
-                    if (node < n && sub == 0) coef.above[node] = (unsigned char)above, sh.fine[node] = good;
+                    if (go && sub == 0) sh.fine[node] = good;
                     if (!group_wait(sh.b_free, c + 1, BAR_PATH, THREADS)) break;   // the products before; all have climbed
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -360,11 +393,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                             e[j][h] = mul2(mul2(pack2(bb[2 * h], bb[2 * h + 1]), k2), G[j][h]);
                             g[j][h] = mul2(pack2(qq[2 * h], qq[2 * h + 1]), G[j][h]);
                         }
-                        if (node < n) {
+                        if (go) {
                             const float2 g0 = unpack2(G[j][0]), g1 = unpack2(G[j][1]);
                             *reinterpret_cast<float4 *>(&sh.alpha[node][4 * (sub + 8 * j)]) =
-                                make_float4(__fdividef(kk[0], g0.x), __fdividef(kk[1], g0.y), __fdividef(kk[2], g1.x),
-                                            __fdividef(kk[3], g1.y));
+                                make_float4(kk[0] * inverse(g0.x), kk[1] * inverse(g0.y), kk[2] * inverse(g1.x), kk[3] * inverse(g1.y));
                             const auto put = [&](uint32_t to, const f32x2 (&x)[2]) {
                                 const float2 x0 = unpack2(x[0]), x1 = unpack2(x[1]);
                                 uint2 hi, lo2;
@@ -382,14 +414,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                 arrive(sh.b_full);
                 group_sync(BAR_PATH, THREADS);   // every k / G is there
                 bool good = true;
-                for (int j = sub; j <= above; j += 8) good = good && sh.fine[coef.anc[pairs(node) + j]];
+                for (int j = sub; j <= above; j += 8) good = good && sh.fine[m.anc[pairs(node) + j]];
                 good = (__ballot_sync(0xffffffffu, good) >> (lane & 24) & 0xffu) == 0xffu;
-                couple<D>(&sh.alpha[0][0], coef.anc, sh.a, coef.c, node < n && good, node, above, lane, e, g);
-                if (__any_sync(0xffffffffu, node < n && !good))
-                    couple_far<__nv_bfloat16, D>(q, k, b, alpha, coef.anc, sh.a, coef.c, node < n && !good, lo, H, head, node,
-                                                 above, lane);
+                couple<D>(&sh.alpha[0][0], m.anc, sh.a, coef, go && good, node, above, lane, e, g);
+                if (__any_sync(0xffffffffu, go && !good))
+                    couple_far<__nv_bfloat16, D>(q, k, b, alpha, m.anc, sh.a, coef, go && !good, lo, H, head, node, above, lane);
                 group_sync(BAR_PATH, THREADS);   // every A and P is there
-                eliminate(sh.a, coef.c, coef.anc, coef.c, node, n, above, lane);
+                eliminate(sh.a, coef, m.anc, coef, go, node, above, lane);
                 arrive(sh.coef_full[c & 1]);
                 ++c;
             }
