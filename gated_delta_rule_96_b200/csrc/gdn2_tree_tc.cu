@@ -359,6 +359,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                 for (int i = t; i < n * (D / 4); i += THREADS)   // group_wait's barrier is behind the last item's reads
                     cp_async16(smem_u32(&sh.alpha[0][0]) + 16 * i, alpha + first + (size_t)(i / (D / 4)) * H * D + i % (D / 4) * 4);
                 const bool go = (t >> 3) < n;
+                if (__all_sync(0xffffffffu, !go)) {   // a warp without a node only keeps the barriers
+                    cp_async_wait();
+                    if (!group_wait(sh.coef_free[c & 1], (c >> 1) + 1, BAR_PATH, THREADS) ||
+                        !group_wait(sh.b_free, c + 1, BAR_PATH, THREADS))
+                        break;
+                    arrive(sh.b_full);
+                    group_sync(BAR_PATH, THREADS);
+                    group_sync(BAR_PATH, THREADS);
+                    arrive(sh.coef_full[c & 1]);
+                    arrive(sh.meta_free[it % METAS]);
+                    ++c;
+                    continue;
+                }
                 const int node = go ? m.order[t >> 3] : 0, above = go ? m.above[node] : -1;
                 Raw<__nv_bfloat16, 4> rk[4], rb[4], rq[4];
                 {
