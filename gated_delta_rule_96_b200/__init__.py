@@ -442,12 +442,21 @@ def _rows(t) -> int:
     return t.numel() // t.shape[-1] if t.shape[-1] else 0
 
 
-def _gated_workspace(o):
-    return new_workspace(gdn2_gated_norm_bwd_workspace_bytes(_rows(o), o.shape[-1]), o.device)
+def _own_workspace(nbytes, device, stream):
+    """A workspace for one call, zeroed on the stream that the call runs on."""
+    if stream is None:
+        return new_workspace(nbytes, device)
+    import torch
+    with torch.cuda.stream(stream):
+        return new_workspace(nbytes, device)
 
 
-def _add_workspace(h):
-    return new_workspace(gdn2_add_norm_bwd_workspace_bytes(_rows(h), h.shape[-1]), h.device)
+def _gated_workspace(o, stream):
+    return _own_workspace(gdn2_gated_norm_bwd_workspace_bytes(_rows(o), o.shape[-1]), o.device, stream)
+
+
+def _add_workspace(h, stream):
+    return _own_workspace(gdn2_add_norm_bwd_workspace_bytes(_rows(h), h.shape[-1]), h.device, stream)
 
 
 def gdn2_gated_norm_fwd(o, gate, weight, y, act="silu", eps=1e-6, stream=None) -> None:
@@ -462,7 +471,7 @@ def gdn2_gated_norm_bwd(o, gate, weight, dy, do, dgate, dweight, act="silu", eps
     """Gradients of gdn2_gated_norm_fwd (include/gdn2.h): do, dgate in the token dtype, dweight fp32."""
     _given(do, dgate, dweight)
     _native().gated_norm_bwd(o, gate, weight, dy, do, dgate, dweight, _gate_code(act), eps,
-                             _gated_workspace(o) if workspace is None else workspace, stream)
+                             _gated_workspace(o, stream) if workspace is None else workspace, stream)
 
 
 def gdn2_add_norm_fwd(x, residual, scale, weight, h, y, eps=1e-6, stream=None) -> None:
@@ -476,7 +485,7 @@ def gdn2_add_norm_bwd(h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweigh
     """Gradients of gdn2_add_norm_fwd at the stored h (include/gdn2.h).  dh may be None (zero); without a
     scale, x, dx and dscale are not used (dx equals dresidual)."""
     _native().add_norm_bwd(h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweight, eps,
-                           _add_workspace(h) if workspace is None else workspace, stream)
+                           _add_workspace(h, stream) if workspace is None else workspace, stream)
 
 
 def gdn2_tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, o, max_nodes, workspace=None,
@@ -488,7 +497,7 @@ def gdn2_tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, o, max_node
     pool).  Malformed indices are reported in the workspace's status."""
     _given(o)
     _native().tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, o, max_nodes,
-                       new_workspace(0, q.device) if workspace is None else workspace, stream)
+                       _own_workspace(0, q.device, stream) if workspace is None else workspace, stream)
 
 
 def gdn2_recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index, o, workspace=None,
@@ -499,7 +508,7 @@ def gdn2_recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, 
     int32 or None (entry t is row t); o [total, H, d_v] or None (not wanted).  Malformed indices are reported
     in the workspace's status."""
     _native().recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index, o, False,
-                            new_workspace(0, q.device) if workspace is None else workspace, stream)
+                            _own_workspace(0, q.device, stream) if workspace is None else workspace, stream)
 
 
 def gdn2_state_copy(dst, src, dst_index, src_index, workspace=None, stream=None) -> None:
@@ -508,7 +517,7 @@ def gdn2_state_copy(dst, src, dst_index, src_index, workspace=None, stream=None)
     fp32 caches [slots, ...] with equal slot shapes, one cache or two that do not overlap; the indices int32
     on the device, at most STATE_COPY_MAX_PAIRS."""
     _native().state_copy(dst, src, dst_index, src_index,
-                         new_workspace(0, dst.device) if workspace is None else workspace, stream)
+                         _own_workspace(0, dst.device, stream) if workspace is None else workspace, stream)
 
 
 def _given(*outputs):
@@ -565,7 +574,7 @@ def gated_norm_fwd(o, gate, weight, act="silu", eps=1e-6, stream=None):
 def gated_norm_bwd(o, gate, weight, dy, act="silu", eps=1e-6, workspace=None, stream=None):
     """Allocating convenience wrapper: returns (do, dgate, dweight)."""
     return _native().gated_norm_bwd(o, gate, weight, dy, None, None, None, _gate_code(act), eps,
-                                    _gated_workspace(o) if workspace is None else workspace, stream)
+                                    _gated_workspace(o, stream) if workspace is None else workspace, stream)
 
 
 def add_norm_fwd(x, residual, scale, weight, eps=1e-6, stream=None):
@@ -577,8 +586,9 @@ def add_norm_bwd(h, x, scale, weight, dy, dh=None, eps=1e-6, workspace=None, str
     """Allocating convenience wrapper: returns (dresidual, dx, dscale, dweight); without a scale dx is
     dresidual and dscale None."""
     import torch
-    dresidual, dweight = torch.empty_like(h), torch.empty_like(weight)
-    dx, dscale = (None, None) if scale is None else (torch.empty_like(h), torch.empty_like(scale))
+    with torch.cuda.stream(stream):
+        dresidual, dweight = torch.empty_like(h), torch.empty_like(weight)
+        dx, dscale = (None, None) if scale is None else (torch.empty_like(h), torch.empty_like(scale))
     gdn2_add_norm_bwd(h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweight, eps=eps, workspace=workspace,
                       stream=stream)
     return dresidual, dresidual if dx is None else dx, dscale, dweight
@@ -587,14 +597,14 @@ def add_norm_bwd(h, x, scale, weight, dy, dh=None, eps=1e-6, workspace=None, str
 def tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, max_nodes, workspace=None, stream=None):
     """Allocating convenience wrapper of gdn2_tree_fwd: returns o (rows of no tree hold no values)."""
     return _native().tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, None, max_nodes,
-                              new_workspace(0, q.device) if workspace is None else workspace, stream)
+                              _own_workspace(0, q.device, stream) if workspace is None else workspace, stream)
 
 
 def recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index=None, workspace=None, stream=None):
     """Allocating convenience wrapper of gdn2_recurrent_fwd: updates S, returns o by entry (entries of no
     sequence hold no values)."""
     return _native().recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index, None, True,
-                                   new_workspace(0, q.device) if workspace is None else workspace, stream)
+                                   _own_workspace(0, q.device, stream) if workspace is None else workspace, stream)
 
 
 def _recurrence_function():

@@ -6,6 +6,14 @@
 
 namespace gdn2 {
 
+// Lets `kern` use up to `bytes` of dynamic shared memory on the current device.  At every launch, since the
+// attribute is a device's (and a context's) own and setting it takes a fraction of a microsecond; always the most
+// that any launch of the kernel uses, since another host thread may be between this and its launch.
+template <typename Kernel>
+inline bool allow_smem(Kernel kern, size_t bytes) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+}
+
 // Status header at the start of every prefill workspace (device status words).
 constexpr size_t kStatusBytes = 256;
 

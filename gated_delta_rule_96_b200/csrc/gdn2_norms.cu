@@ -243,6 +243,7 @@ __device__ __forceinline__ void block_sum(float (&x)[C], float (*s)[C]) {
 }
 
 constexpr int MAX_WARPS = 16;   // of a block: rows of up to 512 threads
+constexpr int MAX_WIDTH = 8192;
 
 template <typename Tok, int NV>
 __global__ void __launch_bounds__(512) add_norm_fwd_kernel(const Tok *x, const Tok *residual,
@@ -433,7 +434,7 @@ int gated_fwd_t(const void *o, const void *gate, const float *weight, void *y, l
 template <typename Tok, int D, int ACT>
 int gated_bwd_t(const void *o, const void *gate, const float *weight, const void *dy, void *d_o, void *dgate,
                 float *dweight, long long rows, float eps, float *partial, cudaStream_t st) {
-    static const int per_sm = resident(gated_norm_bwd_kernel<Tok, D, ACT>, 256, 0);
+    static const int per_sm = resident(gated_norm_bwd_kernel<Tok, D, ACT>, 256, 0);   // the same on every B200
     const int blocks = cap_blocks((rows + 7) / 8, per_sm);
     gated_norm_bwd_kernel<Tok, D, ACT><<<blocks, 256, 0, st>>>((const Tok *)o, (const Tok *)gate, weight,
                                                                (const Tok *)dy, (Tok *)d_o, (Tok *)dgate, partial,
@@ -465,8 +466,8 @@ int add_bwd_t(const void *h, const void *x, const float *scale, const float *wei
     int blocks = 0;
     bool ok = false;
     auto go = [&](auto kern) {
-        const size_t smem = sizeof(float) * (size_t)columns;   // up to 64 KB
-        ok = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+        const size_t smem = sizeof(float) * (size_t)columns;
+        ok = allow_smem(kern, sizeof(float) * 2 * MAX_WIDTH);
         if (!ok) return;
         blocks = cap_blocks(rows, resident(kern, nt, smem));
         kern<<<blocks, nt, smem, st>>>((const Tok *)h, (const Tok *)x, scale, weight, (const Tok *)dy, (const Tok *)dh,

@@ -24,6 +24,8 @@
 // A decode step (one token, 128 KB moved for 0.1 MFMA a head) is then bound by HBM: B256 H16 d128 took 166 us
 // with the state loaded to registers by two CTAs an SM that each waited for every latency in turn, and
 // TIME_DECODE here.
+#include <atomic>
+
 #include "gdn2_internal.h"
 #include "gdn2_slots.cuh"
 #include "tc_ptx.cuh"
@@ -425,23 +427,21 @@ template <typename Tok, int K, int V, bool OUT>
 int launch_out(const void *q, const void *k, const void *v, const float *alpha, const void *b, const void *w, float *S,
                long long slot_stride, int num_slots, const int *slots_in, const int *slots_out, const int *cu,
                const int *index, void *o, int batch, int H, int total, int rows, unsigned *status, cudaStream_t st) {
+    const auto kern = recurrent_kernel<Tok, K, V, OUT>;
     constexpr size_t most = smem_bytes<K, V>(V);
     constexpr int threads = 2 * V + 32 * EXTRA_WARPS<K, V>;
-    static const int per_sm = [] {
-        int n = 0;
-        const auto kern = recurrent_kernel<Tok, K, V, OUT>;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, most) != cudaSuccess)
-            return 0;
-        return n;
-    }();
-    if (per_sm < 1) return -6;
+    static std::atomic<int> resident{0};   // CTAs an SM; the same on every B200
+    if (!allow_smem(kern, most)) return -6;
+    int per_sm = resident.load();
+    if (per_sm == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, most) != cudaSuccess || per_sm < 1) return -6;
+        resident.store(per_sm);
+    }
     // few chains: their columns over more SMs
     int splits = 1;
     while (splits < V / 16 && (long long)batch * H * splits * 2 <= 148) splits *= 2;
     const long long items = (long long)batch * H * splits, grid = items < 148 * per_sm ? items : 148 * per_sm;
-    recurrent_kernel<Tok, K, V, OUT><<<(unsigned)grid, 2 * V / splits + 32 * EXTRA_WARPS<K, V>,
-                                       smem_bytes<K, V>(V / splits), st>>>(
+    kern<<<(unsigned)grid, 2 * V / splits + 32 * EXTRA_WARPS<K, V>, smem_bytes<K, V>(V / splits), st>>>(
         (const Tok *)q, (const Tok *)k, (const Tok *)v, alpha, (const Tok *)b, (const Tok *)w, S, slot_stride,
         num_slots, slots_in, slots_out, cu, index, (Tok *)o, batch, H, splits, total, rows, status);
     return launch_status();

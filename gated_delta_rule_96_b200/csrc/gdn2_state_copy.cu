@@ -146,16 +146,14 @@ int launch_state_copy(float *dst, long long dst_stride, int dst_slots, const flo
                       int src_slots, const int *dst_idx, const int *src_idx, int n, long long slot_floats,
                       unsigned *status, cudaStream_t st) {
     using namespace copy;
-    static const bool ok = cudaFuncSetAttribute(state_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                (int)layout(kStateCopyMaxPairs, GROUP).total) == cudaSuccess;
-    if (!ok) return -6;
     const long long vecs = slot_floats / 4, ranges = (vecs + RANGE - 1) / RANGE;
     // up to GROUP pairs a block (four blocks share an SM), fewer while there are not two waves of such blocks
     long long group = (n * ranges + 2 * 4 * 148 - 1) / (2 * 4 * 148);
     group = group < 1 ? 1 : group > GROUP ? GROUP : group;
-    state_copy_kernel<<<dim3((unsigned)ranges, (unsigned)((n + group - 1) / group)), THREADS, layout(n, (int)group).total,
-                        st>>>(dst, dst_stride, dst_slots, src, src_stride, src_slots, dst_idx, src_idx, n, (int)group,
-                              (int)vecs, status);
+    const size_t smem = layout(n, (int)group).total;
+    if (!allow_smem(state_copy_kernel, layout(kStateCopyMaxPairs, GROUP).total)) return -6;
+    state_copy_kernel<<<dim3((unsigned)ranges, (unsigned)((n + group - 1) / group)), THREADS, smem, st>>>(
+        dst, dst_stride, dst_slots, src, src_stride, src_slots, dst_idx, src_idx, n, (int)group, (int)vecs, status);
     return launch_status();
 }
 

@@ -10,7 +10,6 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
@@ -60,6 +59,21 @@ const char *show(at::ScalarType t) {
 const at::Tensor &tensor(const char *name, PyObject *o) {
     if (!THPVariable_Check(o)) throw Refusal{PyExc_TypeError, std::string(name) + " must be a tensor"};
     return THPVariable_Unpack(o);
+}
+
+long long attribute(PyObject *o, const char *name) {
+    PyObject *x = PyObject_GetAttrString(o, name);
+    if (!x) throw Refusal{nullptr, ""};
+    const long long v = PyLong_AsLongLong(x);
+    Py_DECREF(x);
+    if (v == -1 && PyErr_Occurred()) throw Refusal{nullptr, ""};
+    return v;
+}
+
+// a torch.cuda.Stream
+c10::cuda::CUDAStream stream_of(PyObject *o) {
+    return c10::cuda::CUDAStream::unpack3(attribute(o, "stream_id"), (c10::DeviceIndex)attribute(o, "device_index"),
+                                          (c10::DeviceType)attribute(o, "device_type"));
 }
 
 // The tensors of one call.  Types and shapes are checked as they come, layout and device once all are there:
@@ -147,8 +161,7 @@ struct Call {
         *slots = (int)t.size(0);
         return static_cast<float *>(t.data_ptr());
     }
-    // the call itself, on `stream` or the device's current one (None), with the device current and the
-    // interpreter free
+    // the call itself, on `stream` or the device's current one, with the device current and the interpreter free
     template <typename F>
     void run(const char *where, PyObject *stream, F launch) const {
         const c10::Device d = device();
@@ -156,11 +169,11 @@ struct Call {
         if (stream == Py_None) {
             st = c10::cuda::getCurrentCUDAStream(d.index()).stream();
         } else {
-            PyObject *handle = PyObject_GetAttrString(stream, "cuda_stream");
-            if (!handle) throw Refusal{nullptr, ""};
-            st = PyLong_AsVoidPtr(handle);
-            Py_DECREF(handle);
-            if (PyErr_Occurred()) throw Refusal{nullptr, ""};
+            const c10::cuda::CUDAStream s = stream_of(stream);
+            if (s.device_index() != d.index())
+                throw Refusal{PyExc_ValueError, "the stream is of cuda:" + std::to_string(s.device_index()) +
+                                                    ", the tensors are on cuda:" + std::to_string(d.index())};
+            st = s.stream();
         }
         int rc;
         {
@@ -197,12 +210,18 @@ int to_int(const char *name, long long x) {
     return (int)x;
 }
 
-// o if it is a tensor; where it is None a new tensor like `like`, which `made` owns
-PyObject *or_new(PyObject *o, const at::Tensor &like, std::vector<PyObject *> &made) {
+// o if it is a tensor; where it is None a new one of `shape`, like `like` otherwise, which `made` owns.  Its memory is
+// the stream's that the call runs on.
+PyObject *or_new(PyObject *o, at::IntArrayRef shape, const at::Tensor &like, PyObject *stream, std::vector<PyObject *> &made) {
     if (o != Py_None) return o;
-    made.push_back(THPVariable_Wrap(at::empty_like(like)));
+    c10::cuda::OptionalCUDAStreamGuard guard;
+    if (stream != Py_None) guard.reset_stream(stream_of(stream));
+    made.push_back(THPVariable_Wrap(at::empty(shape, like.options().requires_grad(false))));
     if (!made.back()) throw Refusal{nullptr, ""};
     return made.back();
+}
+PyObject *or_new(PyObject *o, const at::Tensor &like, PyObject *stream, std::vector<PyObject *> &made) {
+    return or_new(o, like.sizes(), like, stream, made);
 }
 
 // what a function returns: nothing where the outputs were given, the new one, or a tuple of them
@@ -249,7 +268,7 @@ PyObject *gated_norm_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const at::Tensor &t = THPVariable_Unpack(a[0]);
         const void *gate = c.use("gate", a[1], t.scalar_type(), t.sizes());
         const void *weight = c.use("weight", a[2], at::kFloat, t.sizes().slice(t.dim() - 1));
-        void *y = c.use("y", or_new(a[3], t, made), t.scalar_type(), t.sizes());
+        void *y = c.use("y", or_new(a[3], t, a[6], made), t.scalar_type(), t.sizes());
         const int act = to_int("act", whole(a[4])), width = to_int("d_v", t.size(-1));
         const float eps = (float)number(a[5]);
         c.run("gdn2_gated_norm_fwd", a[6], [&](void *st) {
@@ -271,9 +290,9 @@ PyObject *gated_norm_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const void *gate = c.use("gate", a[1], type, shape);
         const void *weight = c.use("weight", a[2], at::kFloat, last);
         const void *dy = c.use("dy", a[3], type, shape);
-        void *d_o = c.use("do", or_new(a[4], t, made), type, shape);
-        void *dgate = c.use("dgate", or_new(a[5], t, made), type, shape);
-        void *dweight = c.use("dweight", or_new(a[6], THPVariable_Unpack(a[2]), made), at::kFloat, last);
+        void *d_o = c.use("do", or_new(a[4], t, a[10], made), type, shape);
+        void *dgate = c.use("dgate", or_new(a[5], t, a[10], made), type, shape);
+        void *dweight = c.use("dweight", or_new(a[6], THPVariable_Unpack(a[2]), a[10], made), at::kFloat, last);
         const int act = to_int("act", whole(a[7])), width = to_int("d_v", t.size(-1));
         const float eps = (float)number(a[8]);
         size_t bytes;
@@ -299,8 +318,8 @@ PyObject *add_norm_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const void *scale = c.use("scale", a[2], at::kFloat, last, true);
         const void *weight = c.use("weight", a[3], at::kFloat, last);
         const bool allocate = PyObject_IsTrue(a[6]) == 1;
-        void *y = c.use("y", allocate ? or_new(Py_None, t, made) : a[5], type, shape);
-        void *h = c.use("h", allocate ? or_new(Py_None, t, made) : a[4], type, shape, true);
+        void *y = c.use("y", allocate ? or_new(Py_None, t, a[8], made) : a[5], type, shape);
+        void *h = c.use("h", allocate ? or_new(Py_None, t, a[8], made) : a[4], type, shape, true);
         const float eps = (float)number(a[7]);
         const int width = to_int("width", t.size(-1));
         c.run("gdn2_add_norm_fwd", a[8], [&](void *st) {
@@ -372,7 +391,7 @@ PyObject *tree_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const int *cu = c.index("cu_nodes", a[8], &ends), *parents = c.index("parents", a[9], &total);
         int num;
         const float *S = c.pool("S", a[6], {x.H, x.K, x.V}, &stride, &num);
-        void *o = c.use("o", or_new(a[10], THPVariable_Unpack(a[2]), made), x.type, {x.rows, x.H, x.V});
+        void *o = c.use("o", or_new(a[10], THPVariable_Unpack(a[2]), a[13], made), x.type, {x.rows, x.H, x.V});
         const int most = to_int("max_nodes", whole(a[11])), seqs = to_int("batch", batch);
         size_t bytes;
         void *ws = c.workspace(a[12], &bytes);
@@ -397,10 +416,7 @@ PyObject *recurrent_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         int num;
         float *S = c.pool("S", a[6], {x.H, x.K, x.V}, &stride, &num);
         PyObject *given = a[11];
-        if (PyObject_IsTrue(a[12]) == 1) {
-            made.push_back(THPVariable_Wrap(at::empty({total, x.H, x.V}, THPVariable_Unpack(a[2]).options())));
-            if (!(given = made.back())) throw Refusal{nullptr, ""};
-        }
+        if (PyObject_IsTrue(a[12]) == 1) given = or_new(Py_None, {total, x.H, x.V}, THPVariable_Unpack(a[2]), a[14], made);
         void *o = c.use("o", given, x.type, {total, x.H, x.V}, true);
         const int seqs = to_int("batch", batch), entries = to_int("entries", total);
         size_t bytes;

@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q,
     if (lo < 0 || hi < lo || hi > total || hi - lo > max_nodes) bad = DEV_RANGE;
     else if (slot < -1 || slot >= num_slots) bad = DEV_SLOT;
 
-    // Everything that needs no more than the item's place is on its way before the first barrier.
+    // The state is on its way before the first barrier.
     // The warp's slice of the state: rows 4 (rg + 8 j) + i, columns c0 .. c0 + 3; where there are more warps than
     // column groups they share the nodes.
     const int groups = cols / 16, shares = (nt >> 5) / groups;
@@ -76,7 +76,11 @@ __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q,
             if (node < n) rk[j].load(k + row + 32 * j), rb[j].load(b + row + 32 * j), rq[j].load(q + row + 32 * j);
         }
     };
-    fetch(warp * 4 + (lane >> 3));
+    if (__syncthreads_or(bad != 0)) {
+        if (bad) atomicOr(status, bad);
+        return;
+    }
+    if (n == 0) return;
 #pragma unroll 4
     for (int i = tid; i < n * (K / 4); i += nt)   // alpha of all nodes, four channels a thread at a time
         *reinterpret_cast<float4 *>(sa + 4 * i) = *reinterpret_cast<const float4 *>(
@@ -92,16 +96,11 @@ __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q,
         rw.get(y);
         *reinterpret_cast<float4 *>(sr + 4 * i) = make_float4(x[0] * y[0], x[1] * y[1], x[2] * y[2], x[3] * y[3]);
     }
-    if (__syncthreads_or(bad != 0)) {
-        if (bad) atomicOr(status, bad);
-        return;
-    }
-    if (n == 0) return;
     if (tid < n) depth[tid] = (unsigned char)list_path(sp, anc, tid);
     __syncthreads();
     for (int n0 = warp * 4; n0 < n; n0 += nt / 8) {
         const int node = n0 + (lane >> 3), sub = lane & 7;
-        if (n0 >= nt / 8) fetch(node);
+        fetch(node);
         f32x2 G[RJ][2];
         climb<K>(sa, anc, node < n, node, node < n ? depth[node] : -1, lane, G);
         const bool good = in_range<K>(G, lane);
@@ -195,13 +194,11 @@ int launch_t(const void *q, const void *k, const void *v, const float *alpha, co
         return sizeof(float) * (size_t)n * (4 * K + 2 * cols) + (2 * sizeof(float) + 1) * (size_t)pairs(n) +
                (sizeof(int) + 2) * (size_t)n;
     };
-    static const bool ok = cudaFuncSetAttribute(tree_kernel<Tok, K, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                (int)smem(MAX_NODES, V)) == cudaSuccess;
-    if (!ok) return -6;
     // few chains: their columns over more SMs
     int splits = 1;
     while (splits < V / 16 && (long long)batch * H * splits * 2 <= 148) splits *= 2;
     const int cols = V / splits;
+    if (!allow_smem(tree_kernel<Tok, K, V>, smem(MAX_NODES, V))) return -6;
     tree_kernel<Tok, K, V><<<dim3(H * splits, batch), 2 * cols < 128 ? 128 : 2 * cols, smem(max_nodes, cols), st>>>(
         (const Tok *)q, (const Tok *)k, (const Tok *)v, alpha, (const Tok *)b, (const Tok *)w, S, slot_stride,
         num_slots, slots, cu, parents, (Tok *)o, H, splits, total, max_nodes, status);

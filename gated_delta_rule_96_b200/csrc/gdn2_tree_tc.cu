@@ -453,9 +453,7 @@ int launch_tc(const void *q, const void *k, const void *v, const float *alpha, c
               const float *S, long long slot_stride, int num_slots, const int *slots, const int *cu, const int *parents,
               void *o, int batch, int H, int total, int max_nodes, unsigned *status, cudaStream_t st) {
     constexpr int smem = (int)sizeof(TcShared) + 1024;
-    static const bool ok =
-        cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
-    if (!ok) return -6;
+    if (!allow_smem(tree_tc_kernel, smem)) return -6;
     using bf = __nv_bfloat16;
     const long long items = (long long)batch * H;
     tree_tc_kernel<<<(unsigned)(items < 148 ? items : 148), TC_THREADS, smem, st>>>(

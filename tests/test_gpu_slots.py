@@ -377,6 +377,71 @@ def test_offsets_past_32_bits():
     assert torch.equal(pool[first - 1], pool[first]) and not pool[:first - 1].any()
 
 
+def test_calls_on_a_side_stream_allocate_there():
+    """`stream=` without a workspace: the outputs and the workspace are the stream's, while the current stream is
+    kept busy."""
+    torch, g = cuda_or_skip()
+    H = 3
+    x = tokens(torch, 50, 6, H, 128, 128, "bf16")
+    pool = make_pool(torch, 51, 4, H, 128, 128)
+    par, cu, slots = [-1, 0, 0, 1, -1, 0], [0, 4, 6], [1, 2]
+    want_tree = g.tree_fwd(*x, pool, i32(torch, slots), i32(torch, cu), i32(torch, par), 4)
+    p = pool.clone()
+    want_rec = g.recurrent_fwd(*x, p, i32(torch, slots), i32(torch, [3, 0]), i32(torch, cu))
+    idx = i32(torch, slots), i32(torch, cu), i32(torch, par), i32(torch, [3, 0])
+    o, gate, w = x[2].reshape(-1, 128), x[5].reshape(-1, 128), torch.ones(128, device="cuda")
+    want_norm = g.gated_norm_bwd(o, gate, w, gate)
+    side, busy = torch.cuda.Stream(), torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for _ in range(4):
+            busy = busy @ busy * 1e-2                   # the current stream lags behind
+        a = g.tree_fwd(*x, pool, idx[0], idx[1], idx[2], 4, stream=side)
+        b = g.recurrent_fwd(*x, pool, idx[0], idx[3], idx[1], stream=side)
+        c = g.gated_norm_bwd(o, gate, w, gate, stream=side)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            assert torch.equal(a, want_tree) and torch.equal(b, want_rec) and torch.equal(pool, p)
+            assert all(torch.equal(s, t) for s, t in zip(c, want_norm))
+        side.synchronize()
+    torch.cuda.synchronize()
+
+
+def test_two_graphs_share_a_workspace():
+    """The workspace of the calls over slots holds status words only: two captured graphs replayed at the same
+    time on two streams do not disturb one another, and what either reports stays reported."""
+    torch, g = cuda_or_skip()
+    H, B = 2, 40
+    ws, graphs, outs, wants = g.new_workspace(0), [], [], []
+    torch.cuda.synchronize()
+    for seed, last in ((60, B - 1), (61, 77)):           # the second one's last tree hangs on no slot
+        x = tokens(torch, seed, 20 * B, H, 128, 128, "bf16")
+        pool = make_pool(torch, seed, B, H, 128, 128)
+        rng = np.random.default_rng(seed)
+        par = sum((random_tree(rng, 20, 5) for _ in range(B)), [])
+        slots = i32(torch, list(range(B - 1)) + [last])
+        cu, parents = i32(torch, range(0, 20 * B + 1, 20)), i32(torch, par)
+        o = torch.full_like(x[2], float("nan"))
+        g.gdn2_tree_fwd(*x, pool, slots, cu, parents, o, 20)
+        wants.append(o.clone())
+        graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=s):
+            g.gdn2_tree_fwd(*x, pool, slots, cu, parents, o, 20, workspace=ws)
+        graphs.append((graph, s, x, pool, slots, cu, parents))
+        outs.append(o)
+    for _ in range(5):
+        for o in outs:
+            o.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for graph, s, *_ in graphs:
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], wants[0])
+        assert torch.equal(outs[1].nan_to_num(7.0), wants[1].nan_to_num(7.0)) and torch.isnan(outs[1][-20:]).all()
+        assert g.gdn2_workspace_status(ws, clear=True) == g.DEV_SLOT
+
+
 def test_serving_round_together():
     """As a server uses them: fork a sequence, draft a tree for each continuation, read the tree out, norm and
     gate it, take the accepted paths into the cache, and move the survivors together; everything captured in
