@@ -1,20 +1,20 @@
 // Drafted trees over a state cache on the tensor cores (sm_100a): bf16 tokens, d_k = d_v = 128.  The formulas are
 // those of gdn2_tree.cu; what is different is where the two products with the state run, and that a
-// persistent CTA's warps work on three (sequence, head) items at once.
+// persistent CTA's warps work on several (sequence, head) items at once.
 //
 // S^T [e G; q G]^T, 128 x 128 x 2n, is 2 n 128^2 FMA a head, more than CUDA cores do in the time that HBM takes
 // for the state and the tokens from five nodes on.  Both factors are split into two bf16, x = hi + lo (16
 // significant bits, relative error 2^-17): three tcgen05 products hi hi + hi lo + lo hi keep the error far
 // below the rounding of the bf16 output, where one product of bf16 operands would double that rounding.
-//   loader warp             S by bulk copies, 32 rows at a time, into two staging buffers
-//   state group  (4 warps)  a column a thread from there, split, into tensor memory: the A operand S^T, lane =
-//                           value column, two buffers
-//   path group   (16 warps) eight lanes a node up to its root: the rows e G and q G, split, into the B operand's
-//                           swizzled images, k / G and the coefficients to shared memory
+//   state group  (4 warps)  a column of S a thread, split, into tensor memory: the A operand S^T, lane = value
+//                           column, two buffers
+//   path group   (8 warps)  eight lanes a node up to its root: the rows e G and q G, split, into the B operand's
+//                           swizzled images, and k / G
+//   pair group   (8 warps)  the coefficients along the paths, from those
 //   column group (8 warps)  R = u - S^T (e G) and S^T (q G) from tensor memory (lane = value column) to shared
-//                           memory, then o = S^T (q G) + C R, a node a warp and four columns a lane
-//   lead warp               reads and checks the items, brings the tokens' lines into L2 ahead of the groups,
-//                           and issues the products
+//                           memory, then o = S^T (q G) + C R, two nodes a warp and eight columns a lane
+//   lead warp               reads and checks the items, lists their paths, brings the tokens' lines into L2 ahead
+//                           of the groups, and issues the products
 #include "gdn2_tree.cuh"
 #include "tc_ptx.cuh"
 
@@ -24,11 +24,11 @@ namespace tree {
 using namespace gdn2::tc;
 
 constexpr int D = 128;
-constexpr int COLUMN_WARPS = 8, STATE_WARPS = 4, PATH_WARPS = 16;   // in this order; then loader and lead
-constexpr int LOADER = COLUMN_WARPS + STATE_WARPS + PATH_WARPS, LEAD = LOADER + 1, TC_THREADS = 32 * (LEAD + 1);
-constexpr int STAGE_ROWS = 32, STAGES = 2;   // of the state
+constexpr int COLUMN_WARPS = 8, STATE_WARPS = 4, PATH_WARPS = 8, PAIR_WARPS = 8;   // in this order; then the lead
+constexpr int PATH0 = COLUMN_WARPS + STATE_WARPS, PAIR0 = PATH0 + PATH_WARPS, LEAD = PAIR0 + PAIR_WARPS,
+              TC_THREADS = 32 * (LEAD + 1);
 constexpr int METAS = 3;
-constexpr uint32_t BAR_COLUMN = 1, BAR_PATH = 2, BAR_STATE = 3, WAIT_LIMIT = 1u << 20;
+constexpr uint32_t BAR_COLUMN = 1, BAR_PATH = 2, BAR_PAIR = 3, BAR_STATE = 4, WAIT_LIMIT = 1u << 20;
 constexpr uint32_t TM_S = 0, TM_D = 256, TM_COLS = 512;   // S: two buffers of hi (64 columns) and lo (64)
 
 // An item: its nodes lo .. lo+n-1, the state's slot, the nodes' parents, paths and numbers of ancestors, and the
@@ -37,18 +37,17 @@ struct Meta {
     int lo, n, slot, head;
     signed char parent[MAX_NODES];
     unsigned char anc[MAX_PAIRS], above[MAX_NODES], order[MAX_NODES];
+    unsigned char fine[MAX_NODES];   // whether a node's G is in range (the path group's)
 };
 
 struct TcShared {
     unsigned char b_hi[2 * MAX_NODES * D * 2], b_lo[2 * MAX_NODES * D * 2];   // [e G; q G], swizzled
-    float stage[STAGES][STAGE_ROWS][D];
-    float alpha[MAX_NODES][D];                // then k / G
+    float alpha[MAX_NODES][D], key[MAX_NODES][D];   // key: k / G
     float r[MAX_NODES][D], x[MAX_NODES][D];   // u, then R; S^T (q G); by node and value column
     float a[MAX_PAIRS], c[2][MAX_PAIRS];      // A; P, then C
     Meta meta[METAS];
-    unsigned char fine[MAX_NODES];            // whether a node's G is in range
-    unsigned long long meta_full[METAS], meta_free[METAS], stage_full[STAGES], stage_free[STAGES], s_full[2], s_free[2],
-        coef_full[2], coef_free[2], b_full, b_free, d_full, d_free;
+    unsigned long long meta_full[METAS], meta_free[METAS], s_full[2], s_free[2], coef_full[2], coef_free[2], b_full, b_free,
+        d_full, d_free;
     uint32_t tmem, abort;
 };
 static_assert(sizeof(TcShared) + 1024 <= 227 * 1024, "shared memory of an SM");
@@ -64,6 +63,9 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     hi = pack_bf16(x, y);
     lo = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
 }
+
+// Which of the nodes, the deepest first, eight lanes take in a round: the shallowest behind the deepest.
+__device__ __forceinline__ int place_of(int round, int team) { return round ? MAX_NODES - 1 - team : team; }
 
 __device__ __forceinline__ float inverse(float x) {   // to one unit of fp32
     float y;
@@ -89,12 +91,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(sh.s_full[i]), STATE_WARPS);
             mbar_init(bar(sh.s_free[i]), 1);
-            mbar_init(bar(sh.coef_full[i]), PATH_WARPS);
+            mbar_init(bar(sh.coef_full[i]), PAIR_WARPS);
             mbar_init(bar(sh.coef_free[i]), COLUMN_WARPS);
         }
-        for (int i = 0; i < STAGES; ++i) mbar_init(bar(sh.stage_full[i]), 1), mbar_init(bar(sh.stage_free[i]), STATE_WARPS);
         mbar_init(bar(sh.b_full), PATH_WARPS);
-        mbar_init(bar(sh.b_free), 1);
+        mbar_init(bar(sh.b_free), 1 + PAIR_WARPS);   // the products, and the pair group
         mbar_init(bar(sh.d_full), 1);
         mbar_init(bar(sh.d_free), COLUMN_WARPS);
         sh.abort = 0;
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
         if (!ok) *abort = 1u;
         return ok;
     };
-    const int poller = warp < COLUMN_WARPS ? 0 : warp < COLUMN_WARPS + STATE_WARPS ? COLUMN_WARPS : COLUMN_WARPS + STATE_WARPS;
+    const int poller = warp < COLUMN_WARPS ? 0 : warp < PATH0 ? COLUMN_WARPS : warp < PAIR0 ? PATH0 : PAIR0;
     const auto group_wait = [&](unsigned long long &x, int phase, uint32_t id, uint32_t threads) {
         const bool ok = !group_or(id, threads, warp == poller && !wait(x, phase));
         fence_after();
@@ -286,27 +287,25 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
             }
             arrive(sh.meta_free[it % METAS]);
         }
-    } else if (warp < COLUMN_WARPS + STATE_WARPS) {
+    } else if (warp < PATH0) {
         const int col = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
             if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_STATE, 32 * STATE_WARPS)) break;
             const Meta &m = sh.meta[it % METAS];
-            const int n = m.n, slot = m.slot;
+            const int n = m.n, slot = m.slot, head = m.head;
             arrive(sh.meta_free[it % METAS]);
             if (n == 0) continue;
-            if (!group_wait(sh.s_free[c & 1], (c >> 1) + 1, BAR_STATE, 32 * STATE_WARPS)) break;
+            const float *src = S + (size_t)(slot < 0 ? 0 : slot) * slot_stride + (size_t)head * D * D + col;
             const uint32_t to = tmem + lanes + TM_S + (c & 1) * 128;
             bool ok = true;
 #pragma unroll 1
-            for (int part = 0; part < D / STAGE_ROWS; ++part) {
-                const int g = c * (D / STAGE_ROWS) + part, stage = g % STAGES;
-                if (!(ok = group_wait(sh.stage_full[stage], g / STAGES, BAR_STATE, 32 * STATE_WARPS))) break;
+            for (int part = 0; part < 4; ++part) {
                 float x[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = slot < 0 ? 0.f : sh.stage[stage][i][col];
-                arrive(sh.stage_free[stage]);
+                for (int i = 0; i < 32; ++i) x[i] = slot < 0 ? 0.f : __ldcs(src + (size_t)(32 * part + i) * D);
+                if (part == 0 && !(ok = group_wait(sh.s_free[c & 1], (c >> 1) + 1, BAR_STATE, 32 * STATE_WARPS))) break;
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) split2(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
@@ -319,62 +318,25 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
             arrive(sh.s_full[c & 1]);
             ++c;
         }
-    } else if (warp == LOADER) {
-        for (int it = 0;; ++it) {
-            const long long at = blockIdx.x + (long long)it * gridDim.x;
-            if (at >= items) break;
-            if (!warp_wait(sh.meta_full[it % METAS], it / METAS)) break;
-            const Meta &m = sh.meta[it % METAS];
-            const int n = m.n, slot = m.slot, head = m.head;
-            arrive(sh.meta_free[it % METAS]);
-            if (n == 0) continue;
-            bool ok = true;
-            for (int part = 0; part < D / STAGE_ROWS && ok; ++part) {
-                const int g = c * (D / STAGE_ROWS) + part, stage = g % STAGES;
-                ok = warp_wait(sh.stage_free[stage], g / STAGES + 1);
-                if (ok && lane == 0) {
-                    constexpr uint32_t bytes = sizeof(sh.stage[0]);
-                    mbar_arrive_expect_tx(bar(sh.stage_full[stage]), slot < 0 ? 0 : bytes);
-                    if (slot >= 0)
-                        bulk_g2s(smem_u32(&sh.stage[stage][0][0]),
-                                 S + (size_t)slot * slot_stride + ((size_t)head * D + STAGE_ROWS * part) * D, bytes,
-                                 bar(sh.stage_full[stage]));
-                }
-                __syncwarp();
-            }
-            if (!ok) break;
-            ++c;
-        }
-    } else {
+    } else if (warp < PAIR0) {
         constexpr int THREADS = 32 * PATH_WARPS;
-        const int t = tid - 32 * (COLUMN_WARPS + STATE_WARPS), sub = lane & 7;
+        const int t = tid - 32 * PATH0, sub = lane & 7;
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
-            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_PATH, THREADS)) break;
-            const Meta &m = sh.meta[it % METAS];
-            const int n = m.n;
+            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_PATH, THREADS)) break;   // and the last item's climbs
+            Meta &m = sh.meta[it % METAS];
+            const int n = m.n, rows = (n + 7) / 8 * 8;
             if (n > 0) {
-                const int lo = m.lo, head = m.head, rows = (n + 7) / 8 * 8;
-                const size_t first = ((size_t)lo * H + head) * D;
-                for (int i = t; i < n * (D / 4); i += THREADS)   // group_wait's barrier is behind the last item's reads
+                const size_t first = ((size_t)m.lo * H + m.head) * D;
+                for (int i = t; i < n * (D / 4); i += THREADS)
                     cp_async16(smem_u32(&sh.alpha[0][0]) + 16 * i, alpha + first + (size_t)(i / (D / 4)) * H * D + i % (D / 4) * 4);
-                const bool go = (t >> 3) < n;
-                if (__all_sync(0xffffffffu, !go)) {   // a warp without a node only keeps the barriers
-                    cp_async_wait();
-                    if (!group_wait(sh.coef_free[c & 1], (c >> 1) + 1, BAR_PATH, THREADS) ||
-                        !group_wait(sh.b_free, c + 1, BAR_PATH, THREADS))
-                        break;
-                    arrive(sh.b_full);
-                    group_sync(BAR_PATH, THREADS);
-                    group_sync(BAR_PATH, THREADS);
-                    arrive(sh.coef_full[c & 1]);
-                    arrive(sh.meta_free[it % METAS]);
-                    ++c;
-                    continue;
-                }
-                const int node = go ? m.order[t >> 3] : 0, above = go ? m.above[node] : -1;
-                Raw<__nv_bfloat16, 4> rk[4], rb[4], rq[4];
-                {
+                bool ok = true;
+#pragma unroll 1
+                for (int round = 0; round < 2; ++round) {
+                    const int place = place_of(round, t >> 3);
+                    const bool go = place < n;
+                    const int node = go ? m.order[place] : 0, above = go ? m.above[node] : -1;
+                    Raw<__nv_bfloat16, 4> rk[4], rb[4], rq[4];
                     const size_t row = first + (size_t)node * H * D + 4 * sub;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -383,57 +345,94 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                         rq[j].clear();
                         if (go) rk[j].load(k + row + 32 * j), rb[j].load(b + row + 32 * j), rq[j].load(q + row + 32 * j);
                     }
-                }
-                cp_async_wait();
-                if (!group_wait(sh.coef_free[c & 1], (c >> 1) + 1, BAR_PATH, THREADS)) break;
-                float *coef = sh.c[c & 1];
-                f32x2 e[4][2], g[4][2];
-                {
+                    if (round == 0) {
+                        cp_async_wait();
+                        group_sync(BAR_PATH, THREADS);
+                    }
                     f32x2 G[4][2];
                     climb<D>(&sh.alpha[0][0], m.anc, go, node, above, lane, G);
                     const bool good = in_range<D>(G, lane);
-                    if (go && sub == 0) sh.fine[node] = good;
-                    if (!group_wait(sh.b_free, c + 1, BAR_PATH, THREADS)) break;   // the products before; all have climbed
+                    // the products and the pairs of the item before
+                    if (round == 0 && !(ok = group_wait(sh.b_free, c + 1, BAR_PATH, THREADS))) break;
+                    if (!go) continue;
+                    if (sub == 0) m.fine[node] = good;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         float kk[4], bb[4], qq[4];
                         rk[j].get(kk);
                         rb[j].get(bb);
                         rq[j].get(qq);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const f32x2 k2 = pack2(kk[2 * h], kk[2 * h + 1]);
-                            e[j][h] = mul2(mul2(pack2(bb[2 * h], bb[2 * h + 1]), k2), G[j][h]);
-                            g[j][h] = mul2(pack2(qq[2 * h], qq[2 * h + 1]), G[j][h]);
-                        }
-                        if (go) {
-                            const float2 g0 = unpack2(G[j][0]), g1 = unpack2(G[j][1]);
-                            *reinterpret_cast<float4 *>(&sh.alpha[node][4 * (sub + 8 * j)]) =
-                                make_float4(kk[0] * inverse(g0.x), kk[1] * inverse(g0.y), kk[2] * inverse(g1.x), kk[3] * inverse(g1.y));
-                            const auto put = [&](uint32_t to, const f32x2 (&x)[2]) {
-                                const float2 x0 = unpack2(x[0]), x1 = unpack2(x[1]);
-                                uint2 hi, lo2;
-                                split2(x0.x, x0.y, hi.x, lo2.x);
-                                split2(x1.x, x1.y, hi.y, lo2.y);
-                                *reinterpret_cast<uint2 *>(sh.b_hi + to) = hi;
-                                *reinterpret_cast<uint2 *>(sh.b_lo + to) = lo2;
-                            };
-                            put(sw_off(node, 4 * (sub + 8 * j), 2 * MAX_NODES), e[j]);
-                            put(sw_off(rows + node, 4 * (sub + 8 * j), 2 * MAX_NODES), g[j]);
-                        }
+                        const float2 g0 = unpack2(G[j][0]), g1 = unpack2(G[j][1]);
+                        *reinterpret_cast<float4 *>(&sh.key[node][4 * (sub + 8 * j)]) =
+                            make_float4(kk[0] * inverse(g0.x), kk[1] * inverse(g0.y), kk[2] * inverse(g1.x), kk[3] * inverse(g1.y));
+                        const auto put = [&](int to, f32x2 x, f32x2 y) {
+                            const float2 x0 = unpack2(x), x1 = unpack2(y);
+                            const uint32_t at = sw_off(to, 4 * (sub + 8 * j), 2 * MAX_NODES);
+                            uint2 hi, lo2;
+                            split2(x0.x, x0.y, hi.x, lo2.x);
+                            split2(x1.x, x1.y, hi.y, lo2.y);
+                            *reinterpret_cast<uint2 *>(sh.b_hi + at) = hi;
+                            *reinterpret_cast<uint2 *>(sh.b_lo + at) = lo2;
+                        };
+                        put(node, mul2(mul2(pack2(bb[0], bb[1]), pack2(kk[0], kk[1])), G[j][0]),
+                            mul2(mul2(pack2(bb[2], bb[3]), pack2(kk[2], kk[3])), G[j][1]));
+                        put(rows + node, mul2(pack2(qq[0], qq[1]), G[j][0]), mul2(pack2(qq[2], qq[3]), G[j][1]));
                     }
                 }
+                if (!ok) break;
                 fence_async_smem();
                 arrive(sh.b_full);
-                group_sync(BAR_PATH, THREADS);   // every k / G is there
-                bool good = true;
-                for (int j = sub; j <= above; j += 8) good = good && sh.fine[m.anc[pairs(node) + j]];
-                good = (__ballot_sync(0xffffffffu, good) >> (lane & 24) & 0xffu) == 0xffu;
-                couple<D>(&sh.alpha[0][0], m.anc, sh.a, coef, go && good, node, above, lane, e, g);
-                if (__any_sync(0xffffffffu, go && !good))
-                    couple_far<__nv_bfloat16, D>(q, k, b, alpha, m.anc, sh.a, coef, go && !good, lo, H, head, node, above, lane);
-                group_sync(BAR_PATH, THREADS);   // every A and P is there
-                eliminate(sh.a, coef, m.anc, coef, go, node, above, lane);
+                ++c;
+            }
+            arrive(sh.meta_free[it % METAS]);
+        }
+    } else {
+        constexpr int THREADS = 32 * PAIR_WARPS;
+        const int t = tid - 32 * PAIR0, sub = lane & 7;
+        for (int it = 0;; ++it) {
+            if (blockIdx.x + (long long)it * gridDim.x >= items) break;
+            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_PAIR, THREADS)) break;
+            const Meta &m = sh.meta[it % METAS];
+            const int n = m.n, rows = (n + 7) / 8 * 8;
+            if (n > 0) {
+                if (!group_wait(sh.coef_free[c & 1], (c >> 1) + 1, BAR_PAIR, THREADS) ||
+                    !group_wait(sh.b_full, c, BAR_PAIR, THREADS))
+                    break;
+                float *coef = sh.c[c & 1];
+#pragma unroll 1
+                for (int round = 0; round < 2; ++round) {
+                    const int place = place_of(round, t >> 3);
+                    const bool go = place < n;
+                    if (__all_sync(0xffffffffu, !go)) continue;
+                    const int node = go ? m.order[place] : 0, above = go ? m.above[node] : -1;
+                    bool good = go;
+                    for (int j = sub; j <= above; j += 8) good = good && m.fine[m.anc[pairs(node) + j]];
+                    good = (__ballot_sync(0xffffffffu, good) >> (lane & 24) & 0xffu) == 0xffu;
+                    f32x2 e[4][2], g[4][2];   // the rows again: hi + lo
+                    const auto get = [&](int from, int j, f32x2 (&x)[2]) {
+                        const uint32_t at = sw_off(from, 4 * (sub + 8 * j), 2 * MAX_NODES);
+                        const uint2 hi = *reinterpret_cast<const uint2 *>(sh.b_hi + at), lo2 = *reinterpret_cast<const uint2 *>(sh.b_lo + at);
+                        const auto two = [](uint32_t x) { return pack2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)); };
+                        x[0] = add2(two(hi.x), two(lo2.x));
+                        x[1] = add2(two(hi.y), two(lo2.y));
+                    };
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) get(node, j, e[j]), get(rows + node, j, g[j]);
+                    couple<D>(&sh.key[0][0], m.anc, sh.a, coef, good, node, above, lane, e, g);
+                    if (__any_sync(0xffffffffu, go && !good))
+                        couple_far<__nv_bfloat16, D>(q, k, b, alpha, m.anc, sh.a, coef, go && !good, m.lo, H, m.head, node, above,
+                                                     lane);
+                }
+                arrive(sh.b_free);
+                group_sync(BAR_PAIR, THREADS);   // every A and P is there
+#pragma unroll 1
+                for (int round = 0; round < 2; ++round) {
+                    const int place = place_of(round, t >> 3);
+                    const bool go = place < n;
+                    if (__all_sync(0xffffffffu, !go)) continue;
+                    const int node = go ? m.order[place] : 0;
+                    eliminate(sh.a, coef, m.anc, coef, go, node, go ? m.above[node] : -1, lane);
+                }
                 arrive(sh.coef_full[c & 1]);
                 ++c;
             }
