@@ -77,7 +77,8 @@ __device__ __forceinline__ void climb(const float *sa, const unsigned char *anc,
     }
 }
 
-// Whether G_n and 1 / G_n can stand for themselves: at all the node's channels in [2^-100, 2^100].
+// Whether G_n and 1 / G_n can stand for themselves: at all the node's channels in [2^-80, 2^80], far enough from the
+// ends of fp32 for the products with tokens and for the second of two bf16 parts.
 template <int K>
 __device__ __forceinline__ bool in_range(const f32x2 (&G)[K / 32][2], int lane) {
     bool fine = true;
@@ -86,7 +87,7 @@ __device__ __forceinline__ bool in_range(const f32x2 (&G)[K / 32][2], int lane) 
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const float2 x = unpack2(G[j][c]);
-            fine = fine && x.x >= 0x1p-100f && x.x <= 0x1p100f && x.y >= 0x1p-100f && x.y <= 0x1p100f;   // false for a NaN
+            fine = fine && x.x >= 0x1p-80f && x.x <= 0x1p80f && x.y >= 0x1p-80f && x.y <= 0x1p80f;   // false for a NaN
         }
     return (__ballot_sync(0xffffffffu, fine) >> (lane & 24) & 0xffu) == 0xffu;
 }

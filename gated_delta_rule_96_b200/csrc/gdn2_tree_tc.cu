@@ -8,9 +8,10 @@
 // below the rounding of the bf16 output, where one product of bf16 operands would double that rounding.
 //   state group  (4 warps)  a column of S a thread, split, into tensor memory: the A operand S^T, lane = value
 //                           column, two buffers
-//   path group   (8 warps)  eight lanes a node up to its root: the rows e G and q G, split, into the B operand's
-//                           swizzled images, and k / G
-//   pair group   (8 warps)  the coefficients along the paths, from those
+//   path group   (8 warps)  G, two channels a thread from parents to children; then, eight lanes a node, the rows
+//                           e G, q G and k / G, split, into swizzled images
+//   pair group   (8 warps)  [e G; q G] [k / G]^T, 2n x 128 x n and split alike, holds A and P of all pairs of nodes:
+//                           from tensor memory (lane = row) those of the paths to lists, then the elimination
 //   column group (8 warps)  R = u - S^T (e G) and S^T (q G) from tensor memory (lane = value column) to shared
 //                           memory, then o = S^T (q G) + C R, two nodes a warp and eight columns a lane
 //   lead warp               reads and checks the items, lists their paths, brings the tokens' lines into L2 ahead
@@ -29,7 +30,7 @@ constexpr int PATH0 = COLUMN_WARPS + STATE_WARPS, PAIR0 = PATH0 + PATH_WARPS, LE
               TC_THREADS = 32 * (LEAD + 1);
 constexpr int METAS = 3;
 constexpr uint32_t BAR_COLUMN = 1, BAR_PATH = 2, BAR_PAIR = 3, BAR_STATE = 4, WAIT_LIMIT = 1u << 20;
-constexpr uint32_t TM_S = 0, TM_D = 256, TM_COLS = 512;   // S: two buffers of hi (64 columns) and lo (64)
+constexpr uint32_t TM_S = 0, TM_D = 256, TM_P = 384, TM_COLS = 512;   // S: two buffers of hi (64 columns) and lo (64)
 
 // An item: its nodes lo .. lo+n-1, the state's slot, the nodes' parents, paths and numbers of ancestors, and the
 // nodes by that number, the deepest first (so that the nodes of a warp take about as many steps).
@@ -42,12 +43,14 @@ struct Meta {
 
 struct TcShared {
     unsigned char b_hi[2 * MAX_NODES * D * 2], b_lo[2 * MAX_NODES * D * 2];   // [e G; q G], swizzled
-    float alpha[MAX_NODES][D], key[MAX_NODES][D];   // key: k / G
+    unsigned char k_hi[MAX_NODES * D * 2], k_lo[MAX_NODES * D * 2];           // k / G
+    float alpha[MAX_NODES][D];                // then G
     float r[MAX_NODES][D], x[MAX_NODES][D];   // u, then R; S^T (q G); by node and value column
     float a[MAX_PAIRS], c[2][MAX_PAIRS];      // A; P, then C
     Meta meta[METAS];
+    unsigned long long path[MAX_NODES];       // a bit for each node on a node's path
     unsigned long long meta_full[METAS], meta_free[METAS], s_full[2], s_free[2], coef_full[2], coef_free[2], b_full, b_free,
-        d_full, d_free;
+        d_full, d_free, p_full, p_free;
     uint32_t tmem, abort;
 };
 static_assert(sizeof(TcShared) + 1024 <= 227 * 1024, "shared memory of an SM");
@@ -95,9 +98,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
             mbar_init(bar(sh.coef_free[i]), COLUMN_WARPS);
         }
         mbar_init(bar(sh.b_full), PATH_WARPS);
-        mbar_init(bar(sh.b_free), 1 + PAIR_WARPS);   // the products, and the pair group
+        mbar_init(bar(sh.b_free), 1);
         mbar_init(bar(sh.d_full), 1);
         mbar_init(bar(sh.d_free), COLUMN_WARPS);
+        mbar_init(bar(sh.p_full), 2);   // the products, and the lead for what the path group wrote
+        mbar_init(bar(sh.p_free), PAIR_WARPS);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -183,18 +188,36 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                 arrive(sh.meta_full[it % METAS]);
             }
             if (before > 0) {   // the item before: its products
-                const int rows = (before + 7) / 8 * 8;
-                if (!warp_wait(sh.s_full[c & 1], c >> 1) || !warp_wait(sh.b_full, c) || !warp_wait(sh.d_free, c + 1)) break;
+                const int rows = (before + 7) / 8 * 8, cols = (before + 15) / 16 * 16;
+                const uint64_t hi = desc_kmajor(smem_u32(sh.b_hi), 2 * MAX_NODES, 0), lo = desc_kmajor(smem_u32(sh.b_lo), 2 * MAX_NODES, 0),
+                               k_hi = desc_kmajor(smem_u32(sh.k_hi), MAX_NODES, 0), k_lo = desc_kmajor(smem_u32(sh.k_lo), MAX_NODES, 0);
+                // eight steps of 16 channels; the address field counts 16 bytes: 32 bytes a step, and the half's image
+                const auto step = [](int rows, int j) { return (j >> 2) * (rows * 128 >> 4) + (j & 3) * 2; };
+                if (!warp_wait(sh.b_full, c) || !warp_wait(sh.p_free, c + 1)) break;
+                fence_after();
+                if (lane == 0) {   // the pairs; what lies behind the rows and columns of nodes is not read
+                    const uint32_t idesc = idesc_bf16(128, cols, 0, 0);
+                    const auto products = [&](uint64_t a, uint64_t desc, uint32_t acc) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            mma_ss(tmem + TM_P, a + step(2 * MAX_NODES, j), desc + step(MAX_NODES, j), idesc, acc | (j > 0));
+                    };
+                    products(hi, k_hi, 0);
+                    products(lo, k_hi, 1);
+                    products(hi, k_lo, 1);
+                    mma_commit(bar(sh.p_full));
+                    mbar_arrive(bar(sh.p_full));
+                }
+                __syncwarp();
+                if (!warp_wait(sh.s_full[c & 1], c >> 1) || !warp_wait(sh.d_free, c + 1)) break;
                 fence_after();
                 if (lane == 0) {
                     const uint32_t idesc = idesc_bf16(128, 2 * rows, 0, 0), s = tmem + TM_S + (c & 1) * 128;
-                    const auto products = [&](uint32_t a, uint64_t desc, uint32_t acc) {   // eight steps of 16 channels
+                    const auto products = [&](uint32_t a, uint64_t desc, uint32_t acc) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)   // the address field counts 16 bytes: 32 bytes a step, 16 KB a half
-                            mma_ts(tmem + TM_D, a + 8 * j, desc + (j >> 2) * (2 * MAX_NODES * 128 >> 4) + (j & 3) * 2, idesc, acc | (j > 0));
+                        for (int j = 0; j < 8; ++j)
+                            mma_ts(tmem + TM_D, a + 8 * j, desc + step(2 * MAX_NODES, j), idesc, acc | (j > 0));
                     };
-                    const uint64_t hi = desc_kmajor(smem_u32(sh.b_hi), 2 * MAX_NODES, 0),
-                                   lo = desc_kmajor(smem_u32(sh.b_lo), 2 * MAX_NODES, 0);
                     products(s, hi, 0);
                     products(s, lo, 1);
                     products(s + 64, hi, 1);
@@ -323,7 +346,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
         const int t = tid - 32 * PATH0, sub = lane & 7;
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
-            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_PATH, THREADS)) break;   // and the last item's climbs
+            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_PATH, THREADS)) break;   // and the last item's rows
             Meta &m = sh.meta[it % METAS];
             const int n = m.n, rows = (n + 7) / 8 * 8;
             if (n > 0) {
@@ -332,51 +355,71 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                     cp_async16(smem_u32(&sh.alpha[0][0]) + 16 * i, alpha + first + (size_t)(i / (D / 4)) * H * D + i % (D / 4) * 4);
                 bool ok = true;
 #pragma unroll 1
-                for (int round = 0; round < 2; ++round) {
-                    const int place = place_of(round, t >> 3);
-                    const bool go = place < n;
-                    const int node = go ? m.order[place] : 0, above = go ? m.above[node] : -1;
-                    Raw<__nv_bfloat16, 4> rk[4], rb[4], rq[4];
-                    const size_t row = first + (size_t)node * H * D + 4 * sub;
+                for (int round = 0; round < 2 && 32 * round < n; ++round) {
+                    const int node = 32 * round + (t >> 3);
+                    const bool go = node < n;
+                    Raw<__nv_bfloat16, 8> rk[2], rb[2], rq[2];
+                    const size_t row = first + (size_t)node * H * D + 8 * sub;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 2; ++j) {
                         rk[j].clear();
                         rb[j].clear();
                         rq[j].clear();
-                        if (go) rk[j].load(k + row + 32 * j), rb[j].load(b + row + 32 * j), rq[j].load(q + row + 32 * j);
+                        if (go) rk[j].load(k + row + 64 * j), rb[j].load(b + row + 64 * j), rq[j].load(q + row + 64 * j);
                     }
                     if (round == 0) {
                         cp_async_wait();
                         group_sync(BAR_PATH, THREADS);
+                        if (t < D / 2) {   // a parent stands before its children
+                            float *at = &sh.alpha[0][2 * t];
+                            for (int i0 = 0; i0 < n; i0 += 4) {
+                                const char4 p4 = *reinterpret_cast<const char4 *>(m.parent + i0);
+                                const int up[4] = {p4.x, p4.y, p4.z, p4.w};
+                                f32x2 a[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const f32x2 *>(at + (i0 + i) * D);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (i0 + i < n && up[i] >= 0)
+                                        *reinterpret_cast<f32x2 *>(at + (i0 + i) * D) = mul2(*reinterpret_cast<const f32x2 *>(at + up[i] * D), a[i]);
+                            }
+                        }
+                        if (!(ok = group_wait(sh.b_free, c + 1, BAR_PATH, THREADS))) break;   // the products of the item before
                     }
                     f32x2 G[4][2];
-                    climb<D>(&sh.alpha[0][0], m.anc, go, node, above, lane, G);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) load2(&sh.alpha[node][8 * sub + 64 * (j >> 1) + 4 * (j & 1)], G[j]);
                     const bool good = in_range<D>(G, lane);
-                    // the products and the pairs of the item before
-                    if (round == 0 && !(ok = group_wait(sh.b_free, c + 1, BAR_PATH, THREADS))) break;
                     if (!go) continue;
                     if (sub == 0) m.fine[node] = good;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float kk[4], bb[4], qq[4];
-                        rk[j].get(kk);
-                        rb[j].get(bb);
-                        rq[j].get(qq);
-                        const float2 g0 = unpack2(G[j][0]), g1 = unpack2(G[j][1]);
-                        *reinterpret_cast<float4 *>(&sh.key[node][4 * (sub + 8 * j)]) =
-                            make_float4(kk[0] * inverse(g0.x), kk[1] * inverse(g0.y), kk[2] * inverse(g1.x), kk[3] * inverse(g1.y));
-                        const auto put = [&](int to, f32x2 x, f32x2 y) {
-                            const float2 x0 = unpack2(x), x1 = unpack2(y);
-                            const uint32_t at = sw_off(to, 4 * (sub + 8 * j), 2 * MAX_NODES);
-                            uint2 hi, lo2;
-                            split2(x0.x, x0.y, hi.x, lo2.x);
-                            split2(x1.x, x1.y, hi.y, lo2.y);
-                            *reinterpret_cast<uint2 *>(sh.b_hi + at) = hi;
-                            *reinterpret_cast<uint2 *>(sh.b_lo + at) = lo2;
+                    for (int j = 0; j < 2; ++j) {
+                        const int at = 8 * sub + 64 * j;
+                        const auto put = [&](unsigned char *to_hi, unsigned char *to_lo, uint32_t to, const f32x2 (&x)[4]) {
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) split2(unpack2(x[i]).x, unpack2(x[i]).y, hi[i], lo[i]);
+                            *reinterpret_cast<uint4 *>(to_hi + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4 *>(to_lo + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         };
-                        put(node, mul2(mul2(pack2(bb[0], bb[1]), pack2(kk[0], kk[1])), G[j][0]),
-                            mul2(mul2(pack2(bb[2], bb[3]), pack2(kk[2], kk[3])), G[j][1]));
-                        put(rows + node, mul2(pack2(qq[0], qq[1]), G[j][0]), mul2(pack2(qq[2], qq[3]), G[j][1]));
+                        float kk[8], y[8];
+                        f32x2 x[4];
+                        rk[j].get(kk);
+                        rb[j].get(y);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i] = mul2(mul2(pack2(y[2 * i], y[2 * i + 1]), pack2(kk[2 * i], kk[2 * i + 1])), G[2 * j + (i >> 1)][i & 1]);
+                        put(sh.b_hi, sh.b_lo, sw_off(node, at, 2 * MAX_NODES), x);
+                        rq[j].get(y);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = mul2(pack2(y[2 * i], y[2 * i + 1]), G[2 * j + (i >> 1)][i & 1]);
+                        put(sh.b_hi, sh.b_lo, sw_off(rows + node, at, 2 * MAX_NODES), x);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 d = unpack2(G[2 * j + (i >> 1)][i & 1]);
+                            x[i] = mul2(pack2(kk[2 * i], kk[2 * i + 1]), pack2(inverse(d.x), inverse(d.y)));
+                        }
+                        put(sh.k_hi, sh.k_lo, sw_off(node, at, MAX_NODES), x);
                     }
                 }
                 if (!ok) break;
@@ -388,42 +431,57 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
         }
     } else {
         constexpr int THREADS = 32 * PAIR_WARPS;
-        const int t = tid - 32 * PAIR0, sub = lane & 7;
+        const int t = tid - 32 * PAIR0;
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
             if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_PAIR, THREADS)) break;
             const Meta &m = sh.meta[it % METAS];
             const int n = m.n, rows = (n + 7) / 8 * 8;
             if (n > 0) {
+                if (t < n) {
+                    unsigned long long path = 0ull;
+                    for (int h = 0; h <= m.above[t]; h += 4) {
+                        const uchar4 a4 = *reinterpret_cast<const uchar4 *>(m.anc + pairs(t) + h);
+                        path |= 1ull << a4.x | 1ull << a4.y | 1ull << a4.z | 1ull << a4.w;
+                    }
+                    sh.path[t] = path;
+                }
                 if (!group_wait(sh.coef_free[c & 1], (c >> 1) + 1, BAR_PAIR, THREADS) ||
-                    !group_wait(sh.b_full, c, BAR_PAIR, THREADS))
+                    !group_wait(sh.p_full, c, BAR_PAIR, THREADS))
                     break;
                 float *coef = sh.c[c & 1];
+                const unsigned long long fine = __ballot_sync(0xffffffffu, lane < n && m.fine[lane]) |
+                                                (unsigned long long)__ballot_sync(0xffffffffu, lane + 32 < n && m.fine[lane + 32]) << 32;
+                // A row a thread, half its columns: those on the row's path, where all their G are in range.  The
+                // ancestor i of a node stands above(node) - above(i) places behind it.
+                const int i0 = 32 * (warp - PAIR0 >> 2), line = 32 * (warp & 3) + lane, who = line < rows ? line : line - rows;
+                if (i0 < n && 32 * (warp & 3) < 2 * rows) {
+                    uint32_t y[32];
+                    tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + TM_P + i0, y);
+                    const unsigned long long path = who < n ? sh.path[who] : 0ull;
+                    const uint32_t mine = path & ~fine ? 0u : (uint32_t)(path >> i0);
+                    float *to = (line < rows ? sh.a : coef) + (who < n ? pairs(who) + m.above[who] : 0);
+                    wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const uchar4 a4 = *reinterpret_cast<const uchar4 *>(m.above + i0 + i);
+                        if (mine >> i & 1) to[-a4.x] = __uint_as_float(y[i]);
+                        if (mine >> (i + 1) & 1) to[-a4.y] = __uint_as_float(y[i + 1]);
+                        if (mine >> (i + 2) & 1) to[-a4.z] = __uint_as_float(y[i + 2]);
+                        if (mine >> (i + 3) & 1) to[-a4.w] = __uint_as_float(y[i + 3]);
+                    }
+                }
+                fence_before();
+                arrive(sh.p_free);
+                // the others from the tokens
 #pragma unroll 1
                 for (int round = 0; round < 2; ++round) {
-                    const int place = place_of(round, t >> 3);
-                    const bool go = place < n;
-                    if (__all_sync(0xffffffffu, !go)) continue;
-                    const int node = go ? m.order[place] : 0, above = go ? m.above[node] : -1;
-                    bool good = go;
-                    for (int j = sub; j <= above; j += 8) good = good && m.fine[m.anc[pairs(node) + j]];
-                    good = (__ballot_sync(0xffffffffu, good) >> (lane & 24) & 0xffu) == 0xffu;
-                    f32x2 e[4][2], g[4][2];   // the rows again: hi + lo
-                    const auto get = [&](int from, int j, f32x2 (&x)[2]) {
-                        const uint32_t at = sw_off(from, 4 * (sub + 8 * j), 2 * MAX_NODES);
-                        const uint2 hi = *reinterpret_cast<const uint2 *>(sh.b_hi + at), lo2 = *reinterpret_cast<const uint2 *>(sh.b_lo + at);
-                        const auto two = [](uint32_t x) { return pack2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)); };
-                        x[0] = add2(two(hi.x), two(lo2.x));
-                        x[1] = add2(two(hi.y), two(lo2.y));
-                    };
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) get(node, j, e[j]), get(rows + node, j, g[j]);
-                    couple<D>(&sh.key[0][0], m.anc, sh.a, coef, good, node, above, lane, e, g);
-                    if (__any_sync(0xffffffffu, go && !good))
-                        couple_far<__nv_bfloat16, D>(q, k, b, alpha, m.anc, sh.a, coef, go && !good, m.lo, H, m.head, node, above,
-                                                     lane);
+                    const int node = 32 * round + (t >> 3);
+                    const bool far = node < n && (sh.path[node] & ~fine);
+                    if (__any_sync(0xffffffffu, far))
+                        couple_far<__nv_bfloat16, D>(q, k, b, alpha, m.anc, sh.a, coef, far, m.lo, H, m.head, far ? node : 0,
+                                                     far ? m.above[node] : -1, lane);
                 }
-                arrive(sh.b_free);
                 group_sync(BAR_PAIR, THREADS);   // every A and P is there
 #pragma unroll 1
                 for (int round = 0; round < 2; ++round) {
