@@ -8,14 +8,15 @@
 // below the rounding of the bf16 output, where one product of bf16 operands would double that rounding.
 //   state group  (4 warps)  a column of S a thread, split, into tensor memory: the A operand S^T, lane = value
 //                           column, two buffers
-//   path group   (8 warps)  G, two channels a thread from parents to children; then, eight lanes a node, the rows
+//   path group   (8 warps)  G, a channel a thread from parents to children; then, eight lanes a node, the rows
 //                           e G, q G and k / G, split, into swizzled images
 //   pair group   (8 warps)  [e G; q G] [k / G]^T, 2n x 128 x n and split alike, holds A and P of all pairs of nodes:
 //                           from tensor memory (lane = row) those of the paths to lists, then the elimination
 //   column group (8 warps)  R = u - S^T (e G) and S^T (q G) from tensor memory (lane = value column) to shared
 //                           memory, then o = S^T (q G) + C R, two nodes a warp and eight columns a lane
-//   lead warp               reads and checks the items, lists their paths, brings the tokens' lines into L2 ahead
-//                           of the groups, and issues the products
+//   scout warp              reads and checks the items, lists their paths, brings the tokens' lines into L2 ahead
+//                           of the groups
+//   lead warp               issues the products
 #include "gdn2_tree.cuh"
 #include "tc_ptx.cuh"
 
@@ -25,9 +26,9 @@ namespace tree {
 using namespace gdn2::tc;
 
 constexpr int D = 128;
-constexpr int COLUMN_WARPS = 8, STATE_WARPS = 4, PATH_WARPS = 8, PAIR_WARPS = 8;   // in this order; then the lead
+constexpr int COLUMN_WARPS = 8, STATE_WARPS = 4, PATH_WARPS = 8, PAIR_WARPS = 8;   // in this order; then the lead and the scout
 constexpr int PATH0 = COLUMN_WARPS + STATE_WARPS, PAIR0 = PATH0 + PATH_WARPS, LEAD = PAIR0 + PAIR_WARPS,
-              TC_THREADS = 32 * (LEAD + 1);
+              SCOUT = LEAD + 1, TC_THREADS = 32 * (SCOUT + 1);
 constexpr int METAS = 3;
 constexpr uint32_t BAR_COLUMN = 1, BAR_PATH = 2, BAR_PAIR = 3, BAR_STATE = 4, WAIT_LIMIT = 1u << 20;
 constexpr uint32_t TM_S = 0, TM_D = 256, TM_P = 384, TM_COLS = 512;   // S: two buffers of hi (64 columns) and lo (64)
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
     volatile uint32_t *abort = &sh.abort;
 
     if (tid == 0) {
-        for (int i = 0; i < METAS; ++i) mbar_init(bar(sh.meta_full[i]), 1), mbar_init(bar(sh.meta_free[i]), LEAD);   // a warp each, but the lead
+        for (int i = 0; i < METAS; ++i) mbar_init(bar(sh.meta_full[i]), 1), mbar_init(bar(sh.meta_free[i]), SCOUT);   // a warp each, but the scout
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(sh.s_full[i]), STATE_WARPS);
             mbar_init(bar(sh.s_free[i]), 1);
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
     };
 
     int c = 0;
-    if (warp == LEAD) {
+    if (warp == SCOUT) {
         const auto look = [&](long long at, Meta &m) {
             const int seq = (int)(at / H), head = (int)(at % H), lo = cu[seq], hi = cu[seq + 1], slot = slots[seq];
             unsigned bad = 0;
@@ -175,20 +176,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                 prefetch_l2(alpha + row);
                 prefetch_l2(alpha + row + 32);
             }
-            __syncwarp();
-            return n;
         };
-        int before = 0;   // nodes of the item before
         for (int it = 0;; ++it) {
             const long long at = blockIdx.x + (long long)it * gridDim.x;
-            int n = 0;
-            if (at < items) {
-                if (!warp_wait(sh.meta_free[it % METAS], it / METAS + 1)) break;
-                n = look(at, sh.meta[it % METAS]);
-                arrive(sh.meta_full[it % METAS]);
-            }
-            if (before > 0) {   // the item before: its products
-                const int rows = (before + 7) / 8 * 8, cols = (before + 15) / 16 * 16;
+            if (at >= items || !warp_wait(sh.meta_free[it % METAS], it / METAS + 1)) break;
+            look(at, sh.meta[it % METAS]);
+            arrive(sh.meta_full[it % METAS]);
+        }
+    } else if (warp == LEAD) {
+        for (int it = 0;; ++it) {
+            if (blockIdx.x + (long long)it * gridDim.x >= items) break;
+            if (!warp_wait(sh.meta_full[it % METAS], it / METAS)) break;
+            const int n = sh.meta[it % METAS].n;
+            arrive(sh.meta_free[it % METAS]);
+            if (n > 0) {
+                const int rows = (n + 7) / 8 * 8, cols = (n + 15) / 16 * 16;
                 const uint64_t hi = desc_kmajor(smem_u32(sh.b_hi), 2 * MAX_NODES, 0), lo = desc_kmajor(smem_u32(sh.b_lo), 2 * MAX_NODES, 0),
                                k_hi = desc_kmajor(smem_u32(sh.k_hi), MAX_NODES, 0), k_lo = desc_kmajor(smem_u32(sh.k_lo), MAX_NODES, 0);
                 // eight steps of 16 channels; the address field counts 16 bytes: 32 bytes a step, and the half's image
@@ -228,8 +230,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                 __syncwarp();
                 ++c;
             }
-            if (at >= items) break;
-            before = n;
         }
     } else if (warp < COLUMN_WARPS) {
         const int col = tid & 127, half = tid >> 7;   // value column, warpgroup
@@ -353,7 +353,35 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                 const size_t first = ((size_t)m.lo * H + m.head) * D;
                 for (int i = t; i < n * (D / 4); i += THREADS)
                     cp_async16(smem_u32(&sh.alpha[0][0]) + 16 * i, alpha + first + (size_t)(i / (D / 4)) * H * D + i % (D / 4) * 4);
-                bool ok = true;
+                cp_async_wait();
+                group_sync(BAR_PATH, THREADS);
+                if (t < D) {   // G from parents to children, who stand behind them: four nodes a load latency
+                    float *at = &sh.alpha[0][t];
+                    float next[4];
+                    char4 next4 = *reinterpret_cast<const char4 *>(m.parent);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) next[i] = at[i * D];
+#pragma unroll 1
+                    for (int i0 = 0; i0 < n; i0 += 4) {
+                        const int up[4] = {next4.x, next4.y, next4.z, next4.w};
+                        float x[4], g[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) g[i] = at[min(max(up[i], 0), i0) * D], x[i] = next[i];
+                        const int ahead = min(i0 + 4, MAX_NODES - 4);
+                        next4 = *reinterpret_cast<const char4 *>(m.parent + ahead);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) next[i] = at[(ahead + i) * D];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                            for (int f = 0; f < i; ++f) g[i] = up[i] == i0 + f ? x[f] : g[i];
+                            x[i] *= up[i] < 0 ? 1.f : g[i];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) at[(i0 + i) * D] = x[i];   // behind the last node: anything
+                    }
+                }
+                if (!group_wait(sh.b_free, c + 1, BAR_PATH, THREADS)) break;   // the products of the item before
 #pragma unroll 1
                 for (int round = 0; round < 2 && 32 * round < n; ++round) {
                     const int node = 32 * round + (t >> 3);
@@ -366,25 +394,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                         rb[j].clear();
                         rq[j].clear();
                         if (go) rk[j].load(k + row + 64 * j), rb[j].load(b + row + 64 * j), rq[j].load(q + row + 64 * j);
-                    }
-                    if (round == 0) {
-                        cp_async_wait();
-                        group_sync(BAR_PATH, THREADS);
-                        if (t < D / 2) {   // a parent stands before its children
-                            float *at = &sh.alpha[0][2 * t];
-                            for (int i0 = 0; i0 < n; i0 += 4) {
-                                const char4 p4 = *reinterpret_cast<const char4 *>(m.parent + i0);
-                                const int up[4] = {p4.x, p4.y, p4.z, p4.w};
-                                f32x2 a[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const f32x2 *>(at + (i0 + i) * D);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    if (i0 + i < n && up[i] >= 0)
-                                        *reinterpret_cast<f32x2 *>(at + (i0 + i) * D) = mul2(*reinterpret_cast<const f32x2 *>(at + up[i] * D), a[i]);
-                            }
-                        }
-                        if (!(ok = group_wait(sh.b_free, c + 1, BAR_PATH, THREADS))) break;   // the products of the item before
                     }
                     f32x2 G[4][2];
 #pragma unroll
@@ -422,7 +431,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                         put(sh.k_hi, sh.k_lo, sw_off(node, at, MAX_NODES), x);
                     }
                 }
-                if (!ok) break;
                 fence_async_smem();
                 arrive(sh.b_full);
                 ++c;
