@@ -205,14 +205,16 @@ int launch_t(const void *q, const void *k, const void *v, const float *alpha, co
     return launch_status();
 }
 
-// Which kernel: the tensor-core one's period for an item hardly depends on its nodes (5.3 us an SM for one, 12.5
-// for 64), this one's grows with them and is half of it for one; H16, us, this / that:
-//   one user      8 nodes  7.0 / 9.0   16 nodes   8.6 / 10.1   32 nodes  14.8 / 12.7   64 nodes  27.7 / 17.7
-//   4 users       8 nodes  9.3 / 9.9   16 nodes  12.3 / 10.4
-//   32 users      8 nodes 24.9 / 28.2  16 nodes  38.1 / 32.0   32 nodes  77.0 / 42.5
-//   128 users     8 nodes 96.3 / 91.8  16 nodes 144.3 / 103.2  64 nodes 609.1 / 190.7
+// Which kernel: the tensor-core one's period for an item hardly depends on its nodes (6.0 us an SM for one, 10.6 for
+// 64), this one's grows with them and is two thirds of it for one; H16, cold caches, us, this / that:
+//   one user      8 nodes  8.8 / 11.5   16 nodes  10.1 / 12.3   32 nodes  16.3 / 13.7   64 nodes  30.2 / 18.7
+//   4 users       8 nodes 11.4 / 11.9   32 nodes  25.0 / 14.5
+//   8 users       4 nodes 10.5 / 12.4    8 nodes  12.5 / 12.6   32 nodes  26.6 / 16.0   64 nodes  45.7 / 22.3
+//   32 users      4 nodes 23.0 / 26.1    8 nodes  29.5 / 26.7   16 nodes  43.6 / 28.4   32 nodes  72.1 / 34.0
+//   128 users     4 nodes 70.8 / 83.3    8 nodes  92.9 / 85.2   16 nodes 139.6 / 87.9   64 nodes 575.5 / 146.4
 bool use_tc(int batch, int H, int max_nodes) {
-    return max_nodes > 16 || (max_nodes > 8 && (long long)batch * H > 32);
+    const long long items = (long long)batch * H;
+    return max_nodes > (items > 148 ? 6 : items > 32 ? 8 : 16);
 }
 
 }  // namespace tree

@@ -223,7 +223,7 @@ GDN2_API int gdn2_add_norm_bwd(const void *h, const void *x, const float *scale,
  *   max_nodes  the most nodes of a tree, at most GDN2_TREE_MAX_NODES
  *
  * A node reads only itself and its ancestors: values of other branches, NaN included, do not reach
- * it.  Any decay is exact, zero included.  batch at most 65,535.  An accepted path is taken into the
+ * it.  Any decay is exact, zero included.  o must not alias an input.  batch at most 65,535.  An accepted path is taken into the
  * cache by gdn2_recurrent_fwd with the path's nodes as `index`.
  */
 #define GDN2_TREE_MAX_NODES 64
@@ -250,9 +250,11 @@ GDN2_API int gdn2_tree_fwd(const void *q, const void *k, const void *v, const fl
  *                                left as they were
  *
  * A slot that one sequence writes may be neither read nor written by another one of the call: such a
- * writer is left out (GDN2_DEV_CONFLICT).  The token rows are walked one at a time in fp32, with the
- * state in registers: exact for any decay, and meant for runs up to some hundred tokens (long
- * prompts: gdn2_chunk_fwd).  batch and H at most 65,535.
+ * writer is left out (GDN2_DEV_CONFLICT).  Sequences may share tokens through `index`, but not
+ * entries.  o must not alias an input.  The state stays on the SM from a run's first token to its
+ * last, in fp32; every fourth token ends a block of the chunk form whose decay ratios are products,
+ * so any decay is exact.  Meant for runs up to some hundred tokens (long prompts: gdn2_chunk_fwd).
+ * batch and H at most 65,535.
  */
 GDN2_API int gdn2_recurrent_fwd(const void *q, const void *k, const void *v, const float *alpha, const void *b,
                                 const void *w, float *S, long long slot_stride, int num_slots, const int *slots_in,
