@@ -5,7 +5,9 @@ Tolerances.  A step of the recurrence in fp32 adds at most some 22 roundings of 
 to the largest term (16 in-thread and 3 shuffled additions of a dot product, the decay, the update), the map
 of a step does not grow what came before by more than the terms' own size, and the longest runs here have 64
 steps: 22 * 64 * 2^-24 = 8.4e-5 of the largest value, under the fp32 bar of 1e-4 that the other parity tests
-use.  bf16 outputs add one rounding, 2^-8 of the value.  Copies are exact."""
+use.  bf16 outputs add one rounding, 2^-8 of the value.  Where trees are taken on the tensor cores, a factor is two
+bf16, 2^-17 off: for unit vectors of 128 channels a product of two is off by some 2^-16 / sqrt(128) = 1.3e-6, on a
+path of 64 nodes by sqrt(64) times that, 1.1e-5.  Copies are exact."""
 import numpy as np
 import pytest
 
@@ -114,6 +116,34 @@ def test_tree_shapes_on_a_zero_state_and_with_hard_decays(dtype, shape, n):
         o, ref, rows, status = run_tree(torch, g, x, make_pool(torch, 2, 3, 2, 128, 128), [-1, 2], [n, n], parents * 2)
         assert status == 0
         close(o, ref, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("decay", [2.0 ** -20, 2.0 ** -39, 0.42, 0.3])
+def test_tree_decays_whose_products_leave_the_range_along_a_path(dtype, decay):
+    """The products pass 2^-80, and further down fp32's smallest number, on every long path, with short ones beside."""
+    torch, g = cuda_or_skip()
+    n = 64
+    parents = [i - 1 for i in range(n)] + [-1] + [(i - 1) // 2 if i % 3 else i - 1 for i in range(1, n)]
+    x = tokens(torch, 5, 2 * n, 3, 128, 128, dtype)
+    x[3].fill_(decay)
+    x[3][::5, :, 7] = 1.0                        # a channel that decays less than the others
+    o, ref, rows, status = run_tree(torch, g, x, make_pool(torch, 6, 2, 3, 128, 128), [1, 0], [n, n], parents)
+    assert status == 0
+    close(o, ref, dtype)
+
+
+@pytest.mark.parametrize("heads", [3, 40])
+def test_tree_sizes_of_every_kernel(heads):
+    """The same trees as few and as many items, in calls for every most number of nodes: the kernels agree."""
+    torch, g = cuda_or_skip()
+    for n in (1, 5, 6, 7, 8, 9, 15, 16, 17, 24, 25):
+        sizes = [n, max(1, n // 2), n, 0, n]
+        parents = sum((random_tree(np.random.default_rng(n), m, 4) for m in sizes), [])
+        x = tokens(torch, n, sum(sizes), heads, 128, 128, "bf16")
+        o, ref, rows, status = run_tree(torch, g, x, make_pool(torch, n, 5, heads, 128, 128), [4, 2, -1, 1, 0], sizes, parents)
+        assert status == 0
+        close(o, ref, "bf16")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
