@@ -37,6 +37,20 @@ int check_norm(long long rows, float eps, int dtype) {
     return eps >= 0.f && eps <= 1.f ? GDN2_OK : GDN2_ERR_VALUE;
 }
 
+// Whether slots of two caches share memory without being one cache: where their ranges meet, they must lie one
+// stride apart and between one another.
+bool caches_clash(const float *a, long long stride_a, int slots_a, const float *b, long long stride_b, int slots_b,
+                  long long floats) {
+    if (!slots_a || !slots_b || !floats || a == b) return false;
+    const long long apart = ((long long)reinterpret_cast<uintptr_t>(b) - (long long)reinterpret_cast<uintptr_t>(a)) / 4;
+    if (apart >= (slots_a - 1) * stride_a + floats || -apart >= (slots_b - 1) * stride_b + floats) return false;
+    if (slots_a == 1 && slots_b == 1) return true;
+    const long long stride = slots_a == 1 ? stride_b : stride_a;   // one slot has no stride
+    if (slots_a > 1 && slots_b > 1 && stride_a != stride_b) return true;
+    const long long into = (apart % stride + stride) % stride;
+    return into < floats || stride - into < floats;
+}
+
 // a cache of states: `num_slots` slots of [H, d_k, d_v] floats, `slot_stride` floats apart
 int check_pool(const void *S, long long slot_stride, int num_slots, int H, int K, int V) {
     if (slot_stride < (long long)H * K * V) return GDN2_ERR_SHAPE;
@@ -389,6 +403,7 @@ int gdn2_state_copy(float *dst, long long dst_stride, int dst_slots, const float
     if (slot_floats % 4 || dst_stride % 4 || src_stride % 4) return GDN2_ERR_ALIGN;
     if (pairs > GDN2_STATE_COPY_MAX_PAIRS || slot_floats > (1ll << 31)) return GDN2_ERR_UNSUPPORTED;
     if (dst == src && dst_stride != src_stride) return GDN2_ERR_SHAPE;
+    if (caches_clash(dst, dst_stride, dst_slots, src, src_stride, src_slots, slot_floats)) return GDN2_ERR_SHAPE;
     int rc = check_workspace(workspace, workspace_bytes, gdn2::kStatusBytes);
     if (rc != GDN2_OK) return rc;
     if (pairs == 0 || slot_floats == 0) return GDN2_OK;

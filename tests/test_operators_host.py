@@ -10,6 +10,7 @@ import gated_delta_rule_96_b200 as g
 P = ctypes.c_void_p
 F = P(0x10000)       # never dereferenced: every call below fails validation first or has nothing to do
 ODD = P(0x10004)
+at = lambda floats: P(0x10000 + 4 * floats)  # noqa: E731
 
 
 @pytest.fixture(scope="module")
@@ -84,6 +85,16 @@ NAN = float("nan")
     (lambda l: copy(l, dstride=32), -2), (lambda l: copy(l, dstride=66), -7), (lambda l: copy(l, dstride=128), -2),
     (lambda l: copy(l, dst=None), -1), (lambda l: copy(l, idx=None), -1), (lambda l: copy(l, src=P(0x20008)), -7),
     (lambda l: copy(l, ws=None), -5), (lambda l: copy(l, n=0), -5), (lambda l: copy(l, pairs=0, idx=None), 0),
+    # two caches of 4 slots of 64 floats that share memory (a later part of one, from the end of one slot into the
+    # next, the last slot alone, other strides), and ones that do not (behind, before, between one another)
+    (lambda l: copy(l, src=at(64)), -2), (lambda l: copy(l, src=at(-64)), -2), (lambda l: copy(l, src=at(192), snum=1), -2),
+    (lambda l: copy(l, dstride=128, sstride=128, src=at(60)), -2), (lambda l: copy(l, dstride=128, sstride=128, src=at(-60)), -2),
+    (lambda l: copy(l, dstride=128, sstride=64, src=at(64), pairs=0), -2),
+    (lambda l: copy(l, dnum=1, snum=1, src=at(60), pairs=0), -2), (lambda l: copy(l, src=at(256), pairs=0), 0),
+    (lambda l: copy(l, src=at(-256), pairs=0), 0), (lambda l: copy(l, dstride=128, sstride=128, src=at(64), pairs=0), 0),
+    (lambda l: copy(l, dstride=128, sstride=128, src=at(-64), pairs=0), 0),
+    (lambda l: copy(l, dnum=1, sstride=128, src=at(-64), pairs=0), 0), (lambda l: copy(l, dnum=1, sstride=128, src=at(-128)), -2),
+    (lambda l: copy(l, snum=0, src=at(64), pairs=0), 0),
 ])
 def test_entry_points_refuse(lib, call, want):
     assert call(lib) == want
