@@ -26,7 +26,7 @@ __all__ = [
     "gated_norm_bwd", "gdn2_gated_norm", "gdn2_add_norm_fwd", "gdn2_add_norm_bwd",
     "gdn2_add_norm_bwd_workspace_bytes", "add_norm_fwd", "add_norm_bwd", "gdn2_add_norm", "gdn2_tree_fwd",
     "tree_fwd", "gdn2_recurrent_fwd", "recurrent_fwd", "gdn2_state_copy", "TREE_MAX_NODES",
-    "STATE_COPY_MAX_PAIRS", "DEV_RANGE", "DEV_SLOT", "DEV_PARENT", "DEV_INDEX", "DEV_CONFLICT",
+    "STATE_COPY_MAX_PAIRS", "DEV_RANGE", "DEV_SLOT", "DEV_PARENT", "DEV_INDEX", "DEV_CONFLICT", "DEV_WAIT",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,7 +41,7 @@ TREE_MAX_NODES = 64              # GDN2_TREE_MAX_NODES in include/gdn2.h
 STATE_COPY_MAX_PAIRS = 1024      # GDN2_STATE_COPY_MAX_PAIRS
 GATES = {"silu": 0, "sigmoid": 1}   # gdn2_gate
 # bits of a workspace's status word for malformed device-side indices (GDN2_DEV_*)
-DEV_RANGE, DEV_SLOT, DEV_PARENT, DEV_INDEX, DEV_CONFLICT = 0x100, 0x200, 0x400, 0x800, 0x1000
+DEV_RANGE, DEV_SLOT, DEV_PARENT, DEV_INDEX, DEV_CONFLICT, DEV_WAIT = 0x100, 0x200, 0x400, 0x800, 0x1000, 0x2000
 
 
 class GDN2Error(RuntimeError):
@@ -706,11 +706,13 @@ def _norm_fn(which):
 
 def gdn2_gated_norm(o, gate, weight, act="silu", eps=1e-6):
     """Differentiable gated norm: y = RMSNorm(o) * weight * act(gate) over the last axis, with gradients of
-    o, gate and weight through gdn2_gated_norm_bwd.  CUDA tensors as gdn2_gated_norm_fwd's."""
+    o, gate and weight through gdn2_gated_norm_bwd.  CUDA tensors as gdn2_gated_norm_fwd's.  As for any torch op, a
+    backward pass is captured into a CUDA graph only while no eager graph of the same leaves is alive."""
     return _norm_fn(0).apply(o, gate, weight, act, eps)
 
 
 def gdn2_add_norm(x, residual, weight, scale=None, eps=1e-6):
     """Differentiable residual norm: returns (y, h) with h = residual + scale * x and y = RMSNorm(h) * weight,
-    gradients of x, residual, scale and weight through gdn2_add_norm_bwd.  residual and scale may be None."""
+    gradients of x, residual, scale and weight through gdn2_add_norm_bwd.  residual and scale may be None.  Capture as
+    for gdn2_gated_norm."""
     return _norm_fn(1).apply(x, residual, scale, weight, eps)

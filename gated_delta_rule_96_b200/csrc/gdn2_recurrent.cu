@@ -45,7 +45,9 @@ template <int K, int V>
 constexpr int PRODUCERS = K == 128 && V == 128 ? 2 : 4;
 constexpr int DEPTH = 2;       // state buffers: one worked on, one on its way in or out
 constexpr int RING = 6;        // token blocks ahead
-constexpr uint32_t WAIT_LIMIT = 1u << 21;   // polls, a second or more
+// Polls: a second or more.  The storer and the scout wait for a whole run, up to 0.8 us a token: some 32 polls of the
+// shortest kind a token are added.
+constexpr uint32_t WAIT_LIMIT = 1u << 21, WAIT_TOKEN = 32;
 
 template <int K, int V>
 struct Block {
@@ -302,7 +304,8 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
     __syncthreads();
 
     bool ok = true;   // every wait is bounded; a warp whose wait ran out reports it and leaves
-    auto wait = [&](unsigned long long &x, int phase) { return ok = ok && mbar_wait(bar(x), phase & 1, WAIT_LIMIT); };
+    const uint32_t limit = (uint32_t)min((long long)WAIT_LIMIT + (long long)WAIT_TOKEN * total, 0xffffffffll);
+    auto wait = [&](unsigned long long &x, int phase) { return ok = ok && mbar_wait(bar(x), phase & 1, limit); };
     auto state_of = [&](long long at, int slot) {   // the item's part of a slot
         const int split = (int)(at % splits), head = (int)(at / splits % H);
         return S + (size_t)slot * slot_stride + (size_t)head * K * V + split * cols;

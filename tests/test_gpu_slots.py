@@ -301,6 +301,25 @@ def test_recurrent_is_the_decode_step_and_the_prefill():
     assert np.abs(f64(pool) - f64(ref_S)).max() <= 2 * BAR * np.abs(f64(ref_S)).max()
 
 
+def test_recurrent_runs_of_any_length():
+    """A run of 1.2 million tokens: the warps that wait for its end are not taken for stuck; its halves, one after the
+    other, are the same blocks of four tokens."""
+    torch, g = cuda_or_skip()
+    n, half = 1200001, 600000
+    gen = torch.Generator("cuda").manual_seed(1)
+    r = lambda: torch.randn(n, 1, 64, generator=gen, device="cuda")  # noqa: E731
+    x = [0.1 * r(), 0.1 * r(), r(), torch.sigmoid(r() + 2), torch.sigmoid(r()), torch.sigmoid(r())]
+    pool = make_pool(torch, 1, 2, 1, 64, 64)
+    pool[1] = pool[0]
+    ws = g.new_workspace(0)
+    o = g.recurrent_fwd(*x, pool, i32(torch, [0]), i32(torch, [0]), i32(torch, [0, n]), workspace=ws)
+    first = g.recurrent_fwd(*(a[:half] for a in x), pool, i32(torch, [1]), i32(torch, [1]), i32(torch, [0, half]), workspace=ws)
+    second = g.recurrent_fwd(*(a[half:] for a in x), pool, i32(torch, [1]), i32(torch, [1]), i32(torch, [0, n - half]), workspace=ws)
+    assert g.gdn2_workspace_status(ws) == 0
+    assert torch.equal(o[:half], first) and torch.equal(o[half:], second) and torch.equal(pool[0], pool[1])
+    assert torch.isfinite(o).all() and o.abs().max() > 0
+
+
 def test_recurrent_reports_malformed_indices_and_conflicts():
     torch, g = cuda_or_skip()
     H, n = 2, 3
