@@ -14,6 +14,29 @@ inline bool allow_smem(Kernel kern, size_t bytes) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
+// A launch that the device prepares while the stream's kernel before it still runs: its blocks are placed as that
+// one's leave, and wait there for its end.  One call behind another, us, without and with it: a fork 5.6 / 3.2, one
+// user's tree 8.8 / 6.8, a decode step of residual norms 5.4 / 4.9 (the host), B256 H16 of runs 102 / 99.
+// (griddepcontrol.launch_dependents at the top of every kernel, which lets the next one's blocks in as soon as all of
+// its own have started, is slower: 3.5, 7.0, 4.8, 100, and the full batch of trees 142 against 137.)
+template <typename... Params, typename... Args>
+inline int launch_close(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args) {
+    cudaLaunchAttribute close = {};
+    close.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    close.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = grid;
+    config.blockDim = dim3((unsigned)threads);
+    config.dynamicSmemBytes = smem;
+    config.stream = st;
+    config.attrs = &close;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, kern, static_cast<Params>(args)...) == cudaSuccess ? 0 : -6;
+}
+// First in every such kernel, before any access to memory that is not the block's own: waits until the kernel before
+// has ended and its writes can be seen.
+__device__ __forceinline__ void behind_last_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Status header at the start of every prefill workspace (device status words).
 constexpr size_t kStatusBytes = 256;
 

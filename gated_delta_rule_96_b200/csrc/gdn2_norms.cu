@@ -91,6 +91,7 @@ template <typename Tok, int D, int ACT, int U>
 __global__ void __launch_bounds__(256) gated_norm_fwd_kernel(const Tok *o, const Tok *gate,
                                                              const float *__restrict__ weight, Tok *y,
                                                              long long rows, float eps) {
+    behind_last_kernel();
     using V = V16<Tok>;
     constexpr int N = V::N, LPR = D / N, RPW = 32 / LPR;
     const int lane = threadIdx.x & 31, sub = lane % LPR;
@@ -131,6 +132,7 @@ __global__ void __launch_bounds__(256) gated_norm_bwd_kernel(const Tok *__restri
                                                              const Tok *__restrict__ dy, Tok *__restrict__ d_o,
                                                              Tok *__restrict__ dgate, float *__restrict__ partial,
                                                              long long rows, float eps) {
+    behind_last_kernel();
     using V = V16<Tok>;
     constexpr int N = V::N, LPR = D / N, RPW = 32 / LPR;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPR;
@@ -206,6 +208,7 @@ __global__ void __launch_bounds__(256) gated_norm_bwd_kernel(const Tok *__restri
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float *__restrict__ partial, int groups, int columns,
                                                           float *__restrict__ out0, float *__restrict__ out1,
                                                           int split) {
+    behind_last_kernel();
     __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float t = 0.f;
@@ -250,6 +253,7 @@ __global__ void __launch_bounds__(512) add_norm_fwd_kernel(const Tok *x, const T
                                                            const float *__restrict__ scale,
                                                            const float *__restrict__ weight, Tok *h, Tok *y,
                                                            long long rows, int vecs, float eps) {
+    behind_last_kernel();
     using V = V16<Tok>;
     constexpr int N = V::N;
     __shared__ float s_sum[2][MAX_WARPS][1];
@@ -309,6 +313,7 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) add_norm_bwd_kernel(cons
                                                            Tok *__restrict__ dres, Tok *__restrict__ dx,
                                                            float *__restrict__ partial, long long rows, int vecs,
                                                            float eps) {
+    behind_last_kernel();
     using V = V16<Tok>;
     constexpr int N = V::N;
     __shared__ float s_sum[2][MAX_WARPS][2];
@@ -424,23 +429,20 @@ int gated_fwd_t(const void *o, const void *gate, const float *weight, void *y, l
     // four rows a thread in flight hide the latency of a long stream; a few rows are spread over more blocks
     auto go = [&](auto kern, int u) {
         const long long per_block = (long long)PER_BLOCK * u;
-        kern<<<(unsigned)((rows + per_block - 1) / per_block), 256, 0, st>>>((const Tok *)o, (const Tok *)gate, weight,
-                                                                           (Tok *)y, rows, eps);
+        return launch_close(kern, (unsigned)((rows + per_block - 1) / per_block), 256, 0, st, (const Tok *)o, (const Tok *)gate,
+                            weight, (Tok *)y, rows, eps);
     };
-    if (rows >= (long long)PER_BLOCK * 4 * SMS * 2) go(gated_norm_fwd_kernel<Tok, D, ACT, 4>, 4);
-    else go(gated_norm_fwd_kernel<Tok, D, ACT, 1>, 1);
-    return launch_status();
+    return rows >= (long long)PER_BLOCK * 4 * SMS * 2 ? go(gated_norm_fwd_kernel<Tok, D, ACT, 4>, 4)
+                                                      : go(gated_norm_fwd_kernel<Tok, D, ACT, 1>, 1);
 }
 template <typename Tok, int D, int ACT>
 int gated_bwd_t(const void *o, const void *gate, const float *weight, const void *dy, void *d_o, void *dgate,
                 float *dweight, long long rows, float eps, float *partial, cudaStream_t st) {
     static const int per_sm = resident(gated_norm_bwd_kernel<Tok, D, ACT>, 256, 0);   // the same on every B200
     const int blocks = cap_blocks((rows + 7) / 8, per_sm);
-    gated_norm_bwd_kernel<Tok, D, ACT><<<blocks, 256, 0, st>>>((const Tok *)o, (const Tok *)gate, weight,
-                                                               (const Tok *)dy, (Tok *)d_o, (Tok *)dgate, partial,
-                                                               rows, eps);
-    column_sum_kernel<<<D / 32, 1024, 0, st>>>(partial, blocks, D, dweight, nullptr, D);
-    return launch_status();
+    const int rc = launch_close(gated_norm_bwd_kernel<Tok, D, ACT>, blocks, 256, 0, st, (const Tok *)o, (const Tok *)gate, weight,
+                                (const Tok *)dy, (Tok *)d_o, (Tok *)dgate, partial, rows, eps);
+    return rc ? rc : launch_close(column_sum_kernel, D / 32, 1024, 0, st, partial, blocks, D, dweight, nullptr, D);
 }
 
 template <typename Tok>
@@ -449,13 +451,13 @@ int add_fwd_t(const void *x, const void *residual, const float *scale, const flo
     const int vecs = width / V16<Tok>::N, nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4, nt = row_threads(vecs, nv);
     const unsigned blocks = (unsigned)(rows < (1 << 30) ? rows : (1 << 30));
     auto go = [&](auto kern) {
-        kern<<<blocks, nt, 0, st>>>((const Tok *)x, (const Tok *)residual, scale, weight, (Tok *)h, (Tok *)y, rows,
-                                    vecs, eps);
+        return launch_close(kern, blocks, nt, 0, st, (const Tok *)x, (const Tok *)residual, scale, weight, (Tok *)h, (Tok *)y, rows,
+                            vecs, eps);
     };
-    if (nv == 1) go(add_norm_fwd_kernel<Tok, 1>);
-    else if (nv == 2) go(add_norm_fwd_kernel<Tok, 2>);
-    else if constexpr (sizeof(Tok) == 4) go(add_norm_fwd_kernel<Tok, 4>);   // bf16 rows end at 1024 vectors
-    return launch_status();
+    if (nv == 1) return go(add_norm_fwd_kernel<Tok, 1>);
+    if (nv == 2) return go(add_norm_fwd_kernel<Tok, 2>);
+    if constexpr (sizeof(Tok) == 4) return go(add_norm_fwd_kernel<Tok, 4>);
+    return -6;   // bf16 rows end at 1024 vectors
 }
 template <typename Tok, bool SCALED>
 int add_bwd_t(const void *h, const void *x, const float *scale, const float *weight, const void *dy, const void *dh,
@@ -464,21 +466,18 @@ int add_bwd_t(const void *h, const void *x, const float *scale, const float *wei
     const int vecs = width / V16<Tok>::N, nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4, nt = row_threads(vecs, nv);
     const int columns = width * (SCALED ? 2 : 1);
     int blocks = 0;
-    bool ok = false;
+    int rc = -6;
     auto go = [&](auto kern) {
         const size_t smem = sizeof(float) * (size_t)columns;
-        ok = allow_smem(kern, sizeof(float) * 2 * MAX_WIDTH);
-        if (!ok) return;
+        if (!allow_smem(kern, sizeof(float) * 2 * MAX_WIDTH)) return;
         blocks = cap_blocks(rows, resident(kern, nt, smem));
-        kern<<<blocks, nt, smem, st>>>((const Tok *)h, (const Tok *)x, scale, weight, (const Tok *)dy, (const Tok *)dh,
-                                    (Tok *)dres, (Tok *)dx, partial, rows, vecs, eps);
+        rc = launch_close(kern, blocks, nt, smem, st, (const Tok *)h, (const Tok *)x, scale, weight, (const Tok *)dy, (const Tok *)dh,
+                          (Tok *)dres, (Tok *)dx, partial, rows, vecs, eps);
     };
     if (nv == 1) go(add_norm_bwd_kernel<Tok, 1, SCALED>);
     else if (nv == 2) go(add_norm_bwd_kernel<Tok, 2, SCALED>);
     else if constexpr (sizeof(Tok) == 4) go(add_norm_bwd_kernel<Tok, 4, SCALED>);   // bf16 rows end at 1024 vectors
-    if (!ok) return -6;
-    column_sum_kernel<<<(columns + 31) / 32, 1024, 0, st>>>(partial, blocks, columns, dweight, dscale, width);
-    return launch_status();
+    return rc ? rc : launch_close(column_sum_kernel, (columns + 31) / 32, 1024, 0, st, partial, blocks, columns, dweight, dscale, width);
 }
 
 }  // namespace norms

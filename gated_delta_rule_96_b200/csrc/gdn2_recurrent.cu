@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
     // a producer waits for a ring slot's last use by its parity: it must not be two uses ahead of the consumers
     static_assert(RING >= NP, "each producer's blocks are NP apart");
     extern __shared__ __align__(128) unsigned char raw[];
+    behind_last_kernel();
     Shared<K, V> &sh = *reinterpret_cast<Shared<K, V> *>(raw);
     float *buffers = reinterpret_cast<float *>(raw + sizeof(Shared<K, V>));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -447,10 +448,9 @@ int launch_out(const void *q, const void *k, const void *v, const float *alpha, 
     int splits = 1;
     while (splits < V / 16 && (long long)batch * H * splits * 2 <= 148) splits *= 2;
     const long long items = (long long)batch * H * splits, grid = items < 148 * per_sm ? items : 148 * per_sm;
-    kern<<<(unsigned)grid, 2 * V / splits + 32 * EXTRA_WARPS<K, V>, smem_bytes<K, V>(V / splits), st>>>(
-        (const Tok *)q, (const Tok *)k, (const Tok *)v, alpha, (const Tok *)b, (const Tok *)w, S, slot_stride,
-        num_slots, slots_in, slots_out, cu, index, (Tok *)o, batch, H, splits, total, rows, status);
-    return launch_status();
+    return launch_close(kern, (unsigned)grid, 2 * V / splits + 32 * EXTRA_WARPS<K, V>, smem_bytes<K, V>(V / splits), st,
+                        (const Tok *)q, (const Tok *)k, (const Tok *)v, alpha, (const Tok *)b, (const Tok *)w, S, slot_stride,
+                        num_slots, slots_in, slots_out, cu, index, (Tok *)o, batch, H, splits, total, rows, status);
 }
 
 template <typename Tok, int K, int V>

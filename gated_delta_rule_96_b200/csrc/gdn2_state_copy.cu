@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(THREADS) state_copy_kernel(float *dst, long lo
                                                              const int *__restrict__ src_idx, int n, int group,
                                                              int slot_vecs, unsigned *status) {
     extern __shared__ __align__(16) unsigned char raw[];
+    behind_last_kernel();
     const Layout l = layout(n, group);
     int *s_dst = reinterpret_cast<int *>(raw + l.pairs), *s_src = s_dst + n, *s_key = s_src + n, *s_last = s_key + l.table;
     const int tid = threadIdx.x, first = blockIdx.x * RANGE, len = min(RANGE, slot_vecs - first);
@@ -152,9 +153,8 @@ int launch_state_copy(float *dst, long long dst_stride, int dst_slots, const flo
     group = group < 1 ? 1 : group > GROUP ? GROUP : group;
     const size_t smem = layout(n, (int)group).total;
     if (!allow_smem(state_copy_kernel, layout(kStateCopyMaxPairs, GROUP).total)) return -6;
-    state_copy_kernel<<<dim3((unsigned)ranges, (unsigned)((n + group - 1) / group)), THREADS, smem, st>>>(
-        dst, dst_stride, dst_slots, src, src_stride, src_slots, dst_idx, src_idx, n, (int)group, (int)vecs, status);
-    return launch_status();
+    return launch_close(state_copy_kernel, dim3((unsigned)ranges, (unsigned)((n + group - 1) / group)), THREADS, smem, st, dst,
+                        dst_stride, dst_slots, src, src_stride, src_slots, dst_idx, src_idx, n, (int)group, (int)vecs, status);
 }
 
 }  // namespace gdn2

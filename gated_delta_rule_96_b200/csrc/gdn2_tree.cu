@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q,
                                                    int splits, int total, int max_nodes, unsigned *status) {
     constexpr int RJ = K / 32;
     extern __shared__ __align__(16) float smem[];
+    behind_last_kernel();
     const int cols = V / splits, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
     const int head = blockIdx.x / splits, col0 = blockIdx.x % splits * cols, seq = blockIdx.y;
     float *sk = smem, *sa = sk + max_nodes * K, *se = sa + max_nodes * K, *sq = se + max_nodes * K;   // sk: k / G
@@ -199,10 +200,9 @@ int launch_t(const void *q, const void *k, const void *v, const float *alpha, co
     while (splits < V / 16 && (long long)batch * H * splits * 2 <= 148) splits *= 2;
     const int cols = V / splits;
     if (!allow_smem(tree_kernel<Tok, K, V>, smem(MAX_NODES, V))) return -6;
-    tree_kernel<Tok, K, V><<<dim3(H * splits, batch), 2 * cols < 128 ? 128 : 2 * cols, smem(max_nodes, cols), st>>>(
-        (const Tok *)q, (const Tok *)k, (const Tok *)v, alpha, (const Tok *)b, (const Tok *)w, S, slot_stride,
-        num_slots, slots, cu, parents, (Tok *)o, H, splits, total, max_nodes, status);
-    return launch_status();
+    return launch_close(tree_kernel<Tok, K, V>, dim3(H * splits, batch), 2 * cols < 128 ? 128 : 2 * cols, smem(max_nodes, cols),
+                        st, (const Tok *)q, (const Tok *)k, (const Tok *)v, alpha, (const Tok *)b, (const Tok *)w, S, slot_stride,
+                        num_slots, slots, cu, parents, (Tok *)o, H, splits, total, max_nodes, status);
 }
 
 // Which kernel: the tensor-core one's period for an item hardly depends on its nodes (6.0 us an SM for one, 10.6 for

@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
     const int *__restrict__ cu, const int *__restrict__ parents, __nv_bfloat16 *__restrict__ o, int batch, int H,
     int total, int max_nodes, unsigned *status) {
     extern __shared__ unsigned char raw[];
+    behind_last_kernel();
     TcShared &sh = *reinterpret_cast<TcShared *>(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long items = (long long)batch * H;
@@ -521,10 +522,9 @@ int launch_tc(const void *q, const void *k, const void *v, const float *alpha, c
     if (!allow_smem(tree_tc_kernel, smem)) return -6;
     using bf = __nv_bfloat16;
     const long long items = (long long)batch * H;
-    tree_tc_kernel<<<(unsigned)(items < 148 ? items : 148), TC_THREADS, smem, st>>>(
-        (const bf *)q, (const bf *)k, (const bf *)v, alpha, (const bf *)b, (const bf *)w, S, slot_stride, num_slots, slots,
-        cu, parents, (bf *)o, batch, H, total, max_nodes, status);
-    return launch_status();
+    return launch_close(tree_tc_kernel, (unsigned)(items < 148 ? items : 148), TC_THREADS, smem, st, (const bf *)q, (const bf *)k,
+                        (const bf *)v, alpha, (const bf *)b, (const bf *)w, S, slot_stride, num_slots, slots, cu, parents,
+                        (bf *)o, batch, H, total, max_nodes, status);
 }
 
 }  // namespace tree

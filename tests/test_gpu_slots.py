@@ -456,6 +456,52 @@ def test_calls_on_a_side_stream_allocate_there():
     torch.cuda.synchronize()
 
 
+def test_calls_behind_one_another_see_what_the_last_one_wrote():
+    """Chains of calls with nothing between them, each of which reads what the one before wrote (a launch is prepared
+    while that one still runs), against the same calls one at a time; eager and in a graph."""
+    torch, g = cuda_or_skip()
+    x = tokens(torch, 3, 12, 16, 128, 128, "bf16")
+    weight = torch.ones(2048, device="cuda")
+    slots, cu, parents = i32(torch, [0, 1, 2]), i32(torch, [0, 4, 8, 12]), i32(torch, [-1, 0, 1, 1] * 3)
+    to, frm = i32(torch, [1, 2, 3, 0]), i32(torch, [0, 1, 2, 3])
+    ws, first = g.new_workspace(0), make_pool(torch, 3, 4, 16, 128, 128)
+
+    def chain(pool, o, rows, between):
+        for _ in range(12):
+            g.gdn2_recurrent_fwd(*x, pool, slots, slots, cu, None, o, workspace=ws)
+            between()
+            g.gdn2_state_copy(pool, pool, to, frm, workspace=ws)
+            between()
+            g.gdn2_tree_fwd(*x, pool, slots, cu, parents, o, 4, workspace=ws)
+            between()
+            g.gdn2_add_norm_fwd(o.view(12, 2048), rows, None, weight, rows, o.view(12, 2048))
+            between()
+            g.gdn2_gated_norm_fwd(o, x[2], weight[:128], x[2])
+            between()
+            pool.mul_(0.99)
+            between()
+            g.decode_step(*(a[:4].contiguous() for a in x), pool)
+
+    def run(between, graph=None):
+        pool, o, rows, v = first.clone(), torch.zeros_like(x[2]), torch.zeros(12, 2048, device="cuda").bfloat16(), x[2].clone()
+        torch.cuda.synchronize()
+        if graph is None:
+            chain(pool, o, rows, between)
+        else:
+            with torch.cuda.graph(graph):
+                chain(pool, o, rows, between)
+            graph.replay()
+        torch.cuda.synchronize()
+        out = [pool, o, rows, x[2].clone()]
+        x[2].copy_(v)
+        return out
+    want = run(torch.cuda.synchronize)
+    assert all(torch.isfinite(a.float()).all() for a in want)
+    for got in [run(lambda: None) for _ in range(5)] + [run(lambda: None, torch.cuda.CUDAGraph())]:
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert g.gdn2_workspace_status(ws) == 0
+
+
 def test_two_graphs_share_a_workspace():
     """The workspace of the calls over slots holds status words only: two captured graphs replayed at the same
     time on two streams do not disturb one another, and what either reports stays reported."""
