@@ -33,7 +33,7 @@ inline int launch_close(void (*kern)(Params...), dim3 grid, int threads, size_t 
     config.numAttrs = 1;
     return cudaLaunchKernelEx(&config, kern, static_cast<Params>(args)...) == cudaSuccess ? 0 : -6;
 }
-// First in every such kernel, before any access to memory that is not the block's own: waits until the kernel before
+// In every such kernel, before any access to memory that is not the block's own: waits until the kernel before
 // has ended and its writes can be seen.
 __device__ __forceinline__ void behind_last_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

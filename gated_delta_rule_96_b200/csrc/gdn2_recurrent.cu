@@ -280,7 +280,6 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
     // a producer waits for a ring slot's last use by its parity: it must not be two uses ahead of the consumers
     static_assert(RING >= NP, "each producer's blocks are NP apart");
     extern __shared__ __align__(128) unsigned char raw[];
-    behind_last_kernel();
     Shared<K, V> &sh = *reinterpret_cast<Shared<K, V> *>(raw);
     float *buffers = reinterpret_cast<float *>(raw + sizeof(Shared<K, V>));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -303,6 +302,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
+    behind_last_kernel();
 
     bool ok = true;   // every wait is bounded; a warp whose wait ran out reports it and leaves
     const uint32_t limit = (uint32_t)min((long long)WAIT_LIMIT + (long long)WAIT_TOKEN * total, 0xffffffffll);

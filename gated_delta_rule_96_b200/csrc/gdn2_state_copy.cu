@@ -44,7 +44,6 @@ __global__ void __launch_bounds__(THREADS) state_copy_kernel(float *dst, long lo
                                                              const int *__restrict__ src_idx, int n, int group,
                                                              int slot_vecs, unsigned *status) {
     extern __shared__ __align__(16) unsigned char raw[];
-    behind_last_kernel();
     const Layout l = layout(n, group);
     int *s_dst = reinterpret_cast<int *>(raw + l.pairs), *s_src = s_dst + n, *s_key = s_src + n, *s_last = s_key + l.table;
     const int tid = threadIdx.x, first = blockIdx.x * RANGE, len = min(RANGE, slot_vecs - first);
@@ -56,6 +55,7 @@ __global__ void __launch_bounds__(THREADS) state_copy_kernel(float *dst, long lo
     }
     for (int i = tid; i < RANGE; i += THREADS) reinterpret_cast<uint4 *>(raw + 16)[i] = make_uint4(0, 0, 0, 0);
     fence_async_smem();   // the zeros are read by bulk copies
+    behind_last_kernel();
     for (int i = tid; i < n; i += THREADS) {
         int d = dst_idx[i], s = src_idx[i];
         if (d < -1 || d >= dst_slots || s < -1 || s >= src_slots) {

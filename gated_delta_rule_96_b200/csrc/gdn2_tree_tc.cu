@@ -84,7 +84,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
     const int *__restrict__ cu, const int *__restrict__ parents, __nv_bfloat16 *__restrict__ o, int batch, int H,
     int total, int max_nodes, unsigned *status) {
     extern __shared__ unsigned char raw[];
-    behind_last_kernel();
     TcShared &sh = *reinterpret_cast<TcShared *>(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long items = (long long)batch * H;
@@ -108,6 +107,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    behind_last_kernel();   // and only then tensor memory, which it may hold
     if (warp == LEAD) tmem_alloc(smem_u32(&sh.tmem), TM_COLS);
     fence_before();
     __syncthreads();
