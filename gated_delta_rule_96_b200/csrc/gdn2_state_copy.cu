@@ -7,10 +7,13 @@
 // Both cases move every byte once by bulk copies through shared memory.  Which one a call is, every block
 // finds for itself while its first copies are on their way, from a table of the pairs' destinations:
 // - No slot that changes is read: a block moves 4 KB of each of a few pairs.  4 KB pieces keep DRAM pages
-//   together: compaction of 192 pairs of 1 MB took 77, 67 and 60 us in pieces of 256, 512 and 1,024 bytes.
+//   together: compaction of 192 pairs of 1 MB takes 52 us, and 77, 67 and 60 in
+//   pieces of 256, 512 and 1,024 bytes.
 // - A slot that changes is read too (a reorder in place): a block owns a position range in every slot at
 //   once, as much of it as shared memory holds of all pairs, and writes once all of it has landed.  No other
 //   block touches the range, so any permutation needs no order among the pairs.
+// The compaction runs at 5.6 TB/s of the 6.5 that a plain copy reaches; a fork (three copies of 1 MB) takes 4 us with
+// cold caches and 3 behind another call.
 #include "gdn2_internal.h"
 #include "gdn2_slots.cuh"
 #include "tc_ptx.cuh"

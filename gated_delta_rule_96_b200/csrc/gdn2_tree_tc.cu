@@ -17,6 +17,10 @@
 //   scout warp              reads and checks the items, lists their paths, brings the tokens' lines into L2 ahead
 //                           of the groups
 //   lead warp               issues the products
+// 128 trees of 64 nodes, H16, take 145 us for 403 MB: 10.6 us an item, of which memory needs 4.5.  Half of the issue
+// slots are taken, by the splitting of the operands, the decays, the elimination and the sums; with the pairs on CUDA
+// cores in one group with the paths it took 191 us, with those in groups of their own 181.  Few items (32 trees of up to
+// 32 nodes: 32 us) wait for the chain of one.
 #include "gdn2_tree.cuh"
 #include "tc_ptx.cuh"
 
