@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q,
     if (lo < 0 || hi < lo || hi > total || hi - lo > max_nodes) bad = DEV_RANGE;
     else if (slot < -1 || slot >= num_slots) bad = DEV_SLOT;
 
-    // The state is on its way before the first barrier.
+    // Everything is on its way before the first barrier: the state to registers, the tokens as they are stored to where
+    // their products with the decays will stand.
     // The warp's slice of the state: rows 4 (rg + 8 j) + i, columns c0 .. c0 + 3; where there are more warps than
     // column groups they share the nodes.
     const int groups = cols / 16, shares = (nt >> 5) / groups;
@@ -69,33 +70,40 @@ __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q,
         if (p < -1 || p >= tid) bad = DEV_PARENT;
         sp[tid] = p;
     }
-    Raw<Tok, 4> rk[RJ], rb[RJ], rq[RJ];   // of the lane's node
-    const auto fetch = [&](int node) {
-        const size_t row = ((size_t)(lo + node) * H + head) * K + 4 * (lane & 7);
+    constexpr int TOK = sizeof(Tok);
+    Tok *raw_v = reinterpret_cast<Tok *>(TOK == 4 ? sr : ss), *raw_w = reinterpret_cast<Tok *>(ss) + (TOK == 4 ? 0 : cols);
+    const int pitch = cols * 4 / TOK;   // of a node's v and w: bf16 ones share a row of ss
+    for (int node = warp; node < n; node += nt >> 5) {   // a warp a node, 16 bytes a lane
+        const size_t row = (size_t)(lo + node) * H + head;
+        const auto bring = [&](void *to, const void *from, int at) {
+            cp_async16((uint32_t)__cvta_generic_to_shared(to) + at, static_cast<const char *>(from) + at);
+        };
+        constexpr int CHUNKS = TOK * K / 16;   // of a row of k, b or q
 #pragma unroll
-        for (int j = 0; j < RJ; ++j) {
-            rk[j].clear();
-            rb[j].clear();
-            rq[j].clear();
-            if (node < n) rk[j].load(k + row + 32 * j), rb[j].load(b + row + 32 * j), rq[j].load(q + row + 32 * j);
+        for (int i = 0; i < K / 4; i += 32)
+            if (i + lane < K / 4) bring(sa + node * K, alpha + row * K, 16 * (i + lane));
+#pragma unroll
+        for (int i = 0; i < 3 * CHUNKS; i += 32) {
+            const int which = (i + lane) / CHUNKS, at = 16 * ((i + lane) % CHUNKS);
+            if (which < 3) bring((which == 0 ? sk : which == 1 ? se : sq) + node * K, (which == 0 ? k : which == 1 ? b : q) + row * K, at);
         }
-    };
+        const int chunks = TOK * cols / 16;
+        for (int i = lane; i < 2 * chunks; i += 32)
+            if (i < chunks) bring(raw_v + node * pitch, v + row * V + col0, 16 * i);
+            else bring(raw_w + node * pitch, w + row * V + col0, 16 * (i - chunks));
+    }
+    cp_async_wait();
     if (__syncthreads_or(bad != 0)) {
         if (bad) atomicOr(status, bad);
         return;
     }
     if (n == 0) return;
-#pragma unroll 4
-    for (int i = tid; i < n * (K / 4); i += nt)   // alpha of all nodes, four channels a thread at a time
-        *reinterpret_cast<float4 *>(sa + 4 * i) = *reinterpret_cast<const float4 *>(
-            alpha + ((size_t)(lo + i / (K / 4)) * H + head) * K + i % (K / 4) * 4);
-#pragma unroll 4
     for (int i = tid; i < n * (cols / 4); i += nt) {   // u, until the product is taken off it
-        const size_t at = ((size_t)(lo + i / (cols / 4)) * H + head) * V + col0 + i % (cols / 4) * 4;
+        const int at = i / (cols / 4) * pitch + i % (cols / 4) * 4;
         Raw<Tok, 4> rv, rw;
         float x[4], y[4];
-        rv.load(v + at);
-        rw.load(w + at);
+        rv.load(raw_v + at);
+        rw.load(raw_w + at);
         rv.get(x);
         rw.get(y);
         *reinterpret_cast<float4 *>(sr + 4 * i) = make_float4(x[0] * y[0], x[1] * y[1], x[2] * y[2], x[3] * y[3]);
@@ -104,7 +112,15 @@ __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q,
     __syncthreads();
     for (int n0 = warp * 4; n0 < n; n0 += nt / 8) {
         const int node = n0 + (lane >> 3), sub = lane & 7;
-        fetch(node);
+        Raw<Tok, 4> rk[RJ], rb[RJ], rq[RJ];
+        if (node < n)
+#pragma unroll
+            for (int j = 0; j < RJ; ++j) {
+                rk[j].load(reinterpret_cast<const Tok *>(sk + node * K) + 4 * (sub + 8 * j));
+                rb[j].load(reinterpret_cast<const Tok *>(se + node * K) + 4 * (sub + 8 * j));
+                rq[j].load(reinterpret_cast<const Tok *>(sq + node * K) + 4 * (sub + 8 * j));
+            }
+        __syncwarp();   // before the first of the node's lanes writes over them
         f32x2 G[RJ][2];
         climb<K>(sa, anc, node < n, node, node < n ? depth[node] : -1, lane, G);
         const bool good = in_range<K>(G, lane);

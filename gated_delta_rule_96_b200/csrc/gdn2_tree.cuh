@@ -20,6 +20,11 @@ __host__ __device__ constexpr int pairs(int node) { return 4 * (node / 4 + 1) * 
 constexpr int MAX_PAIRS = pairs(MAX_NODES);
 static_assert(pairs(0) == 0 && pairs(1) == 4 && pairs(4) == 16 && pairs(5) == 24 && pairs(64) == 2176, "row starts");
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // What follows the paths takes eight lanes a node, four nodes a warp; all lanes of a warp make the calls, and
 // `go` says whether the lane's node takes part (its eight lanes alike).
 

@@ -60,11 +60,6 @@ struct TcShared {
 };
 static_assert(sizeof(TcShared) + 1024 <= 227 * 1024, "shared memory of an SM");
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // x = hi + lo, two values at a time as packed bf16 (the first in the low half).  An infinity leaves a NaN in lo:
 // what it meets is not finite either way.
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
