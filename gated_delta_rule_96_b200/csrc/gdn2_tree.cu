@@ -33,8 +33,9 @@ __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q,
     constexpr int RJ = K / 32;
     extern __shared__ __align__(16) float smem[];
     behind_last_kernel();
-    const int cols = V / splits, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-    const int head = blockIdx.x / splits, col0 = blockIdx.x % splits * cols, seq = blockIdx.y;
+    // splits, cols and groups are powers of two: shifts, where a division by them takes as long as a load
+    const int split_bits = __ffs(splits) - 1, cols = V >> split_bits, tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+    const int head = blockIdx.x >> split_bits, col0 = (blockIdx.x & (splits - 1)) * cols, seq = blockIdx.y;
     float *sk = smem, *sa = sk + max_nodes * K, *se = sa + max_nodes * K, *sq = se + max_nodes * K;   // sk: k / G
     float *sr = sq + max_nodes * K, *ss = sr + max_nodes * cols;
     float *cA = ss + max_nodes * cols, *cP = cA + pairs(max_nodes);
@@ -51,8 +52,8 @@ __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q,
     // their products with the decays will stand.
     // The warp's slice of the state: rows 4 (rg + 8 j) + i, columns c0 .. c0 + 3; where there are more warps than
     // column groups they share the nodes.
-    const int groups = cols / 16, shares = (nt >> 5) / groups;
-    const int rg = lane >> 2, c0 = warp % groups * 16 + (lane & 3) * 4;
+    const int groups = cols / 16, group_bits = __ffs(groups) - 1, shares = nt >> 5 >> group_bits;
+    const int rg = lane >> 2, c0 = (warp & (groups - 1)) * 16 + (lane & 3) * 4;
     float s[RJ][4][4];
 #pragma unroll
     for (int j = 0; j < RJ; ++j)
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q,
     }
     if (n == 0) return;
     for (int i = tid; i < n * (cols / 4); i += nt) {   // u, until the product is taken off it
-        const int at = i / (cols / 4) * pitch + i % (cols / 4) * 4;
+        const int at = (i >> (group_bits + 2)) * pitch + (i & (cols / 4 - 1)) * 4;
         Raw<Tok, 4> rv, rw;
         float x[4], y[4];
         rv.load(raw_v + at);
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q,
 
     // S^T (e G) and S^T (q G) of every node
 #pragma unroll 2
-    for (int t = warp / groups; t < n; t += shares) {
+    for (int t = warp >> group_bits; t < n; t += shares) {
         float p[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) p[c] = 0.f;
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q,
     // o: four columns a thread, the nodes in turn over the block
     const size_t first = ((size_t)lo * H + head) * V + col0;
     for (int i = tid; i < n * (cols / 4); i += nt) {
-        const int node = i / (cols / 4), col = i % (cols / 4) * 4, base = pairs(node), above = depth[node];
+        const int node = i >> (group_bits + 2), col = (i & (cols / 4 - 1)) * 4, base = pairs(node), above = depth[node];
         float4 x = *reinterpret_cast<const float4 *>(ss + 4 * i);
 #pragma unroll 4
         for (int j = 0; j <= above; ++j) {
