@@ -250,8 +250,9 @@ __device__ __forceinline__ void consume(const Block<K, V> &in, float (&s)[K / 32
 }
 
 // An item as the scout found it; a malformed one, and one with nothing to do, has n = 0, from = to = -1.
+// The divisions that give its head and column range are the scout's, ahead of the others.
 struct Item {
-    int lo, n, from, to;
+    int lo, n, from, to, head, col0;
 };
 
 template <int K, int V>
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
     Shared<K, V> &sh = *reinterpret_cast<Shared<K, V> *>(raw);
     float *buffers = reinterpret_cast<float *>(raw + sizeof(Shared<K, V>));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int cols = V / splits, consumers = cols / 16;
+    const int split_bits = __ffs(splits) - 1, cols = V >> split_bits, consumers = cols / 16;   // splits: a power of two
     const bool whole = splits == 1;
     const long long items = (long long)batch * H * splits;
     auto bar = [&](unsigned long long &x) { return smem_u32(&x); };
@@ -307,15 +308,15 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
     bool ok = true;   // every wait is bounded; a warp whose wait ran out reports it and leaves
     const uint32_t limit = (uint32_t)min((long long)WAIT_LIMIT + (long long)WAIT_TOKEN * total, 0xffffffffll);
     auto wait = [&](unsigned long long &x, int phase) { return ok = ok && mbar_wait(bar(x), phase & 1, limit); };
-    auto state_of = [&](long long at, int slot) {   // the item's part of a slot
-        const int split = (int)(at % splits), head = (int)(at / splits % H);
-        return S + (size_t)slot * slot_stride + (size_t)head * K * V + split * cols;
+    auto state_of = [&](const Item &x, int slot) {   // the item's part of a slot
+        return S + (size_t)slot * slot_stride + (size_t)x.head * K * V + x.col0;
     };
 
     if (warp == consumers + NP) {   // scout
         auto look = [&](long long at) {
-            const int seq = (int)(at / splits / H), hi = cu[seq + 1];
-            Item x = {cu[seq], 0, slots_in[seq], slots_out[seq]};
+            const long long chain = at >> split_bits;
+            const int seq = (int)(chain / H), hi = cu[seq + 1], head = (int)(chain - (long long)seq * H);
+            Item x = {cu[seq], 0, slots_in[seq], slots_out[seq], head, (int)(at & (splits - 1)) * cols};
             unsigned bad = 0;
             if (x.lo < 0 || hi < x.lo || hi > total) bad = DEV_RANGE;
             else if (x.from < -1 || x.from >= num_slots || x.to < -1 || x.to >= num_slots) bad = DEV_SLOT;
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
             bad = __reduce_or_sync(0xffffffffu, bad);
             x.n = hi - x.lo;
             if (bad && lane == 0) atomicOr(status, bad);
-            if (bad || (x.n == 0 && x.from == x.to)) x = {0, 0, -1, -1};
+            if (bad || (x.n == 0 && x.from == x.to)) x = {0, 0, -1, -1, 0, 0};
             return x;
         };
         for (int it = 0;; ++it) {
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
                 if (whole) {
                     mbar_arrive_expect_tx(bar(sh.landed[d]), x.from >= 0 ? (uint32_t)(4 * K * V) : 0u);
                     if (x.from >= 0)
-                        bulk_g2s(smem_u32(buffers + (size_t)d * K * V), state_of(at, x.from), 4 * K * V, bar(sh.landed[d]));
+                        bulk_g2s(smem_u32(buffers + (size_t)d * K * V), state_of(x, x.from), 4 * K * V, bar(sh.landed[d]));
                 }
             }
         }
@@ -357,9 +358,9 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
         int it = 0;
         for (long long at = blockIdx.x; at < items && ok; at += gridDim.x, ++it) {
             const int d = it % DEPTH, turn = it / DEPTH;
-            const int split = (int)(at % splits), head = (int)(at / splits % H), col0 = split * cols;
             if (!wait(sh.known[d], turn)) break;
             const Item x = sh.item[d];
+            const int head = x.head, col0 = x.col0;
             const int blocks = (x.n + M - 1) / M;
             if (warp >= consumers && warp < consumers + NP) {   // producers
                 for (int i = 0; i < blocks; ++i, ++g) {
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
             } else if (warp > consumers + NP) { // storer
                 if (!wait(sh.done[d], turn)) break;
                 if (lane == 0) {
-                    if (x.to >= 0 && whole) bulk_s2g(state_of(at, x.to), smem_u32(buffers + (size_t)d * K * V), 4 * K * V);
+                    if (x.to >= 0 && whole) bulk_s2g(state_of(x, x.to), smem_u32(buffers + (size_t)d * K * V), 4 * K * V);
                     bulk_commit();
                     bulk_wait_read_all();
                     mbar_arrive(bar(sh.read[d]));
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
                         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
                         if (x.from >= 0) {
                             if (whole) y = *reinterpret_cast<const float4 *>(buffer + (32 * j + i) * pitch);
-                            else y = ld_stream(reinterpret_cast<const float4 *>(state_of(at, x.from) + part + (32 * j + i) * pitch));
+                            else y = ld_stream(reinterpret_cast<const float4 *>(state_of(x, x.from) + part + (32 * j + i) * pitch));
                         }
                         s[j][i][0] = y.x; s[j][i][1] = y.y; s[j][i][2] = y.z; s[j][i][3] = y.w;
                     }
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
                         for (int i = 0; i < 4; ++i) {
                             const float4 y = make_float4(s[j][i][0], s[j][i][1], s[j][i][2], s[j][i][3]);
                             if (whole) *reinterpret_cast<float4 *>(buffer + (32 * j + i) * pitch) = y;
-                            else st_stream(reinterpret_cast<float4 *>(state_of(at, x.to) + part + (32 * j + i) * pitch), y);
+                            else st_stream(reinterpret_cast<float4 *>(state_of(x, x.to) + part + (32 * j + i) * pitch), y);
                         }
                     fence_async_smem();   // the storer's bulk copy reads it
                 }
