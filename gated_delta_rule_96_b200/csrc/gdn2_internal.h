@@ -16,7 +16,7 @@ inline bool allow_smem(Kernel kern, size_t bytes) {
 
 // A launch that the device prepares while the stream's kernel before it still runs: its blocks are placed as that
 // one's leave, and wait there for its end.  One call behind another, us, without and with it: a fork 5.6 / 3.2, one
-// user's tree 8.8 / 6.8, a decode step of residual norms 5.4 / 4.9 (the host), B256 H16 of runs 102 / 99.
+// user's tree 8.8 / 6.8, a decode step of residual norms 5.4 / 4.9 (the host), B256 H16 of runs 102 / 99 (each as the kernel was then).
 // (griddepcontrol.launch_dependents at the top of every kernel, which lets the next one's blocks in as soon as all of
 // its own have started, is slower: 3.5, 7.0, 4.8, 100, and the full batch of trees 142 against 137.)
 template <typename... Params, typename... Args>

@@ -19,9 +19,9 @@ namespace tree {
 
 // The kernel on CUDA cores, any type and size.  One block per (column range, head, sequence); the first
 // cols / 16 warps own 16 columns of the state each, every warp takes part in the rest.  For a few nodes a chain of
-// latencies (8 nodes of one user, H16: 9 us with cold caches, 6.9 a call behind another; the columns over 128 SMs), for
-// many the 2 n d_k d_v FMA of a head and their shared-memory loads (32 users with 32 nodes: 72 us, against 34 on the
-// tensor cores).
+// latencies (8 nodes of one user, H16: 7.4 us with cold caches, 6.1 a call behind another; the columns over 128 SMs),
+// for many the 2 n d_k d_v FMA of a head and their shared-memory loads (32 users with 32 nodes: 70 us, against 35 on
+// the tensor cores).
 template <typename Tok, int K, int V>
 __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q, const Tok *__restrict__ k,
                                                    const Tok *__restrict__ v, const float *__restrict__ alpha,
@@ -225,16 +225,16 @@ int launch_t(const void *q, const void *k, const void *v, const float *alpha, co
                         num_slots, slots, cu, parents, (Tok *)o, H, splits, total, max_nodes, status);
 }
 
-// Which kernel: the tensor-core one's period for an item hardly depends on its nodes (6.0 us an SM for one, 10.6 for
-// 64), this one's grows with them and is two thirds of it for one; H16, cold caches, us, this / that:
-//   one user      8 nodes  8.8 / 11.5   16 nodes  10.1 / 12.3   32 nodes  16.3 / 13.7   64 nodes  30.2 / 18.7
-//   4 users       8 nodes 11.4 / 11.9   32 nodes  25.0 / 14.5
-//   8 users       4 nodes 10.5 / 12.4    8 nodes  12.5 / 12.6   32 nodes  26.6 / 16.0   64 nodes  45.7 / 22.3
-//   32 users      4 nodes 23.0 / 26.1    8 nodes  29.5 / 26.7   16 nodes  43.6 / 28.4   32 nodes  72.1 / 34.0
-//   128 users     4 nodes 70.8 / 83.3    8 nodes  92.9 / 85.2   16 nodes 139.6 / 87.9   64 nodes 575.5 / 146.4
+// Which kernel: the tensor-core one's period for an item hardly depends on its nodes (6.0 us an SM for one, 10.7 for
+// 64), this one's grows with them and is not two thirds of it for one; H16, cold caches, us, this / that:
+//   one user      8 nodes  7.4 / 11.2   16 nodes   9.4 / 11.5   32 nodes  15.5 / 13.6   64 nodes  28.8 / 18.6
+//   4 users       8 nodes 10.2 / 12.0   32 nodes  23.0 / 14.5
+//   8 users       4 nodes  9.5 / 12.3    8 nodes  11.6 / 12.7   32 nodes  25.3 / 15.6   64 nodes  43.1 / 22.4
+//   32 users      4 nodes 21.5 / 26.7    8 nodes  28.2 / 27.2   16 nodes  41.0 / 28.8   32 nodes  69.7 / 34.6
+//   128 users     4 nodes 64.6 / 84.0    8 nodes  86.6 / 86.3   16 nodes 127.0 / 89.5   64 nodes 526.5 / 152.2
 bool use_tc(int batch, int H, int max_nodes) {
     const long long items = (long long)batch * H;
-    return max_nodes > (items > 148 ? 6 : items > 32 ? 8 : 16);
+    return max_nodes > (items > 148 ? 7 : items > 32 ? 8 : 24);
 }
 
 }  // namespace tree
