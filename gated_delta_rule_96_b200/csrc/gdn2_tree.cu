@@ -17,6 +17,82 @@
 namespace gdn2 {
 namespace tree {
 
+// A lane's channels are 4 (sub + 8 j) + c, sub = lane & 7.
+
+// Sums of eight values over the eight lanes of a node: on return lane `sub` holds the total of x[sub].
+__device__ __forceinline__ float node_sums(const float (&x)[8], int lane) {
+    float a[4], b[2];
+    const bool up4 = lane & 4, up2 = lane & 2, up1 = lane & 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        a[i] = (up4 ? x[i + 4] : x[i]) + __shfl_xor_sync(0xffffffffu, up4 ? x[i] : x[i + 4], 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        b[i] = (up2 ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, up2 ? a[i] : a[i + 2], 2);
+    return (up1 ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up1 ? b[0] : b[1], 1);
+}
+
+// G_n, the product of the decays on a node's path, at the lane's channels.  sa: alpha of all nodes in shared
+// memory.
+template <int K>
+__device__ __forceinline__ void climb(const float *sa, const unsigned char *anc, bool go, int node, int above, int lane,
+                                      f32x2 (&G)[K / 32][2]) {
+    const int sub = lane & 7, base = pairs(go ? node : 0), most = __reduce_max_sync(0xffffffffu, go ? above : -1);
+#pragma unroll
+    for (int j = 0; j < K / 32; ++j) G[j][0] = G[j][1] = pack2(1.f, 1.f);
+#pragma unroll 1
+    for (int h = 0; h <= most; h += 4) {
+        if (!go || h > above) continue;
+        const uchar4 whom = *reinterpret_cast<const uchar4 *>(anc + base + h);
+        const int at[4] = {whom.x, whom.y, whom.z, whom.w};
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            if (h + s <= above)
+#pragma unroll
+                for (int j = 0; j < K / 32; ++j) {
+                    f32x2 aa[2];
+                    load2(sa + at[s] * K + 4 * (sub + 8 * j), aa);
+                    G[j][0] = mul2(G[j][0], aa[0]);
+                    G[j][1] = mul2(G[j][1], aa[1]);
+                }
+    }
+}
+
+// A and P of a node's path, to cA and cP, where all its G are in range:  A[n,i] = sum_c (e_n G_n) (k_i / G_i), two
+// operations a channel, no chain from one ancestor to the next, and seven shuffles for four pairs.  sk: k_i / G_i of
+// all nodes in shared memory; e, g: e_n G_n and q_n G_n.
+template <int K>
+__device__ __forceinline__ void couple(const float *sk, const unsigned char *anc, float *cA, float *cP, bool go, int node,
+                                       int above, int lane, const f32x2 (&e)[K / 32][2], const f32x2 (&g)[K / 32][2]) {
+    const int sub = lane & 7, base = pairs(go ? node : 0), most = __reduce_max_sync(0xffffffffu, go ? above : -1);
+#pragma unroll 1
+    for (int h = 0; h <= most; h += 4) {
+        float x[8];
+        const bool some = go && h <= above;
+        const uchar4 whom = some ? *reinterpret_cast<const uchar4 *>(anc + base + h) : make_uchar4(0, 0, 0, 0);
+        const int at[4] = {whom.x, whom.y, whom.z, whom.w};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            f32x2 a[2] = {0ull, 0ull}, p[2] = {0ull, 0ull};
+#pragma unroll
+            for (int j = 0; j < K / 32; ++j) {
+                f32x2 kk[2];
+                load2(sk + at[s] * K + 4 * (sub + 8 * j), kk);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    a[c] = fma2(e[j][c], kk[c], a[c]);
+                    p[c] = fma2(g[j][c], kk[c], p[c]);
+                }
+            }
+            const float2 ya = unpack2(add2(a[0], a[1])), yp = unpack2(add2(p[0], p[1]));
+            x[s] = ya.x + ya.y;
+            x[4 + s] = yp.x + yp.y;
+        }
+        const float sum = node_sums(x, lane);
+        if (some) (sub < 4 ? cA : cP)[base + h + (sub & 3)] = sum;   // the node's own A is not used
+    }
+}
+
 // The kernel on CUDA cores, any type and size.  One block per (column range, head, sequence); the first
 // cols / 16 warps own 16 columns of the state each, every warp takes part in the rest.  For a few nodes a chain of
 // latencies (8 nodes of one user, H16: 7.4 us with cold caches, 6.1 a call behind another; the columns over 128 SMs),
