@@ -54,7 +54,7 @@ struct TcShared {
     float a[MAX_PAIRS], c[2][MAX_PAIRS];      // A; P, then C
     Meta meta[METAS];
     unsigned long long path[MAX_NODES];       // a bit for each node on a node's path
-    unsigned long long meta_full[METAS], meta_free[METAS], s_full[2], s_free[2], coef_full[2], coef_free[2], b_full, b_free,
+    unsigned long long meta_known[METAS], meta_full[METAS], meta_free[METAS], s_full[2], s_free[2], coef_full[2], coef_free[2], b_full, b_free,
         d_full, d_free, p_full, p_free;
     uint32_t tmem, abort;
 };
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
     volatile uint32_t *abort = &sh.abort;
 
     if (tid == 0) {
-        for (int i = 0; i < METAS; ++i) mbar_init(bar(sh.meta_full[i]), 1), mbar_init(bar(sh.meta_free[i]), SCOUT);   // a warp each, but the scout
+        for (int i = 0; i < METAS; ++i) mbar_init(bar(sh.meta_known[i]), 1), mbar_init(bar(sh.meta_full[i]), 1), mbar_init(bar(sh.meta_free[i]), SCOUT);   // a warp each, but the scout
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(sh.s_full[i]), STATE_WARPS);
             mbar_init(bar(sh.s_free[i]), 1);
@@ -135,8 +135,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
 
     int c = 0;
     if (warp == SCOUT) {
-        const auto look = [&](long long at, Meta &m) {
-            const int seq = (int)(at / H), head = (int)(at % H), lo = cu[seq], hi = cu[seq + 1], slot = slots[seq];
+        // an item a turn: its sequence and head without a division
+        int seq = blockIdx.x / (unsigned)H, head = blockIdx.x % (unsigned)H;
+        const int seqs_on = gridDim.x / (unsigned)H, heads_on = gridDim.x % (unsigned)H;
+        for (int it = 0;; ++it) {
+            if (blockIdx.x + (long long)it * gridDim.x >= items || !warp_wait(sh.meta_free[it % METAS], it / METAS + 1)) break;
+            Meta &m = sh.meta[it % METAS];
+            const int lo = cu[seq], hi = cu[seq + 1], slot = slots[seq];
             unsigned bad = 0;
             if (lo < 0 || hi < lo || hi > total || hi - lo > max_nodes) bad = DEV_RANGE;
             else if (slot < -1 || slot >= num_slots) bad = DEV_SLOT;
@@ -152,7 +157,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                 n = 0;
             }
             if (lane == 0) m.lo = lo, m.n = n, m.slot = slot, m.head = head;
-            __syncwarp();
+            arrive(sh.meta_known[it % METAS]);   // all but the pair group go on with that
+            // a line a lane (bulk prefetches of whole rows took 60 cycles each, 24,000 for 64 nodes)
+            for (int i = lane; i < 2 * n; i += 32) {
+                const size_t row = ((size_t)(lo + i / 2) * H + head) * D + i % 2 * 64;
+                prefetch_l2(k + row);
+                prefetch_l2(b + row);
+                prefetch_l2(q + row);
+                prefetch_l2(v + row);
+                prefetch_l2(w + row);
+                prefetch_l2(alpha + row);
+                prefetch_l2(alpha + row + 32);
+            }
             int above[2] = {-1, -1};
 #pragma unroll
             for (int r = 0; r < 2; ++r)
@@ -165,28 +181,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                     if (above[r] == l) m.order[place + __popc(here & ((1u << lane) - 1))] = (unsigned char)(lane + 32 * r);
                     place += __popc(here);
                 }
-            // a line a lane (bulk prefetches of whole rows took 60 cycles each, 24,000 for 64 nodes)
-            for (int i = lane; i < 2 * n; i += 32) {
-                const size_t row = ((size_t)(lo + i / 2) * H + head) * D + i % 2 * 64;
-                prefetch_l2(k + row);
-                prefetch_l2(b + row);
-                prefetch_l2(q + row);
-                prefetch_l2(v + row);
-                prefetch_l2(w + row);
-                prefetch_l2(alpha + row);
-                prefetch_l2(alpha + row + 32);
-            }
-        };
-        for (int it = 0;; ++it) {
-            const long long at = blockIdx.x + (long long)it * gridDim.x;
-            if (at >= items || !warp_wait(sh.meta_free[it % METAS], it / METAS + 1)) break;
-            look(at, sh.meta[it % METAS]);
             arrive(sh.meta_full[it % METAS]);
+            seq += seqs_on;
+            head += heads_on;
+            if (head >= H) head -= H, ++seq;
         }
     } else if (warp == LEAD) {
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
-            if (!warp_wait(sh.meta_full[it % METAS], it / METAS)) break;
+            if (!warp_wait(sh.meta_known[it % METAS], it / METAS)) break;
             const int n = sh.meta[it % METAS].n;
             arrive(sh.meta_free[it % METAS]);
             if (n > 0) {
@@ -236,7 +239,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
-            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_COLUMN, 32 * COLUMN_WARPS)) break;
+            if (!group_wait(sh.meta_known[it % METAS], it / METAS, BAR_COLUMN, 32 * COLUMN_WARPS)) break;
             const Meta &m = sh.meta[it % METAS];
             const int n = m.n;
             if (n > 0) {
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
-            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_STATE, 32 * STATE_WARPS)) break;
+            if (!group_wait(sh.meta_known[it % METAS], it / METAS, BAR_STATE, 32 * STATE_WARPS)) break;
             const Meta &m = sh.meta[it % METAS];
             const int n = m.n, slot = m.slot, head = m.head;
             arrive(sh.meta_free[it % METAS]);
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
         const int t = tid - 32 * PATH0, sub = lane & 7;
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
-            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_PATH, THREADS)) break;   // and the last item's rows
+            if (!group_wait(sh.meta_known[it % METAS], it / METAS, BAR_PATH, THREADS)) break;   // and the last item's rows
             Meta &m = sh.meta[it % METAS];
             const int n = m.n, rows = (n + 7) / 8 * 8;
             if (n > 0) {
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
         const int t = tid - 32 * PAIR0;
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
-            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_PAIR, THREADS)) break;
+            if (!group_wait(sh.meta_full[it % METAS], it / METAS, BAR_PAIR, THREADS)) break;   // paths and order too
             const Meta &m = sh.meta[it % METAS];
             const int n = m.n, rows = (n + 7) / 8 * 8;
             if (n > 0) {
