@@ -59,7 +59,7 @@ __device__ __forceinline__ bool in_range(const f32x2 (&G)[K / 32][2], int lane) 
 // A and P of a node's path, to cA and cP, with the decays multiplied in one by one on the way up, from the tokens in
 // HBM: for decays whose product leaves the range (zero among them), exact for any.
 template <typename Tok, int K>
-__device__ __noinline__ void couple_far(const Tok *q, const Tok *k, const Tok *b, const float *alpha,
+__device__ __forceinline__ void couple_far(const Tok *q, const Tok *k, const Tok *b, const float *alpha,
                                         const unsigned char *anc, float *cA, float *cP, bool go, int lo, int H, int head,
                                         int node, int above, int lane) {
     const int sub = lane & 7, base = pairs(go ? node : 0), most = __reduce_max_sync(0xffffffffu, go ? above : -1);
