@@ -228,15 +228,15 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *__restric
 
 // ---------------------------------------------------------------- residual norm
 
-// A block a row forward: the row's loads are in flight at once, and 2,048 threads an SM hide them.  Backward a block
-// walks rows, since it carries the columns' sums: two blocks an SM; loading the next row ahead took 151 us where this
+// A row is one to sixteen warps', and a block has eight warps or one row.  Forward the row's loads are in flight at once,
+// and 2,048 threads an SM hide them.  Backward a block walks rows, since it carries the columns' sums: two blocks an SM; loading the next row ahead took 151 us where this
 // takes 143, two vectors a thread 145.
 
-// Sum over the block of up to two values at once; `s` is one of two buffers taken in turn, so that one
-// barrier a row is enough.
+// Sum over the `warps` warps of a row, `first` of them the first, of up to two values at once; `s` is one of two buffers
+// taken in turn, so that one barrier a row is enough.  The whole block calls it.
 template <int C>
-__device__ __forceinline__ void block_sum(float (&x)[C], float (*s)[C]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+__device__ __forceinline__ void row_sum(float (&x)[C], float (*s)[C], int first, int warps) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int c = 0; c < C; ++c) x[c] = lane_sum<32>(x[c]);
     if (warps == 1) return;
@@ -247,32 +247,36 @@ __device__ __forceinline__ void block_sum(float (&x)[C], float (*s)[C]) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         x[c] = 0.f;
-        for (int w = 0; w < warps; ++w) x[c] += s[w][c];
+        for (int w = 0; w < warps; ++w) x[c] += s[first + w][c];
     }
 }
 
 constexpr int MAX_WARPS = 16;   // of a block: rows of up to 512 threads
 constexpr int MAX_WIDTH = 8192;
 
-template <typename Tok, int NV>
+template <typename Tok, int NV, bool SHARE>
 __global__ void __launch_bounds__(512) add_norm_fwd_kernel(const Tok *x, const Tok *residual,
                                                            const float *__restrict__ scale,
                                                            const float *__restrict__ weight, Tok *h, Tok *y,
-                                                           long long rows, int vecs, float eps) {
+                                                           long long rows, int vecs, int row_warps, float eps) {
     behind_last_kernel();
+    // SHARE: a block has several rows; the thread's place in its own
+    const int team = SHARE ? (threadIdx.x >> 5) / row_warps : 0, teams = SHARE ? (blockDim.x >> 5) / row_warps : 1,
+              row_threads = SHARE ? 32 * row_warps : blockDim.x, at = threadIdx.x - team * row_threads;
     using V = V16<Tok>;
     constexpr int N = V::N;
     __shared__ float s_sum[2][MAX_WARPS][1];
     const float inv_width = 1.f / (float)(vecs * N);
     int flip = 0;
-    for (long long r = blockIdx.x; r < rows; r += gridDim.x, flip ^= 1) {
-        const size_t base = (size_t)r * vecs;
+    for (long long r0 = (long long)blockIdx.x * teams; r0 < rows; r0 += (long long)gridDim.x * teams, flip ^= 1) {
+        const size_t base = (size_t)(r0 + team) * vecs;
+        const int mine = !SHARE || r0 + team < rows ? vecs : 0;
         uint4 xr[NV], rr[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
+            const int v = at + j * row_threads;
             xr[j] = rr[j] = make_uint4(0, 0, 0, 0);
-            if (v < vecs) {
+            if (v < mine) {
                 xr[j] = __ldcs(reinterpret_cast<const uint4 *>(x) + base + v);
                 if (residual) rr[j] = __ldcs(reinterpret_cast<const uint4 *>(residual) + base + v);
             }
@@ -280,11 +284,11 @@ __global__ void __launch_bounds__(512) add_norm_fwd_kernel(const Tok *x, const T
         float a[NV][N], sum[1] = {0.f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
+            const int v = at + j * row_threads;
             float xf[N], sc[N];
             V::unpack(xr[j], xf);
             V::unpack(rr[j], a[j]);
-            if (scale && v < vecs) load_f32<N>(scale + (size_t)v * N, sc);
+            if (scale && v < mine) load_f32<N>(scale + (size_t)v * N, sc);
             else
 #pragma unroll
                 for (int i = 0; i < N; ++i) sc[i] = 1.f;
@@ -293,14 +297,14 @@ __global__ void __launch_bounds__(512) add_norm_fwd_kernel(const Tok *x, const T
                 a[j][i] = fmaf(sc[i], xf[i], a[j][i]);
                 sum[0] = fmaf(a[j][i], a[j][i], sum[0]);
             }
-            if (h && v < vecs) __stcs(reinterpret_cast<uint4 *>(h) + base + v, V::pack(a[j]));
+            if (h && v < mine) __stcs(reinterpret_cast<uint4 *>(h) + base + v, V::pack(a[j]));
         }
-        block_sum<1>(sum, s_sum[flip]);
+        row_sum<1>(sum, s_sum[flip], team * row_warps, SHARE ? row_warps : blockDim.x >> 5);
         const float inv = rsqrtf(sum[0] * inv_width + eps);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
-            if (v < vecs) {
+            const int v = at + j * row_threads;
+            if (v < mine) {
                 float wt[N];
                 load_f32<N>(weight + (size_t)v * N, wt);
 #pragma unroll
@@ -311,15 +315,18 @@ __global__ void __launch_bounds__(512) add_norm_fwd_kernel(const Tok *x, const T
     }
 }
 
-template <typename Tok, int NV, bool SCALED>
+template <typename Tok, int NV, bool SCALED, bool SHARE>
 __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) add_norm_bwd_kernel(const Tok *__restrict__ h, const Tok *__restrict__ x,
                                                            const float *__restrict__ scale,
                                                            const float *__restrict__ weight,
                                                            const Tok *__restrict__ dy, const Tok *__restrict__ dh,
                                                            Tok *__restrict__ dres, Tok *__restrict__ dx,
                                                            float *__restrict__ partial, long long rows, int vecs,
-                                                           float eps) {
+                                                           int row_warps, float eps) {
     behind_last_kernel();
+    // SHARE: a block has several rows; the thread's place in its own
+    const int team = SHARE ? (threadIdx.x >> 5) / row_warps : 0, teams = SHARE ? (blockDim.x >> 5) / row_warps : 1,
+              row_threads = SHARE ? 32 * row_warps : blockDim.x, at = threadIdx.x - team * row_threads;
     using V = V16<Tok>;
     constexpr int N = V::N;
     __shared__ float s_sum[2][MAX_WARPS][2];
@@ -337,14 +344,15 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) add_norm_bwd_kernel(cons
         for (int i = 0; i < N; ++i) dw[j][i] = ds[j][i] = 0.f;
     __syncthreads();
     int flip = 0;
-    for (long long r = blockIdx.x; r < rows; r += gridDim.x, flip ^= 1) {
-        const size_t base = (size_t)r * vecs;
+    for (long long r0 = (long long)blockIdx.x * teams; r0 < rows; r0 += (long long)gridDim.x * teams, flip ^= 1) {
+        const size_t base = (size_t)(r0 + team) * vecs;
+        const bool live = !SHARE || r0 + team < rows;
         uint4 hr[NV], xr[NV], yr[NV], gr[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
+            const int v = at + j * row_threads;
             hr[j] = xr[j] = yr[j] = gr[j] = make_uint4(0, 0, 0, 0);
-            if (v < vecs) {
+            if (live && v < vecs) {
                 hr[j] = __ldcs(reinterpret_cast<const uint4 *>(h) + base + v);
                 yr[j] = __ldcs(reinterpret_cast<const uint4 *>(dy) + base + v);
                 if (SCALED) xr[j] = __ldcs(reinterpret_cast<const uint4 *>(x) + base + v);
@@ -354,7 +362,7 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) add_norm_bwd_kernel(cons
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
+            const int v = at + j * row_threads;
             float hf[N], df[N], wt[N];
             V::unpack(hr[j], hf);
             V::unpack(yr[j], df);
@@ -365,12 +373,12 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) add_norm_bwd_kernel(cons
                 sum[1] = fmaf(df[i] * wt[i], hf[i], sum[1]);
             }
         }
-        block_sum<2>(sum, s_sum[flip]);
-        const float inv = rsqrtf(sum[0] * inv_width + eps);
+        row_sum<2>(sum, s_sum[flip], team * row_warps, SHARE ? row_warps : blockDim.x >> 5);
+        const float inv = live ? rsqrtf(sum[0] * inv_width + eps) : 0.f;   // eps may be 0
         const float mean = sum[1] * inv * inv * inv_width;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
+            const int v = at + j * row_threads;
             float hf[N], df[N], gf[N], wt[N];
             V::unpack(hr[j], hf);
             V::unpack(yr[j], df);
@@ -381,7 +389,7 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) add_norm_bwd_kernel(cons
                 dw[j][i] = fmaf(df[i], hf[i] * inv, dw[j][i]);
                 gf[i] += inv * (df[i] * wt[i] - hf[i] * mean);
             }
-            if (v < vecs) __stcs(reinterpret_cast<uint4 *>(dres) + base + v, V::pack(gf));
+            if (live && v < vecs) __stcs(reinterpret_cast<uint4 *>(dres) + base + v, V::pack(gf));
             if (SCALED) {
                 float xf[N], sc[N];
                 V::unpack(xr[j], xf);
@@ -391,14 +399,31 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) add_norm_bwd_kernel(cons
                     ds[j][i] = fmaf(gf[i], xf[i], ds[j][i]);
                     gf[i] *= sc[i];
                 }
-                if (v < vecs) __stcs(reinterpret_cast<uint4 *>(dx) + base + v, V::pack(gf));
+                if (live && v < vecs) __stcs(reinterpret_cast<uint4 *>(dx) + base + v, V::pack(gf));
             }
         }
     }
+    // the block's rows added up, one after the other, in place of the weights
+    for (int t = 0; SHARE && t < teams; ++t) {
+        __syncthreads();
+        if (team != t) continue;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int v = at + j * row_threads;
+            if (v >= vecs) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float *w = s_weights + v * N + i;
+                *w = dw[j][i] += t ? *w : 0.f;
+                if (SCALED) w[width] = ds[j][i] += t ? w[width] : 0.f;
+            }
+        }
+    }
+    if (team != teams - 1) return;
     float *mine = partial + (size_t)blockIdx.x * width * (SCALED ? 2 : 1);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int v = threadIdx.x + j * blockDim.x;
+        const int v = at + j * row_threads;
         if (v < vecs)
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
@@ -425,8 +450,11 @@ int resident(Kernel kern, int threads, size_t smem) {
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) == cudaSuccess ? n : 1;
 }
 
-// threads of a block that holds a row of `vecs` 16-byte vectors, NV a thread
-int row_threads(int vecs, int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; }
+// warps that hold a row of `vecs` 16-byte vectors, NV a thread, and the rows of a block: narrow rows share one, since
+// blocks of a warp leave most of an SM empty (forward and backward, us, a row and several rows a block: 149,421 rows of
+// 208 bf16 306 / 98, 60,000 of 512 bf16 182 / 114, 32,768 of 1,024 bf16 138 / 122)
+int row_warps(int vecs, int nv) { return ((vecs + nv - 1) / nv + 31) / 32; }
+int block_rows(int warps) { return warps < 8 ? 8 / warps : 1; }
 
 template <typename Tok, int D, int ACT>
 int gated_fwd_t(const void *o, const void *gate, const float *weight, void *y, long long rows, float eps,
@@ -454,35 +482,38 @@ int gated_bwd_t(const void *o, const void *gate, const float *weight, const void
 template <typename Tok>
 int add_fwd_t(const void *x, const void *residual, const float *scale, const float *weight, void *h, void *y,
               long long rows, int width, float eps, cudaStream_t st) {
-    const int vecs = width / V16<Tok>::N, nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4, nt = row_threads(vecs, nv);
-    const unsigned blocks = (unsigned)(rows < (1 << 30) ? rows : (1 << 30));
+    const int vecs = width / V16<Tok>::N, nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4, warps = row_warps(vecs, nv), teams = block_rows(warps), nt = 32 * warps * teams;
+    const long long want = (rows + teams - 1) / teams;
+    const unsigned blocks = (unsigned)(want < (1 << 30) ? want : (1 << 30));
     auto go = [&](auto kern) {
         return launch_close(kern, blocks, nt, 0, st, (const Tok *)x, (const Tok *)residual, scale, weight, (Tok *)h, (Tok *)y, rows,
-                            vecs, eps);
+                            vecs, warps, eps);
     };
-    if (nv == 1) return go(add_norm_fwd_kernel<Tok, 1>);
-    if (nv == 2) return go(add_norm_fwd_kernel<Tok, 2>);
-    if constexpr (sizeof(Tok) == 4) return go(add_norm_fwd_kernel<Tok, 4>);
+    if (teams > 1) return go(add_norm_fwd_kernel<Tok, 1, true>);
+    if (nv == 1) return go(add_norm_fwd_kernel<Tok, 1, false>);
+    if (nv == 2) return go(add_norm_fwd_kernel<Tok, 2, false>);
+    if constexpr (sizeof(Tok) == 4) return go(add_norm_fwd_kernel<Tok, 4, false>);
     return -6;   // bf16 rows end at 1024 vectors
 }
 template <typename Tok, bool SCALED>
 int add_bwd_t(const void *h, const void *x, const float *scale, const float *weight, const void *dy, const void *dh,
               void *dres, void *dx, float *dscale, float *dweight, long long rows, int width, float eps,
               float *partial, cudaStream_t st) {
-    const int vecs = width / V16<Tok>::N, nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4, nt = row_threads(vecs, nv);
+    const int vecs = width / V16<Tok>::N, nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4, warps = row_warps(vecs, nv), teams = block_rows(warps), nt = 32 * warps * teams;
     const int columns = width * (SCALED ? 2 : 1);
     int blocks = 0;
     int rc = -6;
     auto go = [&](auto kern) {
         const size_t smem = sizeof(float) * (size_t)columns;
         if (!allow_smem(kern, sizeof(float) * 2 * MAX_WIDTH)) return;
-        blocks = cap_blocks(rows, resident(kern, nt, smem));
+        blocks = cap_blocks((rows + teams - 1) / teams, resident(kern, nt, smem));
         rc = launch_close(kern, blocks, nt, smem, st, (const Tok *)h, (const Tok *)x, scale, weight, (const Tok *)dy, (const Tok *)dh,
-                          (Tok *)dres, (Tok *)dx, partial, rows, vecs, eps);
+                          (Tok *)dres, (Tok *)dx, partial, rows, vecs, warps, eps);
     };
-    if (nv == 1) go(add_norm_bwd_kernel<Tok, 1, SCALED>);
-    else if (nv == 2) go(add_norm_bwd_kernel<Tok, 2, SCALED>);
-    else if constexpr (sizeof(Tok) == 4) go(add_norm_bwd_kernel<Tok, 4, SCALED>);   // bf16 rows end at 1024 vectors
+    if (teams > 1) go(add_norm_bwd_kernel<Tok, 1, SCALED, true>);
+    else if (nv == 1) go(add_norm_bwd_kernel<Tok, 1, SCALED, false>);
+    else if (nv == 2) go(add_norm_bwd_kernel<Tok, 2, SCALED, false>);
+    else if constexpr (sizeof(Tok) == 4) go(add_norm_bwd_kernel<Tok, 4, SCALED, false>);   // bf16 rows end at 1024 vectors
     return rc ? rc : launch_close(column_sum_kernel, (columns + 31) / 32, 1024, 0, st, partial, blocks, columns, dweight, dscale, width);
 }
 

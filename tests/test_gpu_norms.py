@@ -142,6 +142,18 @@ def test_add_norm_optional_inputs(dtype, scale, residual, dh):
     check_add(g, torch, t, dtype, scale, residual, dh)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,width", [(9, 8), (5001, 208), (13, 264), (1201, 392), (7, 520), (3, 776), (2001, 1032), (3, 1304)])
+def test_add_norm_rows_that_share_a_block(dtype, rows, width):
+    """One to seven warps a row, the last block partly empty; an empty place takes no part, whatever eps is."""
+    torch, g = cuda_or_skip()
+    t = _make(torch, 3, rows, width, dtype, ("x", "residual", "dy", "dh"), ("scale", "weight"))
+    check_add(g, torch, t, dtype)
+    y, h = g.add_norm_fwd(t["x"], t["residual"], t["scale"], t["weight"])
+    small, none = (g.add_norm_bwd(h, t["x"], t["scale"], t["weight"], t["dy"], t["dh"], eps=eps) for eps in (1e-20, 0.0))
+    assert all(torch.equal(a, b) and torch.isfinite(a.float()).all() for a, b in zip(small, none))
+
+
 def test_add_norm_in_place_and_empty():
     torch, g = cuda_or_skip()
     t = _make(torch, 12, 40, 512, "bf16", ("x", "residual"), ("scale", "weight"))
