@@ -228,18 +228,19 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float *__restric
 
 // ---------------------------------------------------------------- residual norm
 
-// A row is one to sixteen warps', and a block has eight warps or one row.  Forward the row's loads are in flight at once,
+// A row is eight lanes' to sixteen warps', and a block has eight warps or one row.  Forward the row's loads are in flight at once,
 // and 2,048 threads an SM hide them.  Backward a block walks rows, since it carries the columns' sums: two blocks an SM; loading the next row ahead took 151 us where this
 // takes 143, two vectors a thread 145.
 
 // Sum over the `warps` warps of a row, `first` of them the first, of up to two values at once; `s` is one of two buffers
-// taken in turn, so that one barrier a row is enough.  The whole block calls it.
-template <int C>
+// taken in turn, so that one barrier a row is enough.  The whole block calls it.  LANES below 32: a row is as many
+// lanes of a warp.
+template <int C, int LANES>
 __device__ __forceinline__ void row_sum(float (&x)[C], float (*s)[C], int first, int warps) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int c = 0; c < C; ++c) x[c] = lane_sum<32>(x[c]);
-    if (warps == 1) return;
+    for (int c = 0; c < C; ++c) x[c] = lane_sum<LANES>(x[c]);
+    if (LANES < 32 || warps == 1) return;
     if (lane == 0)
 #pragma unroll
         for (int c = 0; c < C; ++c) s[warp][c] = x[c];
@@ -254,15 +255,17 @@ __device__ __forceinline__ void row_sum(float (&x)[C], float (*s)[C], int first,
 constexpr int MAX_WARPS = 16;   // of a block: rows of up to 512 threads
 constexpr int MAX_WIDTH = 8192;
 
-template <typename Tok, int NV, bool SHARE>
+template <typename Tok, int NV, int SHARE>
 __global__ void __launch_bounds__(512) add_norm_fwd_kernel(const Tok *x, const Tok *residual,
                                                            const float *__restrict__ scale,
                                                            const float *__restrict__ weight, Tok *h, Tok *y,
                                                            long long rows, int vecs, int row_warps, float eps) {
     behind_last_kernel();
-    // SHARE: a block has several rows; the thread's place in its own
-    const int team = SHARE ? (threadIdx.x >> 5) / row_warps : 0, teams = SHARE ? (blockDim.x >> 5) / row_warps : 1,
-              row_threads = SHARE ? 32 * row_warps : blockDim.x, at = threadIdx.x - team * row_threads;
+    // the block's rows, and the thread's place in its own
+    const int row_threads = SHARE == 0 ? blockDim.x : SHARE == 32 ? 32 * row_warps : SHARE,
+              team = SHARE == 0 ? 0 : SHARE == 32 ? (threadIdx.x >> 5) / row_warps : threadIdx.x / SHARE,
+              teams = SHARE == 0 ? 1 : SHARE == 32 ? (blockDim.x >> 5) / row_warps : blockDim.x / SHARE,
+              at = threadIdx.x - team * row_threads;
     using V = V16<Tok>;
     constexpr int N = V::N;
     __shared__ float s_sum[2][MAX_WARPS][1];
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(512) add_norm_fwd_kernel(const Tok *x, const T
             }
             if (h && v < mine) __stcs(reinterpret_cast<uint4 *>(h) + base + v, V::pack(a[j]));
         }
-        row_sum<1>(sum, s_sum[flip], team * row_warps, SHARE ? row_warps : blockDim.x >> 5);
+        row_sum<1, SHARE == 0 ? 32 : SHARE>(sum, s_sum[flip], team * row_warps, SHARE ? row_warps : blockDim.x >> 5);
         const float inv = rsqrtf(sum[0] * inv_width + eps);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(512) add_norm_fwd_kernel(const Tok *x, const T
     }
 }
 
-template <typename Tok, int NV, bool SCALED, bool SHARE>
+template <typename Tok, int NV, bool SCALED, int SHARE>
 __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) add_norm_bwd_kernel(const Tok *__restrict__ h, const Tok *__restrict__ x,
                                                            const float *__restrict__ scale,
                                                            const float *__restrict__ weight,
@@ -324,9 +327,11 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) add_norm_bwd_kernel(cons
                                                            float *__restrict__ partial, long long rows, int vecs,
                                                            int row_warps, float eps) {
     behind_last_kernel();
-    // SHARE: a block has several rows; the thread's place in its own
-    const int team = SHARE ? (threadIdx.x >> 5) / row_warps : 0, teams = SHARE ? (blockDim.x >> 5) / row_warps : 1,
-              row_threads = SHARE ? 32 * row_warps : blockDim.x, at = threadIdx.x - team * row_threads;
+    // the block's rows, and the thread's place in its own
+    const int row_threads = SHARE == 0 ? blockDim.x : SHARE == 32 ? 32 * row_warps : SHARE,
+              team = SHARE == 0 ? 0 : SHARE == 32 ? (threadIdx.x >> 5) / row_warps : threadIdx.x / SHARE,
+              teams = SHARE == 0 ? 1 : SHARE == 32 ? (blockDim.x >> 5) / row_warps : blockDim.x / SHARE,
+              at = threadIdx.x - team * row_threads;
     using V = V16<Tok>;
     constexpr int N = V::N;
     __shared__ float s_sum[2][MAX_WARPS][2];
@@ -373,7 +378,7 @@ __global__ void __launch_bounds__(512, NV == 1 ? 2 : 1) add_norm_bwd_kernel(cons
                 sum[1] = fmaf(df[i] * wt[i], hf[i], sum[1]);
             }
         }
-        row_sum<2>(sum, s_sum[flip], team * row_warps, SHARE ? row_warps : blockDim.x >> 5);
+        row_sum<2, SHARE == 0 ? 32 : SHARE>(sum, s_sum[flip], team * row_warps, SHARE ? row_warps : blockDim.x >> 5);
         const float inv = live ? rsqrtf(sum[0] * inv_width + eps) : 0.f;   // eps may be 0
         const float mean = sum[1] * inv * inv * inv_width;
 #pragma unroll
@@ -452,9 +457,10 @@ int resident(Kernel kern, int threads, size_t smem) {
 
 // warps that hold a row of `vecs` 16-byte vectors, NV a thread, and the rows of a block: narrow rows share one, since
 // blocks of a warp leave most of an SM empty (forward and backward, us, a row and several rows a block: 149,421 rows of
-// 208 bf16 306 / 98, 60,000 of 512 bf16 182 / 114, 32,768 of 1,024 bf16 138 / 122)
+// 208 bf16 306 / 98, 60,000 of 512 bf16 182 / 114, 32,768 of 1,024 bf16 138 / 122), and up to 16 vectors a warp, since
+// lanes without a vector do too (a row and several rows a warp: 400,000 of 64 bf16 234 / 94, 250,000 of 128 155 / 108)
 int row_warps(int vecs, int nv) { return ((vecs + nv - 1) / nv + 31) / 32; }
-int block_rows(int warps) { return warps < 8 ? 8 / warps : 1; }
+int block_rows(int vecs, int warps) { return vecs <= 8 ? 32 : vecs <= 16 ? 16 : warps < 8 ? 8 / warps : 1; }
 
 template <typename Tok, int D, int ACT>
 int gated_fwd_t(const void *o, const void *gate, const float *weight, void *y, long long rows, float eps,
@@ -482,24 +488,26 @@ int gated_bwd_t(const void *o, const void *gate, const float *weight, const void
 template <typename Tok>
 int add_fwd_t(const void *x, const void *residual, const float *scale, const float *weight, void *h, void *y,
               long long rows, int width, float eps, cudaStream_t st) {
-    const int vecs = width / V16<Tok>::N, nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4, warps = row_warps(vecs, nv), teams = block_rows(warps), nt = 32 * warps * teams;
+    const int vecs = width / V16<Tok>::N, nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4, warps = row_warps(vecs, nv), teams = block_rows(vecs, warps), nt = teams > 8 ? 256 : 32 * warps * teams;
     const long long want = (rows + teams - 1) / teams;
     const unsigned blocks = (unsigned)(want < (1 << 30) ? want : (1 << 30));
     auto go = [&](auto kern) {
         return launch_close(kern, blocks, nt, 0, st, (const Tok *)x, (const Tok *)residual, scale, weight, (Tok *)h, (Tok *)y, rows,
                             vecs, warps, eps);
     };
-    if (teams > 1) return go(add_norm_fwd_kernel<Tok, 1, true>);
-    if (nv == 1) return go(add_norm_fwd_kernel<Tok, 1, false>);
-    if (nv == 2) return go(add_norm_fwd_kernel<Tok, 2, false>);
-    if constexpr (sizeof(Tok) == 4) return go(add_norm_fwd_kernel<Tok, 4, false>);
+    if (teams == 32) return go(add_norm_fwd_kernel<Tok, 1, 8>);
+    if (teams == 16) return go(add_norm_fwd_kernel<Tok, 1, 16>);
+    if (teams > 1) return go(add_norm_fwd_kernel<Tok, 1, 32>);
+    if (nv == 1) return go(add_norm_fwd_kernel<Tok, 1, 0>);
+    if (nv == 2) return go(add_norm_fwd_kernel<Tok, 2, 0>);
+    if constexpr (sizeof(Tok) == 4) return go(add_norm_fwd_kernel<Tok, 4, 0>);
     return -6;   // bf16 rows end at 1024 vectors
 }
 template <typename Tok, bool SCALED>
 int add_bwd_t(const void *h, const void *x, const float *scale, const float *weight, const void *dy, const void *dh,
               void *dres, void *dx, float *dscale, float *dweight, long long rows, int width, float eps,
               float *partial, cudaStream_t st) {
-    const int vecs = width / V16<Tok>::N, nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4, warps = row_warps(vecs, nv), teams = block_rows(warps), nt = 32 * warps * teams;
+    const int vecs = width / V16<Tok>::N, nv = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4, warps = row_warps(vecs, nv), teams = block_rows(vecs, warps), nt = teams > 8 ? 256 : 32 * warps * teams;
     const int columns = width * (SCALED ? 2 : 1);
     int blocks = 0;
     int rc = -6;
@@ -510,10 +518,12 @@ int add_bwd_t(const void *h, const void *x, const float *scale, const float *wei
         rc = launch_close(kern, blocks, nt, smem, st, (const Tok *)h, (const Tok *)x, scale, weight, (const Tok *)dy, (const Tok *)dh,
                           (Tok *)dres, (Tok *)dx, partial, rows, vecs, warps, eps);
     };
-    if (teams > 1) go(add_norm_bwd_kernel<Tok, 1, SCALED, true>);
-    else if (nv == 1) go(add_norm_bwd_kernel<Tok, 1, SCALED, false>);
-    else if (nv == 2) go(add_norm_bwd_kernel<Tok, 2, SCALED, false>);
-    else if constexpr (sizeof(Tok) == 4) go(add_norm_bwd_kernel<Tok, 4, SCALED, false>);   // bf16 rows end at 1024 vectors
+    if (teams == 32) go(add_norm_bwd_kernel<Tok, 1, SCALED, 8>);
+    else if (teams == 16) go(add_norm_bwd_kernel<Tok, 1, SCALED, 16>);
+    else if (teams > 1) go(add_norm_bwd_kernel<Tok, 1, SCALED, 32>);
+    else if (nv == 1) go(add_norm_bwd_kernel<Tok, 1, SCALED, 0>);
+    else if (nv == 2) go(add_norm_bwd_kernel<Tok, 2, SCALED, 0>);
+    else if constexpr (sizeof(Tok) == 4) go(add_norm_bwd_kernel<Tok, 4, SCALED, 0>);   // bf16 rows end at 1024 vectors
     return rc ? rc : launch_close(column_sum_kernel, (columns + 31) / 32, 1024, 0, st, partial, blocks, columns, dweight, dscale, width);
 }
 

@@ -143,9 +143,9 @@ def test_add_norm_optional_inputs(dtype, scale, residual, dh):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,width", [(9, 8), (5001, 208), (13, 264), (1201, 392), (7, 520), (3, 776), (2001, 1032), (3, 1304)])
+@pytest.mark.parametrize("rows,width", [(9, 8), (33, 32), (4001, 64), (5, 72), (3001, 128), (5001, 208), (13, 264), (1201, 392), (7, 520), (3, 776), (2001, 1032), (3, 1304)])
 def test_add_norm_rows_that_share_a_block(dtype, rows, width):
-    """One to seven warps a row, the last block partly empty; an empty place takes no part, whatever eps is."""
+    """Eight lanes to six warps a row, the last block partly empty; an empty place takes no part, whatever eps is."""
     torch, g = cuda_or_skip()
     t = _make(torch, 3, rows, width, dtype, ("x", "residual", "dy", "dh"), ("scale", "weight"))
     check_add(g, torch, t, dtype)
