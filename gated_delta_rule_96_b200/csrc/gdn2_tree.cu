@@ -295,8 +295,16 @@ int launch_t(const void *q, const void *k, const void *v, const float *alpha, co
     int splits = 1;
     while (splits < V / 16 && (long long)batch * H * splits * 2 <= 148) splits *= 2;
     const int cols = V / splits;
+    // Two threads a column at least; eight warps for the nodes where there is no third block an SM that they would keep
+    // out, for want of blocks or of shared memory (us, 128 threads / 256; H x nodes, d_k-d_v: 1 user 16 x 24, 128-128
+    // bf16 10.7 / 8.2; 2 users 8 x 64, 128-128 fp32 26.9 / 17.9; 128 users 16 x 32, 128-64 bf16 166 / 135; where there is
+    // one, 128 users 16 x 12, 64-64 bf16 35.8 / 46.2).
+    const long long blocks = (long long)H * splits * batch;
+    const int threads = max_nodes > 8 && (blocks <= 2 * 148 || 3 * smem(max_nodes, cols) > 227 * 1024) ? 256
+                        : 2 * cols < 128                                                             ? 128
+                                                                                                     : 2 * cols;
     if (!allow_smem(tree_kernel<Tok, K, V>, smem(MAX_NODES, V))) return -6;
-    return launch_close(tree_kernel<Tok, K, V>, dim3(H * splits, batch), 2 * cols < 128 ? 128 : 2 * cols, smem(max_nodes, cols),
+    return launch_close(tree_kernel<Tok, K, V>, dim3(H * splits, batch), threads, smem(max_nodes, cols),
                         st, (const Tok *)q, (const Tok *)k, (const Tok *)v, alpha, (const Tok *)b, (const Tok *)w, S, slot_stride,
                         num_slots, slots, cu, parents, (Tok *)o, H, splits, total, max_nodes, status);
 }
