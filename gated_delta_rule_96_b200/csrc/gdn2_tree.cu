@@ -310,15 +310,17 @@ int launch_t(const void *q, const void *k, const void *v, const float *alpha, co
 }
 
 // Which kernel: the tensor-core one's period for an item hardly depends on its nodes (6.0 us an SM for one, 10.7 for
-// 64), this one's grows with them and is not two thirds of it for one; H16, cold caches, us, this / that:
-//   one user      8 nodes  7.4 / 11.2   16 nodes   9.4 / 11.5   32 nodes  15.5 / 13.6   64 nodes  28.8 / 18.6
-//   4 users       8 nodes 10.2 / 12.0   32 nodes  23.0 / 14.5
-//   8 users       4 nodes  9.5 / 12.3    8 nodes  11.6 / 12.7   32 nodes  25.3 / 15.6   64 nodes  43.1 / 22.4
-//   32 users      4 nodes 21.5 / 26.7    8 nodes  28.2 / 27.2   16 nodes  41.0 / 28.8   32 nodes  69.7 / 34.6
-//   128 users     4 nodes 64.6 / 84.0    8 nodes  86.6 / 86.3   16 nodes 127.0 / 89.5   64 nodes 526.5 / 152.2
+// 64), this one's grows with them, is not two thirds of it for one, and few items have their columns over all SMs here;
+// H16, cold caches, us, this / that:
+//   1 user      8 nodes  7.4 / 10.7   24 nodes 11.0 / 11.7   40 nodes  14.2 / 14.4   64 nodes  19.6 / 16.4
+//   2 users    24 nodes 12.2 / 11.7   40 nodes 17.2 / 14.7
+//   4 users     9 nodes 10.0 / 11.0   16 nodes 11.5 / 11.4   32 nodes  17.5 / 13.1
+//   8 users     8 nodes 11.6 / 12.7   12 nodes 13.5 / 12.0   16 nodes  16.5 / 12.5
+//   32 users    4 nodes 21.5 / 26.7    8 nodes 27.5 / 25.7   16 nodes  41.0 / 28.8   32 nodes  69.7 / 34.6
+//   128 users   4 nodes 64.6 / 84.0    8 nodes 86.6 / 86.3   16 nodes 127.0 / 89.5   64 nodes 526.5 / 152.2
 bool use_tc(int batch, int H, int max_nodes) {
     const long long items = (long long)batch * H;
-    return max_nodes > (items > 148 ? 7 : items > 32 ? 8 : 24);
+    return max_nodes > (items > 148 ? 7 : items > 64 ? 9 : items > 32 ? 15 : items > 16 ? 20 : 40);
 }
 
 }  // namespace tree
