@@ -485,7 +485,7 @@ def gdn2_add_norm_bwd(h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweigh
     """Gradients of gdn2_add_norm_fwd at the stored h (include/gdn2.h).  dh may be None (zero); without a
     scale, x, dx and dscale are not used (dx equals dresidual)."""
     _native().add_norm_bwd(h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweight, eps,
-                           _add_workspace(h, stream) if workspace is None else workspace, stream)
+                           _add_workspace(h, stream) if workspace is None else workspace, stream, False)
 
 
 def gdn2_tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, o, max_nodes, workspace=None,
@@ -585,13 +585,9 @@ def add_norm_fwd(x, residual, scale, weight, eps=1e-6, stream=None):
 def add_norm_bwd(h, x, scale, weight, dy, dh=None, eps=1e-6, workspace=None, stream=None):
     """Allocating convenience wrapper: returns (dresidual, dx, dscale, dweight); without a scale dx is
     dresidual and dscale None."""
-    import torch
-    with torch.cuda.stream(stream):
-        dresidual, dweight = torch.empty_like(h), torch.empty_like(weight)
-        dx, dscale = (None, None) if scale is None else (torch.empty_like(h), torch.empty_like(scale))
-    gdn2_add_norm_bwd(h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweight, eps=eps, workspace=workspace,
-                      stream=stream)
-    return dresidual, dresidual if dx is None else dx, dscale, dweight
+    out = _native().add_norm_bwd(h, x, scale, weight, dy, dh, None, None, None, None, eps,
+                                 _add_workspace(h, stream) if workspace is None else workspace, stream, True)
+    return out if scale is not None else (out[0], out[0], None, out[1])
 
 
 def tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, max_nodes, workspace=None, stream=None):

@@ -333,9 +333,10 @@ PyObject *add_norm_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     });
 }
 
-// h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweight, eps, workspace, stream
+// h, x, scale, weight, dy, dh, dresidual, dx, dscale, dweight, eps, workspace, stream, allocate (the outputs: without a
+// scale dresidual and dweight alone)
 PyObject *add_norm_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    return guarded(args, n, 13, [](PyObject *const *a, std::vector<PyObject *> &made) {
+    return guarded(args, n, 14, [](PyObject *const *a, std::vector<PyObject *> &made) {
         Call c;
         int dt;
         const void *h = c.tokens("h", a[0], 0, &dt);
@@ -346,8 +347,14 @@ PyObject *add_norm_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const void *scale = c.use("scale", a[2], at::kFloat, last, true);
         const void *weight = c.use("weight", a[3], at::kFloat, last);
         const void *dy = c.use("dy", a[4], type, shape), *dh = c.use("dh", a[5], type, shape, true);
-        void *dres = c.use("dresidual", a[6], type, shape), *dx = c.use("dx", a[7], type, shape, true);
-        void *dscale = c.use("dscale", a[8], at::kFloat, last, true), *dweight = c.use("dweight", a[9], at::kFloat, last);
+        const bool allocate = PyObject_IsTrue(a[13]) == 1, scaled = a[2] != Py_None;
+        const at::Tensor &sums = THPVariable_Unpack(a[3]);   // what the column sums are like
+        const auto out = [&](int i, const at::Tensor &like, bool wanted) {
+            return allocate && wanted ? or_new(Py_None, like, a[12], made) : a[i];
+        };
+        void *dres = c.use("dresidual", out(6, t, true), type, shape), *dx = c.use("dx", out(7, t, scaled), type, shape, true);
+        void *dscale = c.use("dscale", out(8, sums, scaled), at::kFloat, last, true);
+        void *dweight = c.use("dweight", out(9, sums, true), at::kFloat, last);
         const float eps = (float)number(a[10]);
         const int width = to_int("width", t.size(-1));
         size_t bytes;

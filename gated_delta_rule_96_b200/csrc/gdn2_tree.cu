@@ -95,7 +95,7 @@ __device__ __forceinline__ void couple(const float *sk, const unsigned char *anc
 
 // The kernel on CUDA cores, any type and size.  One block per (column range, head, sequence); the first
 // cols / 16 warps own 16 columns of the state each, every warp takes part in the rest.  For a few nodes a chain of
-// latencies (8 nodes of one user, H16: 7.4 us with cold caches, 6.1 a call behind another; the columns over 128 SMs),
+// latencies (8 nodes of one user, H16: 7.4 us with cold caches, 5.8 a call behind another; the columns over 128 SMs),
 // for many the 2 n d_k d_v FMA of a head and their shared-memory loads (32 users with 32 nodes: 70 us, against 35 on
 // the tensor cores).
 template <typename Tok, int K, int V>
