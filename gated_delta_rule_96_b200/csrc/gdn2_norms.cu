@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(256) gated_norm_bwd_kernel(const Tok *__restri
         }
         ss = lane_sum<LPR>(ss);
         sd = lane_sum<LPR>(sd);
-        const float inv = rsqrtf(ss * (1.f / D) + eps);
+        const float inv = r < rows ? rsqrtf(ss * (1.f / D) + eps) : 0.f;   // eps may be 0
         const float mean = sd * inv * inv * (1.f / D);    // mean(dx^ x^) r, to be multiplied by o
         float out[N];
 #pragma unroll

@@ -81,6 +81,17 @@ def test_gated_norm_rows_of_zeros_and_wide_gates():
     assert (f64(y)[1, 1::2] == 0).all()
 
 
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("bf16", 2), ("bf16", 3), ("bf16", 45), ("bf16", 9003), ("f32", 1),
+                                        ("f32", 3), ("f32", 5001)])
+def test_gated_norm_without_an_eps(dtype, rows, d, act):
+    """eps = 0, the rows not filling the last warp: a place without a row takes no part in dweight."""
+    torch, g = cuda_or_skip()
+    t = _make(torch, rows + d, rows, d, dtype, ("o", "gate", "dy"), ("weight",))
+    check_gated(g, torch, t, act, dtype, eps=0.0)
+
+
 def test_gated_norm_in_place_shapes_and_empty():
     torch, g = cuda_or_skip()
     t = _make(torch, 6, 60, 128, "bf16", ("o", "gate", "dy"), ("weight",))
