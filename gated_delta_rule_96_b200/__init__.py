@@ -25,7 +25,7 @@ __all__ = [
     "gdn2_gated_norm_fwd", "gdn2_gated_norm_bwd", "gdn2_gated_norm_bwd_workspace_bytes", "gated_norm_fwd",
     "gated_norm_bwd", "gdn2_gated_norm", "gdn2_add_norm_fwd", "gdn2_add_norm_bwd",
     "gdn2_add_norm_bwd_workspace_bytes", "add_norm_fwd", "add_norm_bwd", "gdn2_add_norm", "gdn2_tree_fwd",
-    "tree_fwd", "gdn2_recurrent_fwd", "recurrent_fwd", "gdn2_state_copy", "TREE_MAX_NODES",
+    "tree_fwd", "gdn2_recurrent_fwd", "recurrent_fwd", "gdn2_state_copy", "gdn2_set_wait_limit", "TREE_MAX_NODES",
     "STATE_COPY_MAX_PAIRS", "DEV_RANGE", "DEV_SLOT", "DEV_PARENT", "DEV_INDEX", "DEV_CONFLICT", "DEV_WAIT",
 ]
 
@@ -114,6 +114,8 @@ def load_library():
     lib.gdn2_recurrent_fwd.restype = i
     lib.gdn2_state_copy.argtypes = [vp, ll, i, vp, ll, i, vp, vp, i, ll, vp, sz, vp]
     lib.gdn2_state_copy.restype = i
+    lib.gdn2_set_wait_limit.argtypes = [ll]
+    lib.gdn2_set_wait_limit.restype = i
     lib.gdn2_status_str.argtypes = [i]
     lib.gdn2_status_str.restype = ctypes.c_char_p
     _lib = lib
@@ -544,6 +546,14 @@ def gdn2_workspace_status(workspace, clear=False, stream=None) -> int:
     if rc != 0:
         raise GDN2Error(rc, "gdn2_workspace_status")
     return out.value
+
+
+def gdn2_set_wait_limit(polls) -> None:
+    """For tests of DEV_WAIT (include/gdn2.h): the calling thread's bounded waits give up after so many polls; -1: the
+    usual limits."""
+    rc = load_library().gdn2_set_wait_limit(int(polls))
+    if rc != 0:
+        raise GDN2Error(rc, "gdn2_set_wait_limit")
 
 
 def chunk_fwd(q, k, v, alpha, b, w, S0=None, C=64, workspace=None, stream=None):

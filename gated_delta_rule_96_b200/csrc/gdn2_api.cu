@@ -12,6 +12,8 @@ namespace {
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool dim_ok(int d) { return d == 64 || d == 128; }
 
+thread_local long long t_wait_limit = -1;   // gdn2_set_wait_limit
+
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 // width of the residual norm: whole 16-byte vectors in either token type, a row within one block's registers
 bool width_ok(int width) { return width > 0 && width % 8 == 0 && width <= 8192; }
@@ -85,6 +87,10 @@ int select_path(int B, int H, int T, int K, int V, int C, int dtype) {
 }
 
 }  // namespace
+
+namespace gdn2 {
+uint32_t wait_limit(uint32_t usual) { return t_wait_limit < 0 ? usual : (uint32_t)t_wait_limit; }
+}  // namespace gdn2
 
 extern "C" {
 
@@ -421,6 +427,12 @@ int gdn2_gemm_phase_probe(int mode, int reps, int nctas, void *workspace, size_t
     if (workspace_bytes < gdn2::kStatusBytes) return GDN2_ERR_WORKSPACE;
     return gdn2::launch_phase_probe(mode, reps, nctas, reinterpret_cast<unsigned int *>(workspace),
                                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+int gdn2_set_wait_limit(long long polls) {
+    if (polls < -1 || polls > 0xffffffffll) return GDN2_ERR_VALUE;
+    t_wait_limit = polls;
+    return GDN2_OK;
 }
 
 int gdn2_workspace_status(void *workspace, int clear, int *out, void *stream) {

@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 #include <stddef.h>
+#include <stdint.h>
 
 namespace gdn2 {
 
@@ -36,6 +37,10 @@ inline int launch_close(void (*kern)(Params...), dim3 grid, int threads, size_t 
 // In every such kernel, before any access to memory that is not the block's own: waits until the kernel before
 // has ended and its writes can be seen.
 __device__ __forceinline__ void behind_last_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Polls of a bounded wait in the next launch: `usual`, unless the calling thread has set another limit
+// (gdn2_set_wait_limit).
+uint32_t wait_limit(uint32_t usual);
 
 // Status header at the start of every prefill workspace (device status words).
 constexpr size_t kStatusBytes = 256;

@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
     const Tok *__restrict__ b, const Tok *__restrict__ w, float *S, long long slot_stride, int num_slots,
     const int *__restrict__ slots_in, const int *__restrict__ slots_out, const int *__restrict__ cu,
     const int *__restrict__ index, Tok *__restrict__ o, int batch, int H, int splits, int total, int rows,
-    unsigned *status) {
+    uint32_t limit, unsigned *status) {
     constexpr int RJ = K / 32, NP = PRODUCERS<K, V>;
     // a producer waits for a ring slot's last use by its parity: it must not be two uses ahead of the consumers
     static_assert(RING >= NP, "each producer's blocks are NP apart");
@@ -305,9 +305,13 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
     __syncthreads();
     behind_last_kernel();
 
-    bool ok = true;   // every wait is bounded; a warp whose wait ran out reports it and leaves
-    const uint32_t limit = (uint32_t)min((long long)WAIT_LIMIT + (long long)WAIT_TOKEN * total, 0xffffffffll);
-    auto wait = [&](unsigned long long &x, int phase) { return ok = ok && mbar_wait(bar(x), phase & 1, limit); };
+    // Every wait is bounded.  A warp whose wait ran out (one verdict for all its lanes) reports it and leaves without
+    // another write to a state or to the ring, and without the arrival that would pass its item on: the storer finds no
+    // item done that lacks a consumer, and the scout refills no buffer that was not stored.
+    bool ok = false;
+    auto wait = [&](unsigned long long &x, int phase) {
+        return __all_sync(0xffffffffu, mbar_wait(bar(x), phase & 1, limit));
+    };
     auto state_of = [&](const Item &x, int slot) {   // the item's part of a slot
         return S + (size_t)slot * slot_stride + (size_t)x.head * K * V + x.col0;
     };
@@ -336,9 +340,10 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
             if (bad || (x.n == 0 && x.from == x.to)) x = {0, 0, -1, -1, 0, 0};
             return x;
         };
-        for (int it = 0;; ++it) {
+        int it = 0;
+        for (;; ++it) {
             const long long at = blockIdx.x + (long long)it * gridDim.x;
-            if (at >= items) break;
+            if ((ok = at >= items)) break;
             const int d = it % DEPTH;
             const Item x = look(at);
             // the storer is done with the buffer, the producers with the words of the item that was there
@@ -353,24 +358,31 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
                 }
             }
         }
+        // The block does not end before the last copies into its memory have landed, whatever the other warps' waits
+        // came to: the last one of each buffer, with the usual limit.
+        for (int i = max(0, it - DEPTH); whole && i < it; ++i)
+            if (!mbar_wait(bar(sh.landed[i % DEPTH]), i / DEPTH & 1, WAIT_LIMIT)) ok = false;
     } else {
         int g = 0;        // token blocks so far
         int it = 0;
-        for (long long at = blockIdx.x; at < items && ok; at += gridDim.x, ++it) {
+        for (long long at = blockIdx.x;; at += gridDim.x, ++it) {
+            if ((ok = at >= items)) break;
             const int d = it % DEPTH, turn = it / DEPTH;
             if (!wait(sh.known[d], turn)) break;
             const Item x = sh.item[d];
             const int head = x.head, col0 = x.col0;
             const int blocks = (x.n + M - 1) / M;
             if (warp >= consumers && warp < consumers + NP) {   // producers
+                bool free = true;
                 for (int i = 0; i < blocks; ++i, ++g) {
                     if (g % NP != warp - consumers) continue;
-                    if (!wait(sh.empty[g % RING], g / RING + 1)) break;
+                    if (!(free = wait(sh.empty[g % RING], g / RING + 1))) break;
                     produce<Tok, K, V>(sh.ring[g % RING], q, k, v, alpha, b, w, index, x.lo + i * M,
                                        min(M, x.n - i * M), H, head, col0, cols, lane);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(sh.full[g % RING]));
                 }
+                if (!free) break;
                 if (lane == 0) mbar_arrive(bar(sh.read[d]));
             } else if (warp > consumers + NP) { // storer
                 if (!wait(sh.done[d], turn)) break;
@@ -398,18 +410,23 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
                         }
                         s[j][i][0] = y.x; s[j][i][1] = y.y; s[j][i][2] = y.z; s[j][i][3] = y.w;
                     }
+                bool filled = true;
 #pragma unroll 1
                 for (int i = 0; i < blocks; ++i, ++g) {
-                    if (!wait(sh.full[g % RING], g / RING)) break;
+                    // A lane's own verdict, and no branch on it: where the wait ran out the warp goes on, over whatever the
+                    // ring holds, to the item's end, and leaves there (a vote for every block cost fp32 runs 5 %, this 2).
+                    // It frees no slot that it did not find filled, so the other warps' blocks stay whole.
+                    filled &= mbar_wait(bar(sh.full[g % RING]), g / RING & 1, filled ? limit : 0u);
                     const int t0 = x.lo + i * M, n = x.n - i * M;
                     const Block<K, V> &in = sh.ring[g % RING];
                     if (n >= 3) consume<Tok, K, V, M, OUT>(in, s, o, t0, n, H, head, col0, warp * 16, lane);
                     else if (n == 2) consume<Tok, K, V, 2, OUT>(in, s, o, t0, n, H, head, col0, warp * 16, lane);
                     else consume<Tok, K, V, 1, OUT>(in, s, o, t0, n, H, head, col0, warp * 16, lane);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(sh.empty[g % RING]));
+                    if (lane == 0 && filled) mbar_arrive(bar(sh.empty[g % RING]));
                 }
-                if (x.to >= 0 && ok) {
+                if (!__all_sync(0xffffffffu, filled)) break;
+                if (x.to >= 0) {
 #pragma unroll
                     for (int j = 0; j < RJ; ++j)
 #pragma unroll
@@ -425,10 +442,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
             }
         }
     }
-    if (!ok) {   // reported; no copy may still be on its way into this CTA's memory when it ends
-        if (lane == 0) atomicOr(status, DEV_WAIT);
-        for (int d = 0; d < DEPTH; ++d) mbar_wait(bar(sh.landed[d]), 0, WAIT_LIMIT);
-    }
+    if (!ok && lane == 0) atomicOr(status, DEV_WAIT);
 }
 
 template <typename Tok, int K, int V, bool OUT>
@@ -449,9 +463,11 @@ int launch_out(const void *q, const void *k, const void *v, const float *alpha, 
     int splits = 1;
     while (splits < V / 16 && (long long)batch * H * splits * 2 <= 148) splits *= 2;
     const long long items = (long long)batch * H * splits, grid = items < 148 * per_sm ? items : 148 * per_sm;
+    const long long polls = (long long)WAIT_LIMIT + (long long)WAIT_TOKEN * total;
     return launch_close(kern, (unsigned)grid, 2 * V / splits + 32 * EXTRA_WARPS<K, V>, smem_bytes<K, V>(V / splits), st,
                         (const Tok *)q, (const Tok *)k, (const Tok *)v, alpha, (const Tok *)b, (const Tok *)w, S, slot_stride,
-                        num_slots, slots_in, slots_out, cu, index, (Tok *)o, batch, H, splits, total, rows, status);
+                        num_slots, slots_in, slots_out, cu, index, (Tok *)o, batch, H, splits, total, rows,
+                        wait_limit(polls < 0xffffffffll ? (uint32_t)polls : 0xffffffffu), status);
 }
 
 template <typename Tok, int K, int V>

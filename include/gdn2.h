@@ -18,7 +18,8 @@
  *   - All tensor pointers are DEVICE pointers to contiguous, row-major buffers, each
  *     16-byte aligned.  The caller owns every buffer; the library allocates nothing
  *     and keeps no state between calls, except gdn2_chunk_fwd_noalloc, whose fixed
- *     scratch array (below) is library-owned device memory shared by all its calls.
+ *     scratch array (below) is library-owned device memory shared by all its calls,
+ *     and a limit for tests (gdn2_set_wait_limit).
  *   - Kernels launch on the calling thread's current CUDA device, which must own every
  *     pointer of the call (and `stream`, if given).
  *   - Calls are asynchronous on `stream` (a cudaStream_t passed as void*; NULL = the
@@ -65,7 +66,9 @@ typedef enum { GDN2_GATE_SILU = 0, GDN2_GATE_SIGMOID = 1 } gdn2_gate;
 
 /* Bits of a workspace's status word (gdn2_workspace_status) for device-side indices that the host
  * cannot check: gdn2_tree_fwd, gdn2_recurrent_fwd and gdn2_state_copy leave the sequence or pair
- * that has one out as a whole, write nothing of it, and set the bit. */
+ * that has one out as a whole, write nothing of it, and set the bit.  GDN2_DEV_WAIT is another
+ * kind: the call gave up, and what it wrote to o is not to be used.  A state is never left half
+ * advanced: each column of a head's state is the one after its run, or as it was. */
 #define GDN2_DEV_RANGE 0x100    /* cumulative lengths that decrease, pass the total, or hold more
                                    than max_nodes nodes                                          */
 #define GDN2_DEV_SLOT 0x200     /* a slot outside [-1, num_slots)                                */
@@ -374,6 +377,11 @@ GDN2_API int gdn2_chunk_bwd_tc(const void *q, const void *k, const void *v, cons
 #define GDN2_PHASE_PROBE_FLOPS_PER_CHUNK 14680064.0
 GDN2_API int gdn2_gemm_phase_probe(int mode, int reps, int nctas, void *workspace, size_t workspace_bytes,
                                    void *stream);
+
+/* For tests of GDN2_DEV_WAIT: how often a bounded wait polls before it gives up, in what the calling
+ * thread launches from here on of gdn2_recurrent_fwd; 0: every wait runs out at once, -1: the usual
+ * limits again.  GDN2_ERR_VALUE outside [-1, 2^32). */
+GDN2_API int gdn2_set_wait_limit(long long polls);
 
 /* Reads the device status word of a workspace (synchronises `stream` first).
  * *out receives 0 when every kernel that used this workspace finished normally, or a

@@ -353,6 +353,49 @@ def test_recurrent_reports_malformed_indices_and_conflicts():
         assert torch.equal(p[idle], pool[idle]), change
 
 
+@pytest.fixture
+def wait_limit():
+    """Sets how often the bounded waits of this thread's calls poll; the usual limits again when the test ends."""
+    import gated_delta_rule_96_b200 as g
+    yield g.gdn2_set_wait_limit
+    g.gdn2_set_wait_limit(-1)
+
+
+@pytest.mark.parametrize("H,sizes", [(16, [40, 0, 300, 1, 7, 3, 90, 12, 1, 5, 2, 33]),    # a CTA holds a head's columns
+                                     (2, [700, 0, 2])])                                  # they are split over CTAs
+def test_recurrent_waits_that_run_out(wait_limit, H, sizes):
+    """Whichever wait runs out: the call ends and says so, and a column of a state is either its run's last one or as it
+    was.  Reported once, the next call is as ever."""
+    torch, g = cuda_or_skip()
+    n = len(sizes)
+    x, pool = tokens(torch, H, sum(sizes), H, 128, 128, "bf16"), make_pool(torch, H, 2 * n, H, 128, 128)
+    src = list(range(n - 1)) + [-1]
+    for dst in (list(range(n)), list(range(n, 2 * n))):                  # in place, and to other slots
+        args = [i32(torch, a) for a in (src, dst, np.concatenate([[0], np.cumsum(sizes)]))]
+        want, ws = pool.clone(), g.new_workspace(0)
+        o_want = torch.full_like(x[2], float("nan"))
+        g.gdn2_recurrent_fwd(*x, want, *args, None, o_want, workspace=ws)
+        assert g.gdn2_workspace_status(ws) == 0
+        for polls in (0, 1, 2, 3, 4, 6, 8, 12, 16, 32, 64, 256, 4096):
+            p, o = pool.clone(), torch.full_like(x[2], float("nan"))
+            wait_limit(polls)
+            g.gdn2_recurrent_fwd(*x, p, *args, None, o, workspace=ws)
+            wait_limit(-1)
+            status = g.gdn2_workspace_status(ws, clear=True)
+            new, old = (p == want).all(-2), (p == pool).all(-2)          # by slot, head and column
+            assert (new | old).all(), polls
+            if n > 10:                                                   # a head's columns go together
+                assert (new.all(-1) | old.all(-1)).all(), polls
+            if status == 0:
+                assert torch.equal(p, want) and torch.equal(o, o_want), polls
+            else:
+                assert status == g.DEV_WAIT
+            if polls == 0:
+                assert status == g.DEV_WAIT and old.all() and torch.isnan(o).all()
+        g.gdn2_recurrent_fwd(*x, pool, *args, None, o, workspace=ws)
+        assert g.gdn2_workspace_status(ws) == 0 and torch.equal(pool, want) and torch.equal(o, o_want)
+
+
 @pytest.mark.parametrize("slots,shape,n", [(5, (1, 64, 64), 1), (9, (3, 64, 128), 4), (40, (2, 128, 128), 33),
                                            (300, (1, 64, 64), 250), (1100, (1, 4), 1024), (2000, (3, 64, 64), 1024)])
 def test_state_copy(slots, shape, n):

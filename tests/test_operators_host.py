@@ -101,6 +101,12 @@ def test_entry_points_refuse(lib, call, want):
     assert g.gdn2_status_str(want) != "unknown status"
 
 
+def test_wait_limit(lib):
+    assert [lib.gdn2_set_wait_limit(n) for n in (-2, 1 << 32, 0, (1 << 32) - 1, -1)] == [-10, -10, 0, 0, 0]
+    with pytest.raises(g.GDN2Error):
+        g.gdn2_set_wait_limit(-5)
+
+
 def test_workspace_sizes():
     assert g.gdn2_gated_norm_bwd_workspace_bytes(-1, 128) == 0 and g.gdn2_gated_norm_bwd_workspace_bytes(4, 96) == 0
     assert g.gdn2_gated_norm_bwd_workspace_bytes(0, 128) >= 256 + 4 * 128
