@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(THREADS) state_copy_kernel(float *dst, long lo
                                                              const float *src, long long src_stride, int src_slots,
                                                              const int *__restrict__ dst_idx,
                                                              const int *__restrict__ src_idx, int n, int group,
-                                                             int slot_vecs, unsigned *status) {
+                                                             int slot_vecs, uint32_t limit, unsigned *status) {
     extern __shared__ __align__(16) unsigned char raw[];
     const Layout l = layout(n, group);
     int *s_dst = reinterpret_cast<int *>(raw + l.pairs), *s_src = s_dst + n, *s_key = s_src + n, *s_last = s_key + l.table;
@@ -119,27 +119,29 @@ __global__ void __launch_bounds__(THREADS) state_copy_kernel(float *dst, long lo
                 reorder |= w >= 0 && s_src[w] != s_src[i];   // a slot that is written over by itself does not change
             }
     reorder = __syncthreads_or(reorder);
-    bool ok = mbar_wait(bar, 0, WAIT_LIMIT);
+    // one verdict for the block, so that a round that is given up has every thread's arrival and ends all the same
+    uint32_t phase = 0;
+    bool ok = mbar_wait(bar, phase, limit);
     for (int i = tid; i < n; i += THREADS)
         if (s_dst[i] >= 0 && last(s_dst[i]) != i) s_dst[i] = -1;
-    __syncthreads();
+    ok = !__syncthreads_or(!ok);
     if (!reorder) {
         if (ok) store(lo, hi, first, len, RANGE);
     } else {
         // a thread loads and stores the same pairs in every round, so its own stores are all it waits for
         const int pitch = l.vecs / n < RANGE ? l.vecs / n : RANGE;
-        uint32_t phase = 1;
-        for (int at = blockIdx.y * pitch; ok && at < len; at += gridDim.y * pitch, phase ^= 1) {
+        for (int at = blockIdx.y * pitch; ok && at < len; at += gridDim.y * pitch) {
             const int count = min(pitch, len - at);
             load(0, n, first + at, count, pitch);
-            ok = mbar_wait(bar, phase, WAIT_LIMIT);
+            phase ^= 1;
+            ok = !__syncthreads_or(!mbar_wait(bar, phase, limit));
             if (ok) store(0, n, first + at, count, pitch);
             bulk_wait_read_all();
         }
     }
-    if (!ok) {   // reported and left out, after one more wait for the copies that are still on their way
-        atomicOr(status, DEV_WAIT);
-        mbar_wait(bar, 0, WAIT_LIMIT);
+    if (!ok) {   // reported and left out, after the usual wait for the round's copies, which are still on their way here
+        if (tid == 0) atomicOr(status, DEV_WAIT);
+        mbar_wait(bar, phase, WAIT_LIMIT);
     }
     bulk_wait_read_all();
 }
@@ -157,7 +159,8 @@ int launch_state_copy(float *dst, long long dst_stride, int dst_slots, const flo
     const size_t smem = layout(n, (int)group).total;
     if (!allow_smem(state_copy_kernel, layout(kStateCopyMaxPairs, GROUP).total)) return -6;
     return launch_close(state_copy_kernel, dim3((unsigned)ranges, (unsigned)((n + group - 1) / group)), THREADS, smem, st, dst,
-                        dst_stride, dst_slots, src, src_stride, src_slots, dst_idx, src_idx, n, (int)group, (int)vecs, status);
+                        dst_stride, dst_slots, src, src_stride, src_slots, dst_idx, src_idx, n, (int)group, (int)vecs,
+                        wait_limit(WAIT_LIMIT), status);
 }
 
 }  // namespace gdn2

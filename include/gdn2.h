@@ -68,7 +68,8 @@ typedef enum { GDN2_GATE_SILU = 0, GDN2_GATE_SIGMOID = 1 } gdn2_gate;
  * cannot check: gdn2_tree_fwd, gdn2_recurrent_fwd and gdn2_state_copy leave the sequence or pair
  * that has one out as a whole, write nothing of it, and set the bit.  GDN2_DEV_WAIT is another
  * kind: the call gave up, and what it wrote to o is not to be used.  A state is never left half
- * advanced: each column of a head's state is the one after its run, or as it was. */
+ * advanced: each column of a head's state is the one after its run, or as it was; each 16 bytes of a
+ * copy's destination are the source's, or as they were. */
 #define GDN2_DEV_RANGE 0x100    /* cumulative lengths that decrease, pass the total, or hold more
                                    than max_nodes nodes                                          */
 #define GDN2_DEV_SLOT 0x200     /* a slot outside [-1, num_slots)                                */
@@ -379,7 +380,7 @@ GDN2_API int gdn2_gemm_phase_probe(int mode, int reps, int nctas, void *workspac
                                    void *stream);
 
 /* For tests of GDN2_DEV_WAIT: how often a bounded wait polls before it gives up, in what the calling
- * thread launches from here on of gdn2_recurrent_fwd; 0: every wait runs out at once, -1: the usual
+ * thread launches from here on of gdn2_recurrent_fwd and gdn2_state_copy; 0: every wait runs out at once, -1: the usual
  * limits again.  GDN2_ERR_VALUE outside [-1, 2^32). */
 GDN2_API int gdn2_set_wait_limit(long long polls);
 

@@ -418,6 +418,34 @@ def test_state_copy(slots, shape, n):
     assert np.array_equal(other.cpu().numpy(), op.state_copy(keep.cpu().numpy(), pool.cpu().numpy(), dst, src))
 
 
+@pytest.mark.parametrize("slots,shape,n", [(5, (2, 64, 64), 4), (300, (4, 128, 128), 250)])
+def test_state_copy_waits_that_run_out(wait_limit, slots, shape, n):
+    """Whichever wait runs out: the call ends and says so, and every value is the source's or as it was."""
+    torch, g = cuda_or_skip()
+    pool = torch.randn(slots, *shape, generator=torch.Generator().manual_seed(n)).cuda()
+    order = np.random.default_rng(n).permutation(slots)
+    for dst, src in ((order[:n], np.roll(order[:n], 1)), (order[:n // 2], order[n // 2:n // 2 * 2])):  # a reorder, a copy
+        to, frm, ws = i32(torch, dst), i32(torch, src), g.new_workspace(0)
+        want = pool.clone()
+        g.gdn2_state_copy(want, want, to, frm, workspace=ws)
+        assert g.gdn2_workspace_status(ws) == 0 and torch.equal(want[dst], pool[src])
+        for polls in (0, 1, 2, 3, 4, 8, 16, 64, 1024):
+            p = pool.clone()
+            wait_limit(polls)
+            g.gdn2_state_copy(p, p, to, frm, workspace=ws)
+            wait_limit(-1)
+            status = g.gdn2_workspace_status(ws, clear=True)
+            assert ((p == want) | (p == pool)).all(), polls
+            if status == 0:
+                assert torch.equal(p, want), polls
+            else:
+                assert status == g.DEV_WAIT
+            if polls == 0:
+                assert status == g.DEV_WAIT and torch.equal(p, pool)
+        g.gdn2_state_copy(pool, pool, to, frm, workspace=ws)
+        assert g.gdn2_workspace_status(ws) == 0 and torch.equal(pool, want)
+
+
 def test_state_copy_reports_bad_slots_and_serves_the_rest():
     torch, g = cuda_or_skip()
     pool = make_pool(torch, 12, 6, 1, 64, 64)
