@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
     const float *__restrict__ alpha, const __nv_bfloat16 *__restrict__ b, const __nv_bfloat16 *__restrict__ w,
     const float *__restrict__ S, long long slot_stride, int num_slots, const int *__restrict__ slots,
     const int *__restrict__ cu, const int *__restrict__ parents, __nv_bfloat16 *__restrict__ o, int batch, int H,
-    int total, int max_nodes, unsigned *status) {
+    int total, int max_nodes, uint32_t limit, unsigned *status) {
     extern __shared__ unsigned char raw[];
     TcShared &sh = *reinterpret_cast<TcShared *>(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
     // the group's barriers.  One warp of a group polls, the others sleep at the barrier.  Phases count the items
     // that have nodes (c); the others only pass their meta on.
     const auto wait = [&](unsigned long long &x, int phase) {
-        const bool ok = mbar_wait(bar(x), phase & 1, WAIT_LIMIT) && !*abort;
+        const bool ok = mbar_wait(bar(x), phase & 1, limit) && !*abort;
         if (!ok) *abort = 1u;
         return ok;
     };
@@ -187,6 +187,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
             if (head >= H) head -= H, ++seq;
         }
     } else if (warp == LEAD) {
+        int pairs_out = 0, state_out = 0;   // items whose products have been issued
         for (int it = 0;; ++it) {
             if (blockIdx.x + (long long)it * gridDim.x >= items) break;
             if (!warp_wait(sh.meta_known[it % METAS], it / METAS)) break;
@@ -213,6 +214,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                     mma_commit(bar(sh.p_full));
                     mbar_arrive(bar(sh.p_full));
                 }
+                ++pairs_out;
                 __syncwarp();
                 if (!warp_wait(sh.s_full[c & 1], c >> 1) || !warp_wait(sh.d_free, c + 1)) break;
                 fence_after();
@@ -230,10 +232,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                     mma_commit(bar(sh.b_free));
                     mma_commit(bar(sh.d_full));
                 }
+                ++state_out;
                 __syncwarp();
                 ++c;
             }
         }
+        // The block gives up neither its shared nor its tensor memory before the last products have ended, whatever the
+        // other warps' waits came to.
+        if (pairs_out && !mbar_wait(bar(sh.p_full), (pairs_out - 1) & 1, WAIT_LIMIT)) *abort = 1u;
+        if (state_out && !mbar_wait(bar(sh.d_full), (state_out - 1) & 1, WAIT_LIMIT)) *abort = 1u;
     } else if (warp < COLUMN_WARPS) {
         const int col = tid & 127, half = tid >> 7;   // value column, warpgroup
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
@@ -526,7 +533,7 @@ int launch_tc(const void *q, const void *k, const void *v, const float *alpha, c
     const long long items = (long long)batch * H;
     return launch_close(tree_tc_kernel, (unsigned)(items < 148 ? items : 148), TC_THREADS, smem, st, (const bf *)q, (const bf *)k,
                         (const bf *)v, alpha, (const bf *)b, (const bf *)w, S, slot_stride, num_slots, slots, cu, parents,
-                        (bf *)o, batch, H, total, max_nodes, status);
+                        (bf *)o, batch, H, total, max_nodes, wait_limit(WAIT_LIMIT), status);
 }
 
 }  // namespace tree

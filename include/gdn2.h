@@ -380,8 +380,8 @@ GDN2_API int gdn2_gemm_phase_probe(int mode, int reps, int nctas, void *workspac
                                    void *stream);
 
 /* For tests of GDN2_DEV_WAIT: how often a bounded wait polls before it gives up, in what the calling
- * thread launches from here on of gdn2_recurrent_fwd and gdn2_state_copy; 0: every wait runs out at once, -1: the usual
- * limits again.  GDN2_ERR_VALUE outside [-1, 2^32). */
+ * thread launches from here on of gdn2_tree_fwd, gdn2_recurrent_fwd and gdn2_state_copy; 0: every
+ * wait runs out at once, -1: the usual limits again.  GDN2_ERR_VALUE outside [-1, 2^32). */
 GDN2_API int gdn2_set_wait_limit(long long polls);
 
 /* Reads the device status word of a workspace (synchronises `stream` first).

@@ -46,6 +46,14 @@ def close(got, ref, dtype):
     assert (np.abs(got - ref) <= bar).all(), f"worst {np.max(np.abs(got - ref) / bar):.2f} of the bar"
 
 
+@pytest.fixture
+def wait_limit():
+    """Sets how often the bounded waits of this thread's calls poll; the usual limits again when the test ends."""
+    import gated_delta_rule_96_b200 as g
+    yield g.gdn2_set_wait_limit
+    g.gdn2_set_wait_limit(-1)
+
+
 def random_tree(rng, n, back):
     return [-1] + [int(rng.integers(max(-1, i - back), i)) for i in range(1, n)] if n else []
 
@@ -166,6 +174,33 @@ def test_tree_branches_do_not_touch_one_another(dtype, n):
     well = [i for i in range(n) if i not in sick]
     assert torch.equal(o[well], clean[well])
     assert not torch.isfinite(o[sick].float()).any()
+
+
+@pytest.mark.parametrize("batch,n", [(20, 64), (3, 41)])
+def test_tree_waits_that_run_out(wait_limit, batch, n):
+    """Whichever wait of the tensor-core kernel runs out: the call ends and says so, a row of o is right or as it was,
+    and the next call is as ever (no product is left on its way, no tensor memory held)."""
+    torch, g = cuda_or_skip()
+    H, sizes = 16, [n - i % 3 for i in range(batch)]
+    cu = np.concatenate([[0], np.cumsum(sizes)])
+    parents = sum((random_tree(np.random.default_rng(i), m, 1 + i) for i, m in enumerate(sizes)), [])
+    x, pool = tokens(torch, n, cu[-1], H, 128, 128, "bf16"), make_pool(torch, n, batch, H, 128, 128)
+    args = [i32(torch, a) for a in (range(batch), cu, parents)]
+    want, ws = torch.full_like(x[2], float("nan")), g.new_workspace(0)
+    g.gdn2_tree_fwd(*x, pool, *args, want, n, workspace=ws)
+    assert g.gdn2_workspace_status(ws) == 0 and torch.isfinite(want).all()
+    for polls in (0, 1, 2, 3, 4, 6, 8, 12, 16, 32, 64, 128, 256, 1024, 4096):
+        o = torch.full_like(want, float("nan"))
+        wait_limit(polls)
+        g.gdn2_tree_fwd(*x, pool, *args, o, n, workspace=ws)
+        wait_limit(-1)
+        status = g.gdn2_workspace_status(ws, clear=True)
+        assert status == g.DEV_WAIT or (status == 0 and torch.equal(o, want)), polls
+        assert ((o == want).all(-1) | torch.isnan(o).all(-1)).all(), polls
+        if polls == 0:
+            assert status == g.DEV_WAIT and torch.isnan(o).all()
+        g.gdn2_tree_fwd(*x, pool, *args, o, n, workspace=ws)
+        assert g.gdn2_workspace_status(ws) == 0 and torch.equal(o, want), polls
 
 
 def test_tree_reports_malformed_indices_and_serves_the_rest():
@@ -351,14 +386,6 @@ def test_recurrent_reports_malformed_indices_and_conflicts():
         written = {c["dst"][i] for i in range(4) if i not in out}
         idle = [s for s in range(8) if s not in written]
         assert torch.equal(p[idle], pool[idle]), change
-
-
-@pytest.fixture
-def wait_limit():
-    """Sets how often the bounded waits of this thread's calls poll; the usual limits again when the test ends."""
-    import gated_delta_rule_96_b200 as g
-    yield g.gdn2_set_wait_limit
-    g.gdn2_set_wait_limit(-1)
 
 
 @pytest.mark.parametrize("H,sizes", [(16, [40, 0, 300, 1, 7, 3, 90, 12, 1, 5, 2, 33]),    # a CTA holds a head's columns
