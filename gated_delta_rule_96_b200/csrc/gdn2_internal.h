@@ -7,12 +7,20 @@
 
 namespace gdn2 {
 
+// Whether a runtime call succeeded.  One that did not is reported by the call at hand; its error does not stay behind
+// for the next one that asks for the last error.
+inline bool succeeded(cudaError_t e) {
+    if (e == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
+}
+
 // Lets `kern` use up to `bytes` of dynamic shared memory on the current device.  At every launch, since the
 // attribute is a device's (and a context's) own and setting it takes a fraction of a microsecond; always the most
 // that any launch of the kernel uses, since another host thread may be between this and its launch.
 template <typename Kernel>
 inline bool allow_smem(Kernel kern, size_t bytes) {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+    return succeeded(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
 }
 
 // A launch that the device prepares while the stream's kernel before it still runs: its blocks are placed as that
@@ -32,7 +40,7 @@ inline int launch_close(void (*kern)(Params...), dim3 grid, int threads, size_t 
     config.stream = st;
     config.attrs = &close;
     config.numAttrs = 1;
-    return cudaLaunchKernelEx(&config, kern, static_cast<Params>(args)...) == cudaSuccess ? 0 : -6;
+    return succeeded(cudaLaunchKernelEx(&config, kern, static_cast<Params>(args)...)) ? 0 : -6;
 }
 // In every such kernel, before any access to memory that is not the block's own: waits until the kernel before
 // has ended and its writes can be seen.

@@ -452,7 +452,7 @@ int cap_blocks(long long want, int per_sm) {
 template <typename Kernel>
 int resident(Kernel kern, int threads, size_t smem) {
     int n = 0;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) == cudaSuccess ? n : 1;
+    return succeeded(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem)) ? n : 1;
 }
 
 // warps that hold a row of `vecs` 16-byte vectors, NV a thread, and the rows of a block: narrow rows share one, since

@@ -456,7 +456,7 @@ int launch_out(const void *q, const void *k, const void *v, const float *alpha, 
     if (!allow_smem(kern, most)) return -6;
     int per_sm = resident.load();
     if (per_sm == 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, most) != cudaSuccess || per_sm < 1) return -6;
+        if (!succeeded(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, most)) || per_sm < 1) return -6;
         resident.store(per_sm);
     }
     // few chains: their columns over more SMs

@@ -600,6 +600,40 @@ def test_calls_behind_one_another_see_what_the_last_one_wrote():
     assert g.gdn2_workspace_status(ws) == 0
 
 
+def test_a_launch_that_fails_leaves_no_error_behind():
+    """A launch on the legacy default stream is refused while a blocking stream is being captured.  The call says so, and
+    the next call, of any kind, does not report it again."""
+    torch, g = cuda_or_skip()
+    from cuda.bindings import runtime as rt
+    x, pool = tokens(torch, 70, 3, 2, 128, 128, "bf16"), make_pool(torch, 71, 3, 2, 128, 128)
+    slots, other, cu, parents = (i32(torch, v) for v in ([0], [1], [0, 3], [-1, 0, 0]))
+    o, gate, w = x[2].reshape(-1, 128), x[5].reshape(-1, 128), torch.ones(128, device="cuda")
+    ws = g.new_workspace(g.gdn2_gated_norm_bwd_workspace_bytes(6, 128))
+    out = [torch.empty_like(o) for _ in range(3)] + [torch.empty_like(w)]
+    calls = [lambda: g.gdn2_tree_fwd(*x, pool, slots, cu, parents, x[2], 3, workspace=ws),
+             lambda: g.gdn2_recurrent_fwd(*x, pool, slots, other, cu, None, x[2], workspace=ws),
+             lambda: g.gdn2_state_copy(pool, pool, other, slots, workspace=ws),
+             lambda: g.gdn2_gated_norm_fwd(o, gate, w, out[0]),
+             lambda: g.gdn2_gated_norm_bwd(o, gate, w, gate, *out[1:], workspace=ws),
+             lambda: g.gdn2_add_norm_fwd(o, gate, None, w, out[0], out[1])]
+    torch.cuda.synchronize()
+    assert torch.cuda.current_stream().cuda_stream == 0
+    for call in calls:
+        err, stream = rt.cudaStreamCreate()                       # a blocking one
+        assert not err
+        assert not rt.cudaStreamBeginCapture(stream, rt.cudaStreamCaptureMode.cudaStreamCaptureModeRelaxed)[0]
+        try:
+            with pytest.raises(g.GDN2Error):
+                call()
+        finally:
+            rt.cudaStreamEndCapture(stream)                       # invalidated: an error, and no graph
+            rt.cudaGetLastError()
+            rt.cudaStreamDestroy(stream)
+        g.gdn2_rms_norm(out[0], w)                                # a launcher that reports the last error it finds
+        call()
+    torch.cuda.synchronize()
+
+
 def test_two_graphs_share_a_workspace():
     """The workspace of the calls over slots holds status words only: two captured graphs replayed at the same
     time on two streams do not disturb one another, and what either reports stays reported."""
