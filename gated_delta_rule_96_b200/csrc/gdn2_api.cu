@@ -408,7 +408,7 @@ int gdn2_state_copy(float *dst, long long dst_stride, int dst_slots, const float
     if (dst_stride < slot_floats || src_stride < slot_floats) return GDN2_ERR_SHAPE;
     if (slot_floats % 4 || dst_stride % 4 || src_stride % 4) return GDN2_ERR_ALIGN;
     if (pairs > GDN2_STATE_COPY_MAX_PAIRS || slot_floats > (1ll << 31)) return GDN2_ERR_UNSUPPORTED;
-    if (dst == src && dst_stride != src_stride) return GDN2_ERR_SHAPE;
+    if (dst == src && dst_slots > 1 && src_slots > 1 && dst_stride != src_stride) return GDN2_ERR_SHAPE;
     if (caches_clash(dst, dst_stride, dst_slots, src, src_stride, src_slots, slot_floats)) return GDN2_ERR_SHAPE;
     int rc = check_workspace(workspace, workspace_bytes, gdn2::kStatusBytes);
     if (rc != GDN2_OK) return rc;

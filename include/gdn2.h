@@ -273,8 +273,9 @@ GDN2_API int gdn2_recurrent_fwd(const void *q, const void *k, const void *v, con
  * skipped; of several pairs with one destination the last counts.
  *
  *   dst, src   caches of dst_slots / src_slots slots, slot_floats floats each, dst_stride /
- *              src_stride floats apart (multiples of 4); one cache (same pointer and stride) or two
- *              that do not overlap (GDN2_ERR_SHAPE; the parts of two layers of one pool do not)
+ *              src_stride floats apart (multiples of 4); one cache (same pointer and stride, or the
+ *              same pointer and one slot on a side) or two that do not overlap (GDN2_ERR_SHAPE; the
+ *              parts of two layers of one pool do not)
  *   pairs      at most GDN2_STATE_COPY_MAX_PAIRS in one call
  */
 #define GDN2_STATE_COPY_MAX_PAIRS 1024

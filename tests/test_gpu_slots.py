@@ -503,6 +503,20 @@ def test_one_layer_of_a_larger_pool():
     assert torch.equal(whole[:, [0, 2]], keep[:, [0, 2]])
 
 
+def test_copies_with_the_first_slot_of_a_layer_alone():
+    """One slot of a strided cache, a part of that cache: to it, and from it, with a clear among the copies."""
+    torch, g = cuda_or_skip()
+    whole = make_pool(torch, 17, 6 * 3, 2, 64, 64).view(6, 3, 2, 64, 64)
+    keep, layer = whole.clone(), whole[:, 1]
+    now = layer.clone()
+    g.gdn2_state_copy(layer[:1], layer, i32(torch, [0]), i32(torch, [3]))
+    assert torch.equal(layer[0], now[3]) and torch.equal(layer[1:], now[1:])
+    g.gdn2_state_copy(layer, layer[:1], i32(torch, [4, 0, 2]), i32(torch, [0, -1, 0]))
+    assert torch.equal(layer[4], now[3]) and torch.equal(layer[2], now[3]) and not layer[0].any()
+    assert torch.equal(layer[[1, 3, 5]], now[[1, 3, 5]])
+    assert torch.equal(whole[:, [0, 2]], keep[:, [0, 2]])
+
+
 def test_offsets_past_32_bits():
     """The last slots of a cache of more than 2^32 floats."""
     torch, g = cuda_or_skip()

@@ -101,6 +101,16 @@ def test_entry_points_refuse(lib, call, want):
     assert g.gdn2_status_str(want) != "unknown status"
 
 
+@pytest.mark.parametrize("change,want", [
+    # one slot has no stride: the first slot of a cache, with the cache's own stride or any other, is part of that cache
+    (dict(dnum=1, dstride=64, sstride=128), 0), (dict(snum=1, sstride=64, dstride=128), 0), (dict(dnum=1, snum=1, dstride=128), 0),
+    (dict(dnum=1, dstride=4096, sstride=128), 0), (dict(dnum=0, sstride=128), 0),
+    # two of one address with more slots each and other strides share memory without being one
+    (dict(dnum=2, snum=2, dstride=128), -2), (dict(dnum=2, dstride=64, sstride=128), -2)])
+def test_state_copy_of_a_one_slot_part(lib, change, want):
+    assert copy(lib, pairs=0, **change) == want
+
+
 def test_wait_limit(lib):
     assert [lib.gdn2_set_wait_limit(n) for n in (-2, 1 << 32, 0, (1 << 32) - 1, -1)] == [-10, -10, 0, 0, 0]
     with pytest.raises(g.GDN2Error):
