@@ -77,11 +77,14 @@ __device__ __forceinline__ float lane_sum(float x) {
 // 1 / (1 + 2^(-x log2 e)) on the special-function unit: two instructions there and two beside them, where
 // expf and the divide take some twenty, which bounded the kernels at two thirds of the copy rate.  Each of
 // the two is good to about one unit of fp32 (the argument's rounding adds |x| / 2 more); the ends are exact.
-__device__ __forceinline__ float sigmoid_(float x) {
+struct Sigmoid {
+    float s, c;   // sigmoid(x), and one less it without the cancellation that the difference has above zero
+};
+__device__ __forceinline__ Sigmoid sigmoid_(float x) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return r;
+    return {r, x > 0.f ? e * r : 1.f - r};
 }
 
 constexpr int ACT_SILU = 0;
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__(256) gated_norm_fwd_kernel(const Tok *o, const
         const float inv = rsqrtf(lane_sum<LPR>(ss) * (1.f / D) + eps);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float s = sigmoid_(g[i]);
+            const float s = sigmoid_(g[i]).s;
             x[i] = x[i] * inv * wt[i] * (ACT == ACT_SILU ? g[i] * s : s);
         }
         if (r < rows) __stcs(reinterpret_cast<uint4 *>(y + r * D) + sub, V::pack(x));
@@ -164,9 +167,9 @@ __global__ void __launch_bounds__(256) gated_norm_bwd_kernel(const Tok *__restri
         fetch(r + step);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float s = sigmoid_(g[i]);
+            const auto [s, c] = sigmoid_(g[i]);
             const float act = ACT == ACT_SILU ? g[i] * s : s;
-            const float slope = ACT == ACT_SILU ? s * (1.f + g[i] * (1.f - s)) : s * (1.f - s);
+            const float slope = ACT == ACT_SILU ? s * (1.f + g[i] * (1.f - s)) : s * c;
             ss = fmaf(x[i], x[i], ss);
             const float dn = d[i] * act;                  // d(x^ weight)
             sd = fmaf(dn * wt[i], x[i], sd);

@@ -92,6 +92,23 @@ def test_gated_norm_without_an_eps(dtype, rows, d, act):
     check_gated(g, torch, t, act, dtype, eps=0.0)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gated_norm_slope_of_wide_open_gates(dtype, d):
+    """dgate of sigmoid gates is a product alone, so it is right to a few units of its own size however far the gate is
+    open: s (1 - s) is 2e-9 at 20, where a difference of two fp32 has lost all digits.  The argument's rounding adds 20
+    units of 2^-24 there to what REL counts otherwise."""
+    torch, g = cuda_or_skip()
+    t = _make(torch, d, 301, d, dtype, ("o", "gate", "dy"), ("weight",))
+    t["gate"].copy_(torch.linspace(-20, 20, 301 * d).view(301, d))
+    _, dgate, _ = g.gated_norm_bwd(t["o"], t["gate"], t["weight"], t["dy"], act="sigmoid")
+    x = {n: f64(a) for n, a in t.items()}
+    slope = 1 / (1 + np.exp(-x["gate"])) / (1 + np.exp(x["gate"]))
+    r = 1 / np.sqrt((x["o"] ** 2).mean(-1, keepdims=True) + EPS)
+    ref = x["dy"] * x["o"] * r * x["weight"] * slope
+    close(dgate, ref, HALF[dtype], np.abs(ref))
+
+
 def test_gated_norm_in_place_shapes_and_empty():
     torch, g = cuda_or_skip()
     t = _make(torch, 6, 60, 128, "bf16", ("o", "gate", "dy"), ("weight",))
