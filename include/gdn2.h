@@ -157,7 +157,8 @@ GDN2_API int gdn2_rms_norm(void *o, const float *weight, long long rows, int d_v
  *                                                           or sigmoid(g) (GDN2_GATE_SIGMOID)
  *   o, gate, y   [rows, d_v]  token dtype; y may be o or gate
  *   weight       [d_v]        fp32
- * d_v in {64, 128}; eps in [0, 1].  fp32 arithmetic, y rounded once.
+ * d_v in {64, 128}; eps in [0, 1].  fp32 arithmetic, y rounded once; with bf16 tokens the sigmoid is
+ * the special-function unit's (some 4 + |gate| units of 2^-24 relative, results below 2^-126 zero).
  */
 GDN2_API int gdn2_gated_norm_fwd(const void *o, const void *gate, const float *weight, void *y, long long rows, int d_v,
                                  int act, float eps, int dtype, void *stream);

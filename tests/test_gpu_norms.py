@@ -109,6 +109,27 @@ def test_gated_norm_slope_of_wide_open_gates(dtype, d):
     close(dgate, ref, HALF[dtype], np.abs(ref))
 
 
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_gated_norm_in_fp32_is_fp32(d, act):
+    """fp32 rows keep fp32's precision over all gates.  In units of 2^-24: expf 4 (2 ulp), its sum 1, the quotient 1, its
+    product 1; the row's sum of squares at most 4 + 5 roundings and eps 1, halved by the root, rsqrtf 4 (2 ulp); four
+    products, the last the output's rounding: 20.  dgate's product has five factors more for the sigmoid (24 in all); the
+    bar for both is 32."""
+    torch, g = cuda_or_skip()
+    t = _make(torch, d, 603, d, "f32", ("o", "gate", "dy"), ("weight",))
+    t["gate"].copy_(torch.linspace(-80, 80, 603 * d).view(603, d))
+    y = g.gated_norm_fwd(t["o"], t["gate"], t["weight"], act=act)
+    x = {n: f64(a) for n, a in t.items()}
+    ref = op.gated_norm(x["o"], x["gate"], x["weight"], act)
+    assert (np.abs(f64(y) - ref) <= 32 * 2.0 ** -24 * np.abs(ref)).all(), np.max(np.abs(f64(y) / ref - 1)) * 2 ** 24
+    if act == "sigmoid":
+        _, dgate, _ = g.gated_norm_bwd(t["o"], t["gate"], t["weight"], t["dy"], act=act)
+        r = 1 / np.sqrt((x["o"] ** 2).mean(-1, keepdims=True) + EPS)
+        ref = x["dy"] * x["o"] * r * x["weight"] / (1 + np.exp(-x["gate"])) / (1 + np.exp(x["gate"]))
+        assert (np.abs(f64(dgate) - ref) <= 32 * 2.0 ** -24 * np.abs(ref)).all()
+
+
 def test_gated_norm_in_place_shapes_and_empty():
     torch, g = cuda_or_skip()
     t = _make(torch, 6, 60, 128, "bf16", ("o", "gate", "dy"), ("weight",))
