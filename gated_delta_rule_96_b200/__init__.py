@@ -25,7 +25,7 @@ __all__ = [
     "gdn2_gated_norm_fwd", "gdn2_gated_norm_bwd", "gdn2_gated_norm_bwd_workspace_bytes", "gated_norm_fwd",
     "gated_norm_bwd", "gdn2_gated_norm", "gdn2_add_norm_fwd", "gdn2_add_norm_bwd",
     "gdn2_add_norm_bwd_workspace_bytes", "add_norm_fwd", "add_norm_bwd", "gdn2_add_norm", "gdn2_tree_fwd",
-    "tree_fwd", "gdn2_recurrent_fwd", "recurrent_fwd", "gdn2_state_copy", "gdn2_set_wait_limit", "TREE_MAX_NODES",
+    "tree_fwd", "gdn2_recurrent_fwd", "recurrent_fwd", "gdn2_state_copy", "gdn2_set_wait_limit", "gdn2_shared_status", "TREE_MAX_NODES",
     "STATE_COPY_MAX_PAIRS", "DEV_RANGE", "DEV_SLOT", "DEV_PARENT", "DEV_INDEX", "DEV_CONFLICT", "DEV_WAIT",
 ]
 
@@ -453,6 +453,40 @@ def _own_workspace(nbytes, device, stream):
         return new_workspace(nbytes, device)
 
 
+_shared = {}   # device index -> the status workspace of the calls over slots that are given none
+
+
+def _slots_workspace(device, stream):
+    """The workspace of a call over slots that is given none: the device's shared one, which holds status words only and
+    so serves any number of calls at once (gdn2_shared_status reads it).  It is made by the first such call; a call that
+    is being captured into a graph before there is one gets a workspace of its own, the graph's."""
+    if device.type != "cuda":
+        return new_workspace(0, device)   # refused with the tensors that it stands beside
+    import torch
+    index = torch.cuda.current_device() if device.index is None else device.index
+    workspace = _shared.get(index)
+    if workspace is None:
+        with torch.cuda.device(index):
+            if torch.cuda.is_current_stream_capturing():
+                return _own_workspace(0, device, stream)
+            made = torch.cuda.Stream()
+            with torch.cuda.stream(made):
+                workspace = new_workspace(0, device)
+            made.synchronize()   # once: whatever stream uses it finds it zeroed
+        workspace = _shared.setdefault(index, workspace)
+    return workspace
+
+
+def gdn2_shared_status(device=None, clear=True, stream=None) -> int:
+    """Status bits (DEV_*) that the calls over slots without a workspace of their own have reported on a device (the
+    current one), as gdn2_workspace_status reads them: of the calls that have ended by the time `stream` (the current
+    one) has.  0: none."""
+    import torch
+    device = torch.device("cuda" if device is None else device)
+    workspace = _shared.get(torch.cuda.current_device() if device.index is None else device.index)
+    return 0 if workspace is None else gdn2_workspace_status(workspace, clear=clear, stream=stream)
+
+
 def _gated_workspace(o, stream):
     return _own_workspace(gdn2_gated_norm_bwd_workspace_bytes(_rows(o), o.shape[-1]), o.device, stream)
 
@@ -496,10 +530,11 @@ def gdn2_tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, o, max_node
     unchanged (include/gdn2.h, gdn2_tree_fwd).  q, k, b, alpha [total, H, d_k]; v, w, o [total, H, d_v];
     slots [batch], cu_nodes [batch + 1], parents [total] int32 on the device; max_nodes: the most nodes of
     a tree, at most TREE_MAX_NODES.  The slots of S may lie any distance apart (one layer's part of a larger
-    pool).  Malformed indices are reported in the workspace's status."""
+    pool).  A tree with malformed indices is left out: its rows of o stay as they were, and the workspace's status
+    says so (without a workspace gdn2_shared_status does)."""
     _given(o)
     _native().tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, o, max_nodes,
-                       _own_workspace(0, q.device, stream) if workspace is None else workspace, stream)
+                       _slots_workspace(q.device, stream) if workspace is None else workspace, stream)
 
 
 def gdn2_recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index, o, workspace=None,
@@ -507,19 +542,21 @@ def gdn2_recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, 
     """The recurrence over ragged runs of tokens, from slot to slot of the state cache S
     [slots, H, d_k, d_v] (include/gdn2.h, gdn2_recurrent_fwd).  q, k, b, alpha [rows, H, d_k]; v, w
     [rows, H, d_v]; slots_in, slots_out [batch] and cu_tokens [batch + 1] int32 on the device; index [total]
-    int32 or None (entry t is row t); o [total, H, d_v] or None (not wanted).  Malformed indices are reported
-    in the workspace's status."""
+    int32 or None (entry t is row t); o [total, H, d_v] or None (not wanted).  A run with malformed indices is left
+    out: its rows of o and its slots stay as they were, and the workspace's status says so (without a workspace
+    gdn2_shared_status does)."""
     _native().recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index, o, False,
-                            _own_workspace(0, q.device, stream) if workspace is None else workspace, stream)
+                            _slots_workspace(q.device, stream) if workspace is None else workspace, stream)
 
 
 def gdn2_state_copy(dst, src, dst_index, src_index, workspace=None, stream=None) -> None:
     """dst[dst_index[i]] = src[src_index[i]] (-1: zeros) for every pair, as if all sources were read first
     (include/gdn2.h, gdn2_state_copy): fork, compact, reorder and clear slots of a state cache.  dst, src:
     fp32 caches [slots, ...] with equal slot shapes, one cache or two that do not overlap; the indices int32
-    on the device, at most STATE_COPY_MAX_PAIRS."""
+    on the device, at most STATE_COPY_MAX_PAIRS.  A pair with a slot out of range is left out, and the workspace's
+    status says so (without a workspace gdn2_shared_status does)."""
     _native().state_copy(dst, src, dst_index, src_index,
-                         _own_workspace(0, dst.device, stream) if workspace is None else workspace, stream)
+                         _slots_workspace(dst.device, stream) if workspace is None else workspace, stream)
 
 
 def _given(*outputs):
@@ -601,16 +638,18 @@ def add_norm_bwd(h, x, scale, weight, dy, dh=None, eps=1e-6, workspace=None, str
 
 
 def tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, max_nodes, workspace=None, stream=None):
-    """Allocating convenience wrapper of gdn2_tree_fwd: returns o (rows of no tree hold no values)."""
+    """Allocating convenience wrapper of gdn2_tree_fwd: returns o.  Rows of no tree, and of a tree that was left out for
+    its malformed indices (the status of the workspace, or gdn2_shared_status, says so), hold no values."""
     return _native().tree_fwd(q, k, v, alpha, b, w, S, slots, cu_nodes, parents, None, max_nodes,
-                              _own_workspace(0, q.device, stream) if workspace is None else workspace, stream)
+                              _slots_workspace(q.device, stream) if workspace is None else workspace, stream)
 
 
 def recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index=None, workspace=None, stream=None):
-    """Allocating convenience wrapper of gdn2_recurrent_fwd: updates S, returns o by entry (entries of no
-    sequence hold no values)."""
+    """Allocating convenience wrapper of gdn2_recurrent_fwd: updates S, returns o by entry.  Entries of no sequence, and
+    of one that was left out for its malformed indices (the status of the workspace, or gdn2_shared_status, says so),
+    hold no values."""
     return _native().recurrent_fwd(q, k, v, alpha, b, w, S, slots_in, slots_out, cu_tokens, index, None, True,
-                                   _own_workspace(0, q.device, stream) if workspace is None else workspace, stream)
+                                   _slots_workspace(q.device, stream) if workspace is None else workspace, stream)
 
 
 def _recurrence_function():

@@ -568,6 +568,61 @@ def test_calls_on_a_side_stream_allocate_there():
     torch.cuda.synchronize()
 
 
+def test_malformed_indices_without_a_workspace_are_reported():
+    """Calls that are given no workspace report to the device's shared status, on any stream and from a graph, with no
+    allocation of their own."""
+    torch, g = cuda_or_skip()
+    x, pool = tokens(torch, 72, 6, 2, 64, 64, "bf16"), make_pool(torch, 73, 4, 2, 64, 64)
+    good, bad, out, cu = i32(torch, [0, 1]), i32(torch, [0, 4]), i32(torch, [2, 3]), i32(torch, [0, 3, 6])
+    par, wrong, src = i32(torch, [-1, 0, 0] * 2), i32(torch, [-1, 0, 0, -1, 1, 0]), i32(torch, [1, 1])
+    keep, o = pool.clone(), torch.full_like(x[2], float("nan"))
+    g.gdn2_state_copy(pool, pool, out, good)                       # the shared workspace is there from here on
+    g.gdn2_shared_status()
+    assert torch.equal(pool[2:], keep[:2])
+    calls = [(lambda st: g.gdn2_tree_fwd(*x, pool, good, cu, wrong, o, 3, stream=st), g.DEV_PARENT),
+             (lambda st: g.gdn2_tree_fwd(*x, pool, bad, cu, par, o, 3, stream=st), g.DEV_SLOT),
+             (lambda st: g.gdn2_recurrent_fwd(*x, pool, good, bad, cu, None, None, stream=st), g.DEV_SLOT),
+             (lambda st: g.gdn2_state_copy(pool, pool, out, bad, stream=st), g.DEV_SLOT),
+             (lambda st: g.gdn2_state_copy(pool, pool, out, src, stream=st), 0)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call, bits in calls:
+        for st in (None, side):
+            before = torch.cuda.memory_stats()["allocation.all.allocated"]
+            call(st)
+            made = torch.cuda.memory_stats()["allocation.all.allocated"] - before
+            side.synchronize()
+            assert g.gdn2_shared_status(clear=False) == bits and g.gdn2_shared_status("cuda:0") == bits
+            assert g.gdn2_shared_status() == 0 and made == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.tree_fwd(*x, pool, bad, cu, par, 3)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert g.gdn2_shared_status() == g.DEV_SLOT and g.gdn2_shared_status() == 0
+
+
+def test_a_call_captured_before_any_other():
+    """The first call of a process, captured, without a workspace: the graph's own."""
+    torch, g = cuda_or_skip()
+    x, pool = tokens(torch, 74, 3, 2, 64, 64, "bf16"), make_pool(torch, 75, 2, 2, 64, 64)
+    args = i32(torch, [1]), i32(torch, [0, 3]), i32(torch, [-1, 0, 1])
+    want, kept = g.tree_fwd(*x, pool, *args, 3), dict(g._shared)
+    try:
+        g._shared.clear()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            o = g.tree_fwd(*x, pool, *args, 3)
+        assert not g._shared
+        o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want)
+    finally:
+        g._shared.update(kept)
+
+
 def test_calls_behind_one_another_see_what_the_last_one_wrote():
     """Chains of calls with nothing between them, each of which reads what the one before wrote (a launch is prepared
     while that one still runs), against the same calls one at a time; eager and in a graph."""
