@@ -444,13 +444,19 @@ def _rows(t) -> int:
     return t.numel() // t.shape[-1] if t.shape[-1] else 0
 
 
-def _own_workspace(nbytes, device, stream):
-    """A workspace for one call, zeroed on the stream that the call runs on."""
+def _on_stream(stream, make, *args):
+    """A call's own memory, made on the stream that the call runs on."""
     if stream is None:
-        return new_workspace(nbytes, device)
+        return make(*args)
     import torch
     with torch.cuda.stream(stream):
-        return new_workspace(nbytes, device)
+        return make(*args)
+
+
+def _sums_workspace(nbytes, device):
+    """For the norms' gradients: partial sums that are written before they are read, no status word, so nothing to zero."""
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 _shared = {}   # device index -> the status workspace of the calls over slots that are given none
@@ -468,7 +474,7 @@ def _slots_workspace(device, stream):
     if workspace is None:
         with torch.cuda.device(index):
             if torch.cuda.is_current_stream_capturing():
-                return _own_workspace(0, device, stream)
+                return _on_stream(stream, new_workspace, 0, device)
             made = torch.cuda.Stream()
             with torch.cuda.stream(made):
                 workspace = new_workspace(0, device)
@@ -488,11 +494,11 @@ def gdn2_shared_status(device=None, clear=True, stream=None) -> int:
 
 
 def _gated_workspace(o, stream):
-    return _own_workspace(gdn2_gated_norm_bwd_workspace_bytes(_rows(o), o.shape[-1]), o.device, stream)
+    return _on_stream(stream, _sums_workspace, gdn2_gated_norm_bwd_workspace_bytes(_rows(o), o.shape[-1]), o.device)
 
 
 def _add_workspace(h, stream):
-    return _own_workspace(gdn2_add_norm_bwd_workspace_bytes(_rows(h), h.shape[-1]), h.device, stream)
+    return _on_stream(stream, _sums_workspace, gdn2_add_norm_bwd_workspace_bytes(_rows(h), h.shape[-1]), h.device)
 
 
 def gdn2_gated_norm_fwd(o, gate, weight, y, act="silu", eps=1e-6, stream=None) -> None:

@@ -229,6 +229,20 @@ def test_backward_is_deterministic_with_a_shared_workspace():
         assert all(torch.equal(a, b) for a, b in zip(first, again))
 
 
+def test_backward_without_a_workspace_zeroes_nothing(monkeypatch):
+    """The gradients' workspace holds no status: nothing of it is read before it is written, and a call that makes its own
+    launches no memset for it."""
+    torch, g = cuda_or_skip()
+    t = _make(torch, 17, 300, 128, "bf16", ("o", "gate", "dy", "h", "x"), ("weight", "scale"))
+    calls = [lambda ws: g.gated_norm_bwd(t["o"], t["gate"], t["weight"], t["dy"], workspace=ws),
+             lambda ws: g.add_norm_bwd(t["h"], t["x"], t["scale"], t["weight"], t["dy"], workspace=ws)]
+    sizes = g.gdn2_gated_norm_bwd_workspace_bytes(300, 128), g.gdn2_add_norm_bwd_workspace_bytes(300, 128)
+    wants = [call(torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")) for call, n in zip(calls, sizes)]
+    monkeypatch.setattr(g, "new_workspace", None)            # it zeroes the status header
+    for call, want in zip(calls, wants):
+        assert all(torch.equal(a, b) for a, b in zip(call(None), want))
+
+
 def test_autograd_of_both_norms():
     """One block's tail and the next one's head, gradients against fp64 autograd of the same formulas."""
     torch, g = cuda_or_skip()
