@@ -14,6 +14,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgdn2.so")
 TORCH_SOURCE = os.path.join(CSRC, "gdn2_torch.cpp")
 TORCH_LIB = os.path.join(HERE, "_gdn2_torch.so")
+TORCH_STAMP = os.path.join(HERE, "_build", "gdn2_torch.stamp")   # what TORCH_LIB was built against
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -32,6 +33,13 @@ def _stale(out, deps):
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _read(path):
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
@@ -60,13 +68,15 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
 
 
 def build_torch(force: bool = False, verbose: bool = False) -> str:
-    """The native half of the binding, against the installed torch; it loads libgdn2.so at run time."""
-    if not force and not _stale(TORCH_LIB, [TORCH_SOURCE, os.path.join(INCLUDE, "gdn2.h")]):
-        return TORCH_LIB
+    """The native half of the binding, against the installed torch; it loads libgdn2.so at run time.  Built anew when its
+    sources have changed, or the torch or Python that it was built against."""
     import shutil
     import sysconfig
 
     import torch
+    against = f"torch {torch.__version__} {os.path.dirname(torch.__file__)}, python {sys.version}\n"
+    if not force and not _stale(TORCH_LIB, [TORCH_SOURCE, os.path.join(INCLUDE, "gdn2.h")]) and _read(TORCH_STAMP) == against:
+        return TORCH_LIB
     root = os.path.dirname(torch.__file__)
     nvcc = shutil.which(os.environ.get("NVCC", "nvcc")) or "/usr/local/cuda/bin/nvcc"
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
@@ -81,6 +91,9 @@ def build_torch(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
     os.replace(tmp, TORCH_LIB)
+    os.makedirs(os.path.dirname(TORCH_STAMP), exist_ok=True)
+    with open(TORCH_STAMP, "w") as f:
+        f.write(against)
     return TORCH_LIB
 
 

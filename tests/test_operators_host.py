@@ -226,3 +226,39 @@ def test_cpu_tensors_are_refused():
     i = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ValueError):
         g.gdn2_state_copy(x, x, i, i)
+
+
+def test_native_half_is_rebuilt_when_it_has_to_be(monkeypatch, tmp_path):
+    """For a newer source, another torch or another Python; not otherwise."""
+    import os
+    import sys
+
+    from gated_delta_rule_96_b200 import build
+    source, made = tmp_path / "gdn2_torch.cpp", []
+    source.write_text("")
+    os.utime(source, (1, 1))
+    monkeypatch.setattr(build, "TORCH_SOURCE", str(source))
+    monkeypatch.setattr(build, "INCLUDE", str(tmp_path))
+    (tmp_path / "gdn2.h").write_text("")
+    os.utime(tmp_path / "gdn2.h", (1, 1))
+    monkeypatch.setattr(build, "TORCH_LIB", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(build, "TORCH_STAMP", str(tmp_path / "made" / "stamp"), raising=False)
+
+    def compile_(cmd):
+        made.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w"):
+            pass
+    monkeypatch.setattr(build.subprocess, "check_call", compile_)
+
+    def built():
+        made.clear()
+        assert build.build_torch() == build.TORCH_LIB and os.path.exists(build.TORCH_LIB)
+        return len(made)
+    assert built() == 1 and built() == 0
+    monkeypatch.setattr(torch, "__version__", "99.0")
+    assert built() == 1 and built() == 0
+    monkeypatch.setattr(sys, "version", "another one")
+    assert built() == 1 and built() == 0
+    os.utime(source)
+    os.utime(build.TORCH_LIB, (2, 2))
+    assert built() == 1 and built() == 0
