@@ -66,6 +66,17 @@ def test_gated_norm(dtype, rows, d, act):
     check_gated(g, torch, t, act, dtype)
 
 
+@pytest.mark.parametrize("dtype,d,rows", [("bf16", 128, 18943), ("bf16", 128, 18944), ("bf16", 128, 18977),
+                                          ("bf16", 64, 37887), ("bf16", 64, 37888), ("bf16", 64, 37901),
+                                          ("f32", 128, 9471), ("f32", 128, 9472), ("f32", 128, 9475),
+                                          ("f32", 64, 18943), ("f32", 64, 18944), ("f32", 64, 18951)])
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+def test_gated_norm_of_many_rows(dtype, d, rows, act):
+    """Both sides of the row counts from which a forward thread has four rows, with and without a remainder."""
+    torch, g = cuda_or_skip()
+    check_gated(g, torch, _make(torch, rows, rows, d, dtype, ("o", "gate", "dy"), ("weight",)), act, dtype)
+
+
 def test_gated_norm_rows_of_zeros_and_wide_gates():
     torch, g = cuda_or_skip()
     t = _make(torch, 5, 6, 128, "f32", ("o", "gate", "dy"), ("weight",))
@@ -201,6 +212,18 @@ def test_add_norm_rows_that_share_a_block(dtype, rows, width):
     y, h = g.add_norm_fwd(t["x"], t["residual"], t["scale"], t["weight"])
     small, none = (g.add_norm_bwd(h, t["x"], t["scale"], t["weight"], t["dy"], t["dh"], eps=eps) for eps in (1e-20, 0.0))
     assert all(torch.equal(a, b) and torch.isfinite(a.float()).all() for a, b in zip(small, none))
+
+
+@pytest.mark.parametrize("dtype,rows,width", [("bf16", 40003, 64), ("bf16", 20011, 128), ("bf16", 30001, 72),
+                                              ("bf16", 9999, 208), ("f32", 40003, 32), ("f32", 20011, 64), ("f32", 5003, 264)])
+@pytest.mark.parametrize("scale", [True, False])
+def test_add_norm_of_more_rows_than_the_blocks_take_at_once(dtype, rows, width, scale):
+    """The backward's blocks (at most 592, of up to 32 rows) walk on to further rows and carry the columns' sums: along a
+    sum's longest chain here 3 rows of a thread, 31 of the block's others, 18 blocks of a group and 5 steps of the last
+    sum, 57 additions of the 64 that the tolerance for sums counts."""
+    torch, g = cuda_or_skip()
+    t = _make(torch, rows, rows, width, dtype, ("x", "residual", "dy", "dh"), ("scale", "weight"))
+    check_add(g, torch, t, dtype, scale=scale)
 
 
 def test_add_norm_in_place_and_empty():
