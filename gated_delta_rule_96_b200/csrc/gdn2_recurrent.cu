@@ -266,6 +266,38 @@ struct Shared {
 template <int K, int V>
 constexpr size_t smem_bytes(int cols) { return sizeof(Shared<K, V>) + (cols < V ? 0 : sizeof(float) * (size_t)DEPTH * K * V); }
 
+// Conflicts between sequences.  Below TABLE_BATCH sequences the scout compares an item's destination with every sequence's
+// slots, an item ahead; for more of them that takes longer than the item, and for all items it grows with the square.
+// From there on a CTA first marks the slots of the call in two bit maps of up to MAX_BUCKETS (slots a multiple of that
+// apart share a place): touched, and touched by more than one sequence; only what stands in the second is compared.
+// Runs of one token, H16, us without / with: B16 d128 9 / 10, d64 5 / 6; B128 50 / 49, 17 / 15; B256 94 / 90, 38 / 31;
+// B1024 577 / 335, 270 / 106; B4096 7,300 / 1,313, 3,075 / 407; B16384 354,000 / 5,233, 76,700 / 1,608.
+constexpr int TABLE_BATCH = 128, MAX_BUCKETS = 1 << 17;
+constexpr size_t table_bytes(int buckets) { return (size_t)buckets / 4; }
+
+__device__ __forceinline__ bool by_more(const uint32_t *table, int buckets, int slot) {
+    const uint32_t at = (uint32_t)slot % (uint32_t)buckets;
+    return table[(buckets + at) >> 5] >> (at & 31) & 1u;
+}
+// By the whole block, before anything else and as a call of its own: inlined, or further down, it made the kernel spill in
+// its loops (accepted paths 43 -> 50 us).
+__device__ __noinline__ void mark_slots(uint32_t *table, int buckets, const int *slots_in, const int *slots_out, int batch,
+                                           int num_slots) {
+    const auto mark = [&](int slot) {
+        if (slot < 0 || slot >= num_slots) return;
+        const uint32_t at = (uint32_t)slot % (uint32_t)buckets, bit = 1u << (at & 31);
+        if (atomicOr(table + (at >> 5), bit) & bit) atomicOr(table + ((buckets + at) >> 5), bit);
+    };
+    for (int i = threadIdx.x; i < buckets / 16; i += blockDim.x) table[i] = 0u;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < batch; i += blockDim.x) {
+        const int from = slots_in[i], to = slots_out[i];
+        mark(to);
+        if (from != to) mark(from);
+    }
+}
+
 // warps: consumers (16 columns each), PRODUCERS, scout, storer
 template <int K, int V>
 constexpr int EXTRA_WARPS = PRODUCERS<K, V> + 2;
@@ -276,11 +308,16 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
     const Tok *__restrict__ b, const Tok *__restrict__ w, float *S, long long slot_stride, int num_slots,
     const int *__restrict__ slots_in, const int *__restrict__ slots_out, const int *__restrict__ cu,
     const int *__restrict__ index, Tok *__restrict__ o, int batch, int H, int splits, int total, int rows,
-    uint32_t limit, unsigned *status) {
+    int buckets, uint32_t limit, unsigned *status) {
     constexpr int RJ = K / 32, NP = PRODUCERS<K, V>;
     // a producer waits for a ring slot's last use by its parity: it must not be two uses ahead of the consumers
     static_assert(RING >= NP, "each producer's blocks are NP apart");
     extern __shared__ __align__(128) unsigned char raw[];
+    if (buckets) {
+        behind_last_kernel();
+        mark_slots(reinterpret_cast<uint32_t *>(raw + smem_bytes<K, V>(V >> (__ffs(splits) - 1))), buckets, slots_in, slots_out,
+                   batch, num_slots);
+    }
     Shared<K, V> &sh = *reinterpret_cast<Shared<K, V> *>(raw);
     float *buffers = reinterpret_cast<float *>(raw + sizeof(Shared<K, V>));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -317,6 +354,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
     };
 
     if (warp == consumers + NP) {   // scout
+        const uint32_t *table = reinterpret_cast<const uint32_t *>(raw + smem_bytes<K, V>(cols));
         auto look = [&](long long at) {
             const long long chain = at >> split_bits;
             const int seq = (int)(chain / H), hi = cu[seq + 1], head = (int)(chain - (long long)seq * H);
@@ -325,7 +363,7 @@ __global__ void __launch_bounds__(2 * V + 32 * EXTRA_WARPS<K, V>) recurrent_kern
             if (x.lo < 0 || hi < x.lo || hi > total) bad = DEV_RANGE;
             else if (x.from < -1 || x.from >= num_slots || x.to < -1 || x.to >= num_slots) bad = DEV_SLOT;
             else {
-                if (x.to >= 0)
+                if (x.to >= 0 && (!buckets || by_more(table, buckets, x.to)))
 #pragma unroll 4
                     for (int i = lane; i < batch; i += 32)
                         if (i != seq && (slots_out[i] == x.to || slots_in[i] == x.to)) bad |= DEV_CONFLICT;
@@ -453,7 +491,7 @@ int launch_out(const void *q, const void *k, const void *v, const float *alpha, 
     constexpr size_t most = smem_bytes<K, V>(V);
     constexpr int threads = 2 * V + 32 * EXTRA_WARPS<K, V>;
     static std::atomic<int> resident{0};   // CTAs an SM; the same on every B200
-    if (!allow_smem(kern, most)) return -6;
+    if (!allow_smem(kern, most + table_bytes(MAX_BUCKETS))) return -6;
     int per_sm = resident.load();
     if (per_sm == 0) {
         if (!succeeded(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, most)) || per_sm < 1) return -6;
@@ -463,10 +501,11 @@ int launch_out(const void *q, const void *k, const void *v, const float *alpha, 
     int splits = 1;
     while (splits < V / 16 && (long long)batch * H * splits * 2 <= 148) splits *= 2;
     const long long items = (long long)batch * H * splits, grid = items < 148 * per_sm ? items : 148 * per_sm;
+    const int buckets = batch < TABLE_BATCH ? 0 : num_slots < MAX_BUCKETS ? (num_slots + 63) / 64 * 64 : MAX_BUCKETS;
     const long long polls = (long long)WAIT_LIMIT + (long long)WAIT_TOKEN * total;
-    return launch_close(kern, (unsigned)grid, 2 * V / splits + 32 * EXTRA_WARPS<K, V>, smem_bytes<K, V>(V / splits), st,
+    return launch_close(kern, (unsigned)grid, 2 * V / splits + 32 * EXTRA_WARPS<K, V>, smem_bytes<K, V>(V / splits) + table_bytes(buckets), st,
                         (const Tok *)q, (const Tok *)k, (const Tok *)v, alpha, (const Tok *)b, (const Tok *)w, S, slot_stride,
-                        num_slots, slots_in, slots_out, cu, index, (Tok *)o, batch, H, splits, total, rows,
+                        num_slots, slots_in, slots_out, cu, index, (Tok *)o, batch, H, splits, total, rows, buckets,
                         wait_limit(polls < 0xffffffffll ? (uint32_t)polls : 0xffffffffu), status);
 }
 

@@ -355,6 +355,64 @@ def test_recurrent_runs_of_any_length():
     assert torch.isfinite(o).all() and o.abs().max() > 0
 
 
+@pytest.mark.parametrize("B,slots", [(127, 400), (128, 400), (1000, 2600), (4100, 140000)])
+def test_recurrent_conflicts_of_large_batches(B, slots):
+    """Whatever finds them, and however many slots lie between: writers of one slot, writers of what another one reads, and
+    updates in place whose slot another one reads are left out; shared sources, slots out of range, slots that differ by
+    the size of a table, and sequences without a slot are no conflict."""
+    torch, g = cuda_or_skip()
+    rng = np.random.default_rng(B)
+    p = rng.permutation(slots - 8)
+    src, dst = p[:B].copy(), p[B:2 * B].copy()
+    far = 1 << 17
+    if slots > far + 8:
+        at = np.flatnonzero(p[:2 * B] < slots - 8 - far)[:40]         # the same place, another slot
+        both = np.concatenate([src, dst])
+        for i, j in zip(at[::2], at[1::2]):
+            if both[i] + far not in both:
+                both[j] = both[i] + far
+        src, dst = both[:B], both[B:]
+    dst[0::9] = src[0::9]                                              # in place
+    dst[1::9], src[2::9] = -1, -1
+    src[3:12:9] = src[4]                                               # a source for several
+    dst[22] = dst[23]                                                  # two writers
+    dst[31] = src[33]                                                  # a writer of what 33 reads
+    src[42] = dst[45]                                                  # 45 in place, read by 42
+    dst[51] = src[51] = slots                                          # out of range, with the next line's reader
+    src[52] = slots + 1
+    dst[60] = src[61] = -1
+    touch = {}
+    for i in range(B):
+        for s in {int(src[i]), int(dst[i])}:
+            touch.setdefault(s, []).append(i)
+    bad_slot = [i for i in range(B) if not (-1 <= src[i] < slots and -1 <= dst[i] < slots)]
+    out = [i for i in range(B) if dst[i] >= 0 and i not in bad_slot and touch[int(dst[i])] != [i]]
+    assert {22, 23, 31, 45} <= set(out)
+    out += bad_slot
+    x = tokens(torch, B, B, 1, 64, 64, "f32")
+    pool = torch.randn(slots, 1, 64, 64, generator=torch.Generator("cuda").manual_seed(B), device="cuda")
+    used = sorted({int(s) for s in np.concatenate([src, dst]) if 0 <= s < slots})
+    row = {s: i for i, s in enumerate(used)}
+    to_row = lambda a: [row.get(int(s), -1) for s in a]  # noqa: E731
+    keep = pool[used].clone()
+    kept_dst = dst.copy()
+    kept_dst[out] = -1
+    ref, after = op.recurrent(*(f64(a) for a in x), f64(keep), to_row(src), to_row(kept_dst), range(B + 1))
+    o, ws = torch.full_like(x[2], float("nan")), g.new_workspace(0)
+    total = pool.double().sum().item() - keep.double().sum().item()
+    g.gdn2_recurrent_fwd(*x, pool, i32(torch, src.tolist()), i32(torch, dst.tolist()), i32(torch, range(B + 1)), None, o, workspace=ws)
+    assert g.gdn2_workspace_status(ws) == g.DEV_CONFLICT | g.DEV_SLOT
+    well = [i for i in range(B) if i not in set(out)]
+    close(o[well], ref[well], "f32")
+    assert torch.isnan(o[out]).all()
+    close(pool[used], after, "f32")
+    written = {row[int(s)] for s in kept_dst if s >= 0}
+    idle = [i for i in range(len(used)) if i not in written]
+    assert torch.equal(pool[used][idle], keep[idle])
+    pool[used] = 0.0
+    assert abs(pool.double().sum().item() - total) <= 1e-6 * max(1.0, abs(total))      # no other slot was touched
+
+
 def test_recurrent_reports_malformed_indices_and_conflicts():
     torch, g = cuda_or_skip()
     H, n = 2, 3
