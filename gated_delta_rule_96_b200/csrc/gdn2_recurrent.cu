@@ -45,9 +45,10 @@ template <int K, int V>
 constexpr int PRODUCERS = K == 128 && V == 128 ? 2 : 4;
 constexpr int DEPTH = 2;       // state buffers: one worked on, one on its way in or out
 constexpr int RING = 6;        // token blocks ahead
-// Polls: a second or more.  The storer and the scout wait for a whole run, up to 0.8 us a token: some 32 polls of the
-// shortest kind a token are added.
-constexpr uint32_t WAIT_LIMIT = 1u << 21, WAIT_TOKEN = 32;
+// Limits of the waits, in polls.  A poll that finds nothing sleeps for some 4 us (runs of 20,000 and 100,000 tokens), so
+// WAIT_LIMIT is 8 s.  The storer and the scout wait for a whole run, measured 0.13 to 0.4 us a token: 4 polls a token,
+// 16 us, are added for it.
+constexpr uint32_t WAIT_LIMIT = 1u << 21, WAIT_TOKEN = 4;
 
 template <int K, int V>
 struct Block {

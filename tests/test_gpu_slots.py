@@ -413,6 +413,19 @@ def test_recurrent_conflicts_of_large_batches(B, slots):
     assert abs(pool.double().sum().item() - total) <= 1e-6 * max(1.0, abs(total))      # no other slot was touched
 
 
+def test_recurrent_waits_for_long_runs_with_a_margin(wait_limit):
+    """A poll a token, a quarter of what is added for a run's length, and nothing beside it, is enough for a long run."""
+    torch, g = cuda_or_skip()
+    n = 100000
+    gen = torch.Generator("cuda").manual_seed(2)
+    r = lambda: torch.randn(n, 1, 64, generator=gen, device="cuda")  # noqa: E731
+    x = [0.1 * r(), 0.1 * r(), r(), torch.sigmoid(r() + 2), torch.sigmoid(r()), torch.sigmoid(r())]
+    pool, ws = make_pool(torch, 1, 1, 1, 64, 64), g.new_workspace(0)
+    wait_limit(n)
+    o = g.recurrent_fwd(*x, pool, i32(torch, [0]), i32(torch, [0]), i32(torch, [0, n]), workspace=ws)
+    assert g.gdn2_workspace_status(ws) == 0 and torch.isfinite(o).all()
+
+
 def test_recurrent_reports_malformed_indices_and_conflicts():
     torch, g = cuda_or_skip()
     H, n = 2, 3
