@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q,
                 *reinterpret_cast<float4 *>(se + at) = make_float4(bb[0] * kk[0] * g0.x, bb[1] * kk[1] * g0.y,
                                                                    bb[2] * kk[2] * g1.x, bb[3] * kk[3] * g1.y);
                 *reinterpret_cast<float4 *>(sq + at) = make_float4(qq[0] * g0.x, qq[1] * g0.y, qq[2] * g1.x, qq[3] * g1.y);
+                // used where G is in range only: two units in the last place there, as the products' own roundings together
                 *reinterpret_cast<float4 *>(sk + at) =
                     make_float4(__fdividef(kk[0], g0.x), __fdividef(kk[1], g0.y), __fdividef(kk[2], g1.x), __fdividef(kk[3], g1.y));
             }

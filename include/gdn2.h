@@ -228,8 +228,17 @@ GDN2_API int gdn2_add_norm_bwd(const void *h, const void *x, const float *scale,
  *   max_nodes  the most nodes of a tree, at most GDN2_TREE_MAX_NODES
  *
  * A node reads only itself and its ancestors: values of other branches, NaN included, do not reach
- * it.  Any decay is exact, zero included.  o must not alias an input.  batch at most 65,535.  An accepted path is taken into the
- * cache by gdn2_recurrent_fwd with the path's nodes as `index`.
+ * it.  Any decay is served, zero included (the products of decays along a path are fp32: half a unit
+ * of 2^-23 a node).  o must not alias an input.  batch at most 65,535.  An accepted path is taken into
+ * the cache by gdn2_recurrent_fwd with the path's nodes as `index`.
+ *
+ * Arithmetic: fp32, o rounded once.  With bf16 tokens and d_k = d_v = 128, calls with max_nodes above
+ * a limit (40 for up to 16 (sequence, head) pairs, 20 to 32, 15 to 64, 9 to 148, else 7) run on the
+ * tensor cores, which take no fp32: there the state, the decayed b k and q and k over its decays enter
+ * their products as sums of two bf16 (17 bits of 24; the accumulation is fp32).  That puts o some 4e-6
+ * of its norm off before its rounding, whose own 1.7e-3 it leaves as it is: one bf16 value in 240 is
+ * rounded the other way.  An infinity in a state or a token gives NaN there where fp32 may keep it.
+ * Calls with fp32 tokens, or other d_k and d_v, are fp32 throughout.
  */
 #define GDN2_TREE_MAX_NODES 64
 GDN2_API int gdn2_tree_fwd(const void *q, const void *k, const void *v, const float *alpha, const void *b,
