@@ -740,6 +740,74 @@ def test_calls_behind_one_another_see_what_the_last_one_wrote():
     assert g.gdn2_workspace_status(ws) == 0
 
 
+def test_every_input_may_be_what_the_kernel_before_wrote():
+    """Tokens, weights, slots, counts, parents and indices, all of them written by the call right before (a copy of a large
+    slot that ends with them), with nothing between: each call reads this round's, not the round's before."""
+    torch, g = cuda_or_skip()
+    floats = 1 << 24
+    pool = torch.zeros(3, floats, device="cuda")                   # two rounds' inputs, and where the calls read them
+    at = [floats]
+
+    def place(*pair):
+        """Two rounds' values of one input, at the slots' end; the input itself."""
+        first, size = pair[0], pair[0].numel()
+        at[0] -= -(-size * first.element_size() // 16) * 4
+        views = [pool[i, at[0]:].view(first.dtype)[:size].view(first.shape) for i in range(3)]
+        for view, value in zip(views, pair):
+            view.copy_(value)
+        return views[2]
+
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    H, n = 3, 44
+    args = {}
+    for few in (12, n):                                            # trees of both kernels
+        rounds = [tokens(torch, 80 + few + i, few, H, 128, 128, "bf16") for i in range(2)]
+        trees = [ints(*random_tree(np.random.default_rng(i), few - 4, 6), -1, 0, 0, 1) for i in range(2)]
+        args[few] = dict(x=[place(a, b) for a, b in zip(*rounds)], parents=place(*trees),
+                         cu=place(ints(0, few - 4, few), ints(0, few - 4, few - 1)), slots=place(ints(0, 1), ints(1, 0)),
+                         index=place(*(torch.randperm(few, generator=torch.Generator().manual_seed(i)).int() for i in range(2))))
+    half = lambda seed, *shape: torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).bfloat16()  # noqa: E731
+    rows = [place(half(i, 40, 128), half(100 + i, 40, 128)) for i in range(4)]
+    weight, scale = (place(torch.rand(128), torch.rand(128) + 1) for _ in range(2))
+    to, frm = place(ints(2, 3), ints(3, 2)), place(ints(0, 1), ints(1, -1))
+    states, out = make_pool(torch, 90, 4, H, 128, 128), ints(2, 3).cuda()
+    ws, big = g.new_workspace(0), torch.empty(g.gdn2_add_norm_bwd_workspace_bytes(40, 128), dtype=torch.uint8, device="cuda")
+
+    def recurrent(a):
+        p = states.clone()
+        return lambda: (g.recurrent_fwd(*a["x"], p, a["slots"], out, a["cu"], index=a["index"], workspace=ws), p)
+
+    def copies():
+        p = states.clone()
+        return lambda: (g.gdn2_state_copy(p, p, to, frm, workspace=ws), p)[1:]
+    calls = [lambda: lambda: g.gated_norm_fwd(rows[0], rows[1], weight),
+             lambda: lambda: g.gated_norm_bwd(rows[0], rows[1], weight, rows[2], workspace=big),
+             lambda: lambda: g.add_norm_fwd(rows[0], rows[1], scale, weight),
+             lambda: lambda: g.add_norm_bwd(rows[0], rows[1], scale, weight, rows[2], rows[3], workspace=big),
+             lambda: lambda: g.tree_fwd(*args[12]["x"], states, args[12]["slots"], args[12]["cu"], args[12]["parents"], 8, workspace=ws),
+             lambda: lambda: g.tree_fwd(*args[n]["x"], states, args[n]["slots"], args[n]["cu"], args[n]["parents"], 44, workspace=ws),
+             lambda: recurrent(args[n]), copies]
+    source, target = [ints(i).cuda() for i in range(2)], ints(2).cuda()
+    flat = lambda r: [r] if torch.is_tensor(r) else list(r)  # noqa: E731
+    for which, call in enumerate(calls):
+        want = []
+        for i in range(2):
+            g.gdn2_state_copy(pool, pool, target, source[i], workspace=ws)
+            torch.cuda.synchronize()
+            want.append([a.clone() for a in flat(call()())])
+            torch.cuda.synchronize()
+        assert not all(torch.equal(a, b) for a, b in zip(*want))
+        for turn in range(40):
+            ready = call()                                         # what it copies it copies before
+            g.gdn2_state_copy(pool, pool, target, source[turn % 2], workspace=ws)
+            got = flat(ready())
+            for a, b in zip(got, want[turn % 2]):
+                if a.shape[0] in (12, n):                          # the second round has one token fewer
+                    a, b = a[:a.shape[0] - turn % 2], b[:b.shape[0] - turn % 2]
+                assert torch.equal(a, b), (which, turn)
+    assert g.gdn2_workspace_status(ws) == 0
+
+
 def test_a_launch_that_fails_leaves_no_error_behind():
     """A launch on the legacy default stream is refused while a blocking stream is being captured.  The call says so, and
     the next call, of any kind, does not report it again."""
