@@ -6,10 +6,12 @@
 // for the state and the tokens from five nodes on.  Both factors are split into two bf16, x = hi + lo (16
 // significant bits, relative error 2^-17): three tcgen05 products hi hi + hi lo + lo hi keep the error far
 // below the rounding of the bf16 output, where one product of bf16 operands would double that rounding.  Of trees of 64
-// nodes o is 4e-6 of its norm off before that rounding (1.66e-3; the fp32 kernel: 1e-7), 4e-6 by the couplings and 4e-7
-// by the products with the state; against fp64 its error is 1.658282e-3 where plain fp32's is 1.658276e-3.  The lo lo
-// products would take a fifth off the 4e-6.  Three bf16 would end it, but the third images of 48 KB do not fit beside the
-// others, and couplings on CUDA cores take a third more time.
+// nodes o is 2e-6 of its norm off before that rounding (1.66e-3; the fp32 kernel: 1e-7), nearly all of it by the couplings
+// and 4e-7 by the products with the state; against fp64 its error is 1.658277e-3 where plain fp32's is 1.658276e-3.
+// (4e-6 while P of a node with itself, which has no decay in it, was a product of those two as well, in place of q k in
+// fp32: 134 us for the full batch, 136 now.  The parent's couplings in fp32 too would leave 6e-7, for 145 to 148 us.  Slow
+// decays keep 4e-6, distant couplings then counting like near ones.  The lo lo products would take a fifth off.  Three bf16
+// would end it, but their images, 48 KB more, do not fit beside the others; couplings on CUDA cores take a third more time.)
 //   state group  (4 warps)  a column of S a thread, split, into tensor memory: the A operand S^T, lane = value
 //                           column, two buffers
 //   path group   (8 warps)  G, a channel a thread from parents to children; then, eight lanes a node, the rows
@@ -57,6 +59,7 @@ struct TcShared {
     float r[MAX_NODES][D], x[MAX_NODES][D];   // u, then R; S^T (q G); by node and value column
     float a[MAX_PAIRS], c[2][MAX_PAIRS];      // A; P, then C
     Meta meta[METAS];
+    float own[2][MAX_NODES];                  // P of a node with itself, q k
     unsigned long long path[MAX_NODES];       // a bit for each node on a node's path
     unsigned long long meta_known[METAS], meta_full[METAS], meta_free[METAS], s_full[2], s_free[2], coef_full[2], coef_free[2], b_full, b_free,
         d_full, d_free, p_full, p_free;
@@ -415,6 +418,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                     const bool good = in_range<D>(G, lane);
                     if (!go) continue;
                     if (sub == 0) m.fine[node] = good;
+                    f32x2 own = 0ull;   // one accumulator: two made it spill (full batch 136 -> 140 us)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int at = 8 * sub + 64 * j;
@@ -435,6 +439,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                         put(sh.b_hi, sh.b_lo, sw_off(node, at, 2 * MAX_NODES), x);
                         rq[j].get(y);
 #pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            own = fma2(pack2(y[2 * i], y[2 * i + 1]), pack2(kk[2 * i], kk[2 * i + 1]), own);
+#pragma unroll
                         for (int i = 0; i < 4; ++i) x[i] = mul2(pack2(y[2 * i], y[2 * i + 1]), G[2 * j + (i >> 1)][i & 1]);
                         put(sh.b_hi, sh.b_lo, sw_off(rows + node, at, 2 * MAX_NODES), x);
 #pragma unroll
@@ -444,6 +451,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                         }
                         put(sh.k_hi, sh.k_lo, sw_off(node, at, MAX_NODES), x);
                     }
+                    const float2 both = unpack2(own);
+                    float sum = both.x + both.y;
+#pragma unroll
+                    for (int h = 4; h > 0; h >>= 1) sum += __shfl_xor_sync(0xffu << (lane & 24), sum, h);
+                    if (sub == 0) sh.own[c & 1][node] = sum;
                 }
                 fence_async_smem();
                 arrive(sh.b_full);
@@ -481,7 +493,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                     uint32_t y[32];
                     tmem_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + TM_P + i0, y);
                     const unsigned long long path = who < n ? sh.path[who] : 0ull;
-                    const uint32_t mine = path & ~fine ? 0u : (uint32_t)(path >> i0);
+                    const uint32_t mine = path & ~fine ? 0u : (uint32_t)((path & ~(1ull << (who & 63))) >> i0);
                     float *to = (line < rows ? sh.a : coef) + (who < n ? pairs(who) + m.above[who] : 0);
                     wait_ld();
 #pragma unroll
@@ -493,6 +505,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                         if (mine >> (i + 3) & 1) to[-a4.w] = __uint_as_float(y[i + 3]);
                     }
                 }
+                if (t < n) coef[pairs(t)] = sh.own[c & 1][t];
                 fence_before();
                 arrive(sh.p_free);
                 // the others from the tokens

@@ -235,9 +235,9 @@ GDN2_API int gdn2_add_norm_bwd(const void *h, const void *x, const float *scale,
  * Arithmetic: fp32, o rounded once.  With bf16 tokens and d_k = d_v = 128, calls with max_nodes above
  * a limit (40 for up to 16 (sequence, head) pairs, 20 to 32, 15 to 64, 9 to 148, else 7) run on the
  * tensor cores, which take no fp32: there the state, the decayed b k and q and k over its decays enter
- * their products as sums of two bf16 (17 bits of 24; the accumulation is fp32).  That puts o some 4e-6
- * of its norm off before its rounding, whose own 1.7e-3 it leaves as it is: one bf16 value in 240 is
- * rounded the other way.  An infinity in a state or a token gives NaN there where fp32 may keep it.
+ * their products as sums of two bf16 (17 bits of 24; the accumulation is fp32).  That puts o some 2e-6
+ * of its norm off before its rounding (4e-6 where decays are slow), whose own 1.7e-3 it leaves as it
+ * is: one bf16 value in some hundreds is rounded the other way.  An infinity in a state or a token gives NaN there where fp32 may keep it.
  * Calls with fp32 tokens, or other d_k and d_v, are fp32 throughout.
  */
 #define GDN2_TREE_MAX_NODES 64

@@ -110,6 +110,23 @@ def test_tree_many_items(seed):
     close(o[kept], ref[kept], "bf16")
 
 
+@pytest.mark.parametrize("items", [(1, 4), (8, 16)])
+def test_tree_values_that_round_the_other_way(items):
+    """What splitting the tensor cores' factors leaves of fp32 before o is rounded, on both kernels: an error of e of o's
+    norm moves a value over a rounding border in proportion to e.  The couplings' split factors (2^-18 and 2^-18, rms a
+    third of it, over 128 terms) would put o 4e-6 off and round one value in 240 the other way; with the largest, a node's
+    own, in fp32 what is left is 2e-6, and the bar is one in 330.  fp32 is 1e-7 off: one in 10,000, bar 2,000."""
+    torch, g = cuda_or_skip()
+    batch, H = items
+    n = 64 if batch > 1 else 32                   # 32 nodes of 4 items: CUDA cores
+    x, pool = tokens(torch, 97, batch * n, H, 128, 128, "bf16"), make_pool(torch, 98, batch, H, 128, 128) / 2
+    parents = sum((random_tree(np.random.default_rng(i), n, 12) for i in range(batch)), [])
+    o, ref, _, status = run_tree(torch, g, x, pool, range(batch), [n] * batch, parents)
+    assert status == 0
+    other = (o.cpu() != torch.from_numpy(ref).bfloat16()).double().mean().item()
+    assert other <= (1 / 330 if batch > 1 else 1 / 2000), 1 / other
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shape", ["chain", "star", "roots", "twos"])
 @pytest.mark.parametrize("n", [6, 64])
