@@ -11,9 +11,10 @@
 // row sums are fp32 shuffles (and one exchange through shared memory where a row spans warps), and every
 // output is rounded once.  The column sums are fp32 per thread over the rows that it walks, then added in
 // a fixed order (per block, then over the blocks by a second kernel), so results do not change from run
-// to run.  HBM bounds them all: gated norm of 524,288 rows of 128 bf16, forward 66 us (6.1 TB/s of 6.5 that a copy
-// reaches), backward 117 us (5.7); residual norm of 32,768 rows of 2,048, forward 88 us (6.1), backward 143 us (5.6);
-// the sum over the blocks 3-4 us.  A few rows (a decode step) take 3 us, latency alone.
+// to run.  HBM bounds them all.  One call behind another, gated norm of 524,288 rows of 128 bf16: forward 64 us (6.3 TB/s of the
+// 6.5 that a copy reaches), backward 113 us (5.9).  A single launch's device time is shorter, 61 and 109 us, since its last
+// writes are still in L2 when it ends; so measured the residual norm of 32,768 rows of 2,048 takes 79 us forward and 139
+// backward, the sum over the blocks 5-7 us, and a few rows (a decode step) 3-4 us, latency alone.
 #include "gdn2_common.cuh"
 #include "gdn2_internal.h"
 

@@ -21,12 +21,12 @@
 //   consumers  state to registers, the blocks, state back to the buffer;
 //   storer     has a bulk copy take the buffer to the slot, and frees it once it has been read.
 // Where a head's columns are split over CTAs (few chains), the consumers move their own part of the state.
-// A decode step (one token, 128 KB moved for 0.1 MFMA a head) is then bound by HBM: B256 H16 d128 takes 94 us, 5.8
+// A decode step (one token, 128 KB moved for 0.1 MFMA a head) is then bound by HBM: B256 H16 d128 takes 90 us, 6.0
 // of the 6.5 TB/s that a plain copy reaches; with the state loaded to registers by two CTAs an SM, which each
-// waited for every latency in turn, it took 166.  Accepted paths (B64 H16 d128, up to 9 tokens) take 42 us, twice
+// waited for every latency in turn, it took 166.  Accepted paths (B64 H16 d128, up to 9 tokens) take 43 us, twice
 // their 145 MB: there it is the consumers, 3,200 cycles for a block of four tokens, as many issue slots for LDS as for
 // FMA, and 2,500 to move a state between shared memory and registers.  fp32 runs of up to 201 tokens (B8 H16 d64) take
-// 44 us, the longest chain's 1,400 cycles a block, one after the other.
+// 46 us, the longest chain's 1,400 cycles a block, one after the other (d128, in bf16 and in fp32: 99 us).
 #include <atomic>
 
 #include "gdn2_internal.h"

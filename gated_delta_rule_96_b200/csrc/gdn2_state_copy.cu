@@ -12,8 +12,10 @@
 // - A slot that changes is read too (a reorder in place): a block owns a position range in every slot at
 //   once, as much of it as shared memory holds of all pairs, and writes once all of it has landed.  No other
 //   block touches the range, so any permutation needs no order among the pairs.
-// The compaction runs at 5.6 TB/s of the 6.5 that a plain copy reaches; a fork (three copies of 1 MB) takes 4 us with
-// cold caches and 3 behind another call.
+// The compaction runs at 5.7 TB/s of the 6.5 that a plain copy reaches; a fork (three copies of 1 MB) takes 5 us with
+// cold caches and 3 behind another call.  A reorder reads its first pieces twice, and its pieces get shorter with the
+// pairs: permutations of 64, 256 and 512 states of 1 MB take 27, 151 and 419 us, where twice their bytes take 21, 83 and
+// 166, and one swap among 192 copies 116 us in place of 65.
 #include "gdn2_internal.h"
 #include "gdn2_slots.cuh"
 #include "tc_ptx.cuh"

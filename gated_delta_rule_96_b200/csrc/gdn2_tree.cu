@@ -95,9 +95,10 @@ __device__ __forceinline__ void couple(const float *sk, const unsigned char *anc
 
 // The kernel on CUDA cores, any type and size.  One block per (column range, head, sequence); the first
 // cols / 16 warps own 16 columns of the state each, every warp takes part in the rest.  For a few nodes a chain of
-// latencies (8 nodes of one user, H16: 7.4 us with cold caches, 5.8 a call behind another; the columns over 128 SMs),
-// for many the 2 n d_k d_v FMA of a head and their shared-memory loads (32 users with 32 nodes: 70 us, against 35 on
-// the tensor cores).
+// latencies (8 nodes of one user, H16: 8.1 us with cold caches, 5.8 a call behind another; the columns over 128 SMs),
+// for many the 2 n d_k d_v FMA of a head and their shared-memory loads (32 users with 32 nodes: 63 us, against 31 on
+// the tensor cores; 128 users of 32 nodes with 128-64 heads 130, of 64 nodes with 64-64 heads 253 and in fp32 547, where
+// the FMA alone would take 30, 30 and 121: a block's stages follow one another, and at 64 nodes it has an SM to itself).
 template <typename Tok, int K, int V>
 __global__ void __launch_bounds__(256, 2) tree_kernel(const Tok *__restrict__ q, const Tok *__restrict__ k,
                                                    const Tok *__restrict__ v, const float *__restrict__ alpha,
@@ -310,15 +311,16 @@ int launch_t(const void *q, const void *k, const void *v, const float *alpha, co
                         num_slots, slots, cu, parents, (Tok *)o, H, splits, total, max_nodes, status);
 }
 
-// Which kernel: the tensor-core one's period for an item hardly depends on its nodes (6.0 us an SM for one, 10.7 for
-// 64), this one's grows with them, is not two thirds of it for one, and few items have their columns over all SMs here;
-// H16, cold caches, us, this / that:
-//   1 user      8 nodes  7.4 / 10.7   24 nodes 11.0 / 11.7   40 nodes  14.2 / 14.4   64 nodes  19.6 / 16.4
-//   2 users    24 nodes 12.2 / 11.7   40 nodes 17.2 / 14.7
-//   4 users     9 nodes 10.0 / 11.0   16 nodes 11.5 / 11.4   32 nodes  17.5 / 13.1
-//   8 users     8 nodes 11.6 / 12.7   12 nodes 13.5 / 12.0   16 nodes  16.5 / 12.5
-//   32 users    4 nodes 21.5 / 26.7    8 nodes 27.5 / 25.7   16 nodes  41.0 / 28.8   32 nodes  69.7 / 34.6
-//   128 users   4 nodes 64.6 / 84.0    8 nodes 86.6 / 86.3   16 nodes 127.0 / 89.5   64 nodes 526.5 / 152.2
+// Which kernel: the tensor-core one's period for an item hardly depends on its nodes (5.2 us an SM for four, 10.3 for 64),
+// this one's grows with them, and few items have their columns over all SMs here.  H16, us, this / that, one call behind
+// another; [with cold caches, device time]:
+//   1 user     24 nodes  7.8 /  9.1 [10.3 / 13.1]   32 nodes  9.7 /  9.9                   40 nodes  14.1 / 12.0 [16.7 / 16.3]
+//   2 users    20 nodes  8.3 /  9.0                 24 nodes  8.7 /  9.1 [11.3 / 13.5]   32 nodes  10.8 / 10.0
+//   4 users    12 nodes  8.0 /  8.3                 16 nodes  8.8 /  8.5 [11.7 / 12.8]   20 nodes  10.1 /  9.1
+//   8 users     8 nodes  8.4 /  8.3 [10.9 / 12.1]   10 nodes  9.2 /  8.8                   16 nodes  11.6 /  8.7 [14.8 / 13.2]
+//   32 users    7 nodes 19.6 / 20.2                  8 nodes 20.6 / 20.1 [24.8 / 25.0]   10 nodes  23.8 / 20.6
+//   128 users   6 nodes 64.9 / 69.4                  7 nodes 68.7 / 69.8                    8 nodes  73.0 / 70.2 [77.3 / 74.1]
+//   with cold caches alone: 32 users of 32 nodes [62.9 / 31.2], 128 of 16 [116.5 / 76.5], of 64 [535.5 / 142.8]
 bool use_tc(int batch, int H, int max_nodes) {
     const long long items = (long long)batch * H;
     return max_nodes > (items > 148 ? 7 : items > 64 ? 9 : items > 32 ? 15 : items > 16 ? 20 : 40);

@@ -23,10 +23,12 @@
 //   scout warp              reads and checks the items, lists their paths, brings the tokens' lines into L2 ahead
 //                           of the groups
 //   lead warp               issues the products
-// 128 trees of 64 nodes, H16, take 145 us for 403 MB: 10.6 us an item, of which memory needs 4.5.  Half of the issue
-// slots are taken, by the splitting of the operands, the decays, the elimination and the sums; with the pairs on CUDA
-// cores in one group with the paths it took 191 us, with those in groups of their own 181.  Few items (32 trees of up to
-// 32 nodes: 32 us) wait for the chain of one.
+// 128 trees of 64 nodes, H16, take 137 us for 403 MB (device time, cold caches; 136 one call behind another): 9.9 us an
+// item, of which memory needs 4.5.  Half of the issue slots are taken, by the splitting of the operands, the decays, the
+// elimination and the sums; with the pairs on CUDA cores in one group with the paths it took 191 us, with those in groups
+// of their own 181, when this took 146.  960 threads leave 64 registers each, and the path and pair groups spill (44 bytes
+// of stores, 72 of loads a thread).  Few items (32 trees of up to 32 nodes: 29 us, 25 one call behind another) wait for
+// the chain of one.
 #include "gdn2_tree.cuh"
 #include "tc_ptx.cuh"
 
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) tree_tc_kernel(
                     const bool good = in_range<D>(G, lane);
                     if (!go) continue;
                     if (sub == 0) m.fine[node] = good;
-                    f32x2 own = 0ull;   // one accumulator: two made it spill (full batch 136 -> 140 us)
+                    f32x2 own = 0ull;   // with two accumulators the full batch took 140 us in place of 136
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int at = 8 * sub + 64 * j;
