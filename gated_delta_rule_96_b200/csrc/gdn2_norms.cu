@@ -89,7 +89,7 @@ __device__ __forceinline__ Sigmoid sigmoid_(float x) {
         // 1 / (1 + 2^(-x log2 e)) on the special-function unit: two instructions there and two beside them, where
         // expf and the divide take some twenty, which bounded the kernels at two thirds of the copy rate.  Each of
         // the two is good to about one unit of fp32 and the argument's rounding adds |x| / 2 more, where the output's
-        // rounding to bf16 is 2^15 units; the ends are exact.
+        // rounding to bf16 is up to 2^16 units; the ends are exact.
         float e, r;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * x));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));

@@ -237,7 +237,8 @@ GDN2_API int gdn2_add_norm_bwd(const void *h, const void *x, const float *scale,
  * tensor cores, which take no fp32: there the state, the decayed b k and q and k over its decays enter
  * their products as sums of two bf16 (17 bits of 24; the accumulation is fp32).  That puts o some 2e-6
  * of its norm off before its rounding (4e-6 where decays are slow), whose own 1.7e-3 it leaves as it
- * is: one bf16 value in some hundreds is rounded the other way.  An infinity in a state or a token gives NaN there where fp32 may keep it.
+ * is: one bf16 value in some hundreds is rounded the other way.  An infinity in a state or a token
+ * gives NaN there where fp32 may keep it.
  * Calls with fp32 tokens, or other d_k and d_v, are fp32 throughout.
  */
 #define GDN2_TREE_MAX_NODES 64

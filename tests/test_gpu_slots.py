@@ -759,14 +759,14 @@ def test_calls_behind_one_another_see_what_the_last_one_wrote():
 
 def test_every_input_may_be_what_the_kernel_before_wrote():
     """Tokens, weights, slots, counts, parents and indices, all of them written by the call right before (a copy of a large
-    slot that ends with them), with nothing between: each call reads this round's, not the round's before."""
+    slot that ends with them), with nothing between: each call reads this turn's, not the turn's before."""
     torch, g = cuda_or_skip()
     floats = 1 << 24
-    pool = torch.zeros(3, floats, device="cuda")                   # two rounds' inputs, and where the calls read them
+    pool = torch.zeros(3, floats, device="cuda")                   # two turns' inputs, and where the calls read them
     at = [floats]
 
     def place(*pair):
-        """Two rounds' values of one input, at the slots' end; the input itself."""
+        """Two turns' values of one input, at the slots' end; the input itself."""
         first, size = pair[0], pair[0].numel()
         at[0] -= -(-size * first.element_size() // 16) * 4
         views = [pool[i, at[0]:].view(first.dtype)[:size].view(first.shape) for i in range(3)]
@@ -778,9 +778,9 @@ def test_every_input_may_be_what_the_kernel_before_wrote():
     H, n = 3, 44
     args = {}
     for few in (12, n):                                            # trees of both kernels
-        rounds = [tokens(torch, 80 + few + i, few, H, 128, 128, "bf16") for i in range(2)]
+        turns = [tokens(torch, 80 + few + i, few, H, 128, 128, "bf16") for i in range(2)]
         trees = [ints(*random_tree(np.random.default_rng(i), few - 4, 6), -1, 0, 0, 1) for i in range(2)]
-        args[few] = dict(x=[place(a, b) for a, b in zip(*rounds)], parents=place(*trees),
+        args[few] = dict(x=[place(a, b) for a, b in zip(*turns)], parents=place(*trees),
                          cu=place(ints(0, few - 4, few), ints(0, few - 4, few - 1)), slots=place(ints(0, 1), ints(1, 0)),
                          index=place(*(torch.randperm(few, generator=torch.Generator().manual_seed(i)).int() for i in range(2))))
     half = lambda seed, *shape: torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).bfloat16()  # noqa: E731
@@ -819,7 +819,7 @@ def test_every_input_may_be_what_the_kernel_before_wrote():
             g.gdn2_state_copy(pool, pool, target, source[turn % 2], workspace=ws)
             got = flat(ready())
             for a, b in zip(got, want[turn % 2]):
-                if a.shape[0] in (12, n):                          # the second round has one token fewer
+                if a.shape[0] in (12, n):                          # the second turn has one token fewer
                     a, b = a[:a.shape[0] - turn % 2], b[:b.shape[0] - turn % 2]
                 assert torch.equal(a, b), (which, turn)
     assert g.gdn2_workspace_status(ws) == 0
