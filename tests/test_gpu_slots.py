@@ -859,6 +859,55 @@ def test_a_launch_that_fails_leaves_no_error_behind():
     torch.cuda.synchronize()
 
 
+def test_calls_of_every_kind_at_once():
+    """Host threads with a stream each: trees on both kernels, runs, reorders, norms and the tensor-core prefill beside one
+    another, all without a workspace of their own (the calls over slots share the device's status), give what each gives
+    alone."""
+    import threading
+    torch, g = cuda_or_skip()
+    H, n, B = 16, 44, 10
+    rng = np.random.default_rng(1)
+    x, few = tokens(torch, 100, n * B, H, 128, 128, "bf16"), tokens(torch, 101, 6 * B, H, 64, 128, "f32")
+    pool, small = make_pool(torch, 102, 2 * B, H, 128, 128), make_pool(torch, 103, 2 * B, H, 64, 128)
+    slots, other, cu = i32(torch, range(B)), i32(torch, range(B, 2 * B)), i32(torch, range(0, n * B + 1, n))
+    cu6, par = i32(torch, range(0, 6 * B + 1, 6)), i32(torch, sum((random_tree(rng, n, 7) for _ in range(B)), []))
+    par6 = i32(torch, sum((random_tree(rng, 6, 3) for _ in range(B)), []))
+    perm, weight = rng.permutation(2 * B), torch.rand(128, device="cuda")
+    to, frm = i32(torch, perm), i32(torch, np.roll(perm, 1))
+    rows, dense = x[2].reshape(-1, 128), [a.view(B, n, H, 128) for a in x]
+
+    def runs():
+        p = pool.clone()
+        return g.recurrent_fwd(*x, p, slots, other, cu), p
+
+    def reorder():
+        p = pool.clone()
+        g.gdn2_state_copy(p, p, to, frm)
+        return (p,)
+    kinds = [lambda: (g.tree_fwd(*x, pool, slots, cu, par, n),), lambda: (g.tree_fwd(*few, small, slots, cu6, par6, 6),), runs, reorder,
+             lambda: g.gated_norm_bwd(rows, x[5].reshape(-1, 128), weight, rows), lambda: g.chunk_fwd(*dense)]
+    wants = [[a.clone() for a in kind()] for kind in kinds]
+    torch.cuda.synchronize()
+    g.gdn2_shared_status()
+    wrong = []
+
+    def work(kind, want):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(30):
+                got = kind()
+                stream.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                    wrong.append(kinds.index(kind))
+    threads = [threading.Thread(target=work, args=pair) for pair in zip(kinds, wants)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong and g.gdn2_shared_status() == 0
+
+
 def test_two_graphs_share_a_workspace():
     """The workspace of the calls over slots holds status words only: two captured graphs replayed at the same
     time on two streams do not disturb one another, and what either reports stays reported."""
